@@ -25,8 +25,9 @@
  *
  * plus gptq_quantize_rtn, the round-to-nearest baseline on the same grid
  * (knowledge note, "Common Confusions"), gptq_dequant_matvec (inference with
- * the packed weights) and gptq2d_round (GPTQ-2D, the two-sided task of the
- * GPTQ-2D abstract on the "Daily Papers" page).
+ * the packed weights), gptq2d_round (GPTQ-2D, the two-sided task of the
+ * GPTQ-2D abstract on the "Daily Papers" page) and the 4-bit floating-point
+ * operators: gptq_fp4_quantize, gptq_fp4_matmul, gptq_fp4_grouped_matmul.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -404,6 +405,109 @@ gptq_status gptq2d_round(const void* W, gptq_dtype wdt, int64_t m, int64_t n,
                          const float* UL, const float* UR, float scale, int32_t clamp,
                          int32_t qmin, int32_t qmax, int32_t* codes, float* E,
                          void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* 7. 4-bit floating point: quantisation and products                        */
+/* ------------------------------------------------------------------------ */
+
+/* Microscaled 4-bit floating point: E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives) with one scale a block of consecutive columns of a row.
+ *   GPTQ_MXFP4  blocks of 32, scale s = 2^e (byte e + 127, 255 = NaN), t = 1
+ *   GPTQ_NVFP4  blocks of 16, scale s in E4M3 (byte 127 = NaN), and one fp32
+ *               scale t a group of rows
+ * An element stands for code * s * t.
+ *
+ * A quantised matrix [rows, n] is three arrays:
+ *   packed  uint8 [rows, gptq_fp4_row_bytes(n)]: two codes a byte, the even
+ *           column in the low half; zero codes up to 32 columns
+ *   scales  uint8 [bands, ceil(n / (4 B)), 512] (B: the block): a tile holds
+ *           128 rows x 4 blocks, the byte of the band's row r and block b at
+ *           16 (r % 32) + 4 (r / 32) + b % 4.  Rows come in groups (experts;
+ *           one group for a plain matrix) and each group's rows start a new
+ *           band of 128, so group g has ceil(rows_g / 128) bands, one group
+ *           after another.  Bytes of rows and blocks that do not exist are
+ *           zero in bands that hold a row
+ *   tensor_scale  fp32 [groups] (GPTQ_NVFP4 only)
+ * Groups are given by `offsets` (int32 [groups + 1] on the device, rising,
+ * group g = rows offsets[g] .. offsets[g + 1] - 1, empty groups allowed, at
+ * most 512 groups; rows outside [offsets[0], offsets[groups]) belong to none),
+ * or, with offsets NULL, are `groups` runs of rows / groups rows. */
+typedef enum { GPTQ_MXFP4 = 0, GPTQ_NVFP4 = 1 } gptq_fp4_format;
+
+/* Bytes of a packed row: 16 * ceil(n / 32); 0 for sizes that are refused. */
+int64_t gptq_fp4_row_bytes(int32_t n);
+
+/* Bytes that the scales of `rows` rows in `groups` groups take: exact for
+ * groups of one size (ragged 0), enough for any offsets with ragged 1.  0 for
+ * sizes that are refused. */
+size_t gptq_fp4_scale_bytes(int64_t rows, int32_t n, gptq_fp4_format format, int32_t groups, int32_t ragged);
+
+/* Bytes of workspace gptq_fp4_quantize needs when it makes the tensor scales
+ * (0 for GPTQ_MXFP4, and where it is given them it needs none). */
+size_t gptq_fp4_quantize_workspace_size(int64_t rows, int32_t n, gptq_fp4_format format, int32_t groups,
+                                        int32_t ragged);
+
+/* Quantises X (weights once, activations before a product).
+ *
+ *   GPTQ_MXFP4  s = 2^(floor(log2 amax) - 2) in [2^-127, 2^127] (2^-127 for a
+ *               block of zeros), amax the block's largest magnitude
+ *   GPTQ_NVFP4  t = max(RN(amax of the group / 2688), 2^-126) in fp32,
+ *               s = the E4M3 value nearest to amax / (6 t), at most 448
+ *   code = the E2M1 value nearest to x / (s t), at most 6 (0 where s is 0)
+ * Every "nearest" is decided on the exact quotient, ties to the even code.  A
+ * block with an infinity or NaN gets the scale NaN and zero codes, and its
+ * values count in no group's maximum.
+ *
+ *   X            [x_rows, ldx] (xdt = GPTQ_F32 or GPTQ_BF16), first n columns
+ *   row_index    int32 [rows] or NULL: row i is X's row row_index[i] (a token's
+ *                row may be taken by several experts); NULL: row i, x_rows >= rows.
+ *                An index outside [0, x_rows) gives a row of zeros and
+ *                GPTQ_ERR_INVALID_ARG in the device status word
+ *   offsets, groups  as above.  Offsets that fall, are negative or pass `rows`
+ *                leave every output untouched and GPTQ_ERR_INVALID_ARG in the
+ *                device status word
+ *   given        0: the tensor scales are made and written; 1: they are read
+ *                (positive and finite).  GPTQ_MXFP4: tensor_scale NULL, given 0
+ *   packed, scales   as above, 16-byte aligned; rows of no group are left as
+ *                they were
+ *   deq          fp32 [rows, n] or NULL: RN((code * s) * t)
+ *   n            1 <= n <= 65535; rows, x_rows < 2^31 - 256
+ *   ws           gptq_fp4_quantize_workspace_size bytes (may be NULL when that
+ *                is 0 or given is 1)
+ * Deterministic.  Errors: GPTQ_ERR_INVALID_ARG before any launch,
+ * GPTQ_ERR_UNSUPPORTED for more tiles than a grid has, GPTQ_ERR_CUDA. */
+gptq_status gptq_fp4_quantize(const void* X, gptq_dtype xdt, int64_t x_rows, int32_t n, int64_t ldx,
+                              const int32_t* row_index, int64_t rows, const int32_t* offsets, int32_t groups,
+                              gptq_fp4_format format, int32_t given, float* tensor_scale, uint8_t* packed,
+                              uint8_t* scales, float* deq, void* ws, size_t ws_bytes, void* stream);
+
+/* y[i, r] = tw tx sum_c W[r, c] X[i, c] with both matrices quantised (one
+ * group each): the block scales are applied by the tensor cores, sums are
+ * fp32 in tensor memory, tensor scales are multiplied in last.
+ *   w_packed, w_scales, w_tensor  W [rows, n]: packed, scales, tensor scale (device fp32 [1];
+ *                NULL with GPTQ_MXFP4)
+ *   x_packed, x_scales, x_tensor   X [tokens, n], likewise, 1 token to 2^31 - 257
+ *   y            [tokens, ldy] (ydt = GPTQ_F32 or GPTQ_BF16), first `rows`
+ *                columns written, ldy >= rows
+ * Packed and scales 16-byte aligned.  Deterministic; asynchronous on `stream`.
+ * Errors: GPTQ_ERR_INVALID_ARG before any launch; GPTQ_ERR_CUDA. */
+gptq_status gptq_fp4_matmul(gptq_fp4_format format, const uint8_t* w_packed, const uint8_t* w_scales, const float* w_tensor,
+                            int64_t rows, int32_t n, const uint8_t* x_packed, const uint8_t* x_scales, const float* x_tensor,
+                            int64_t tokens, void* y, gptq_dtype ydt, int64_t ldy, void* stream);
+
+/* The same product, each group of X's rows with its own W:
+ * y[i, r] = tw[g] tx[g] sum_c W[g, r, c] X[i, c] for row i of group g.
+ *   w_packed, w_scales, w_tensor  W [groups, rows, n]: quantised as groups * rows rows in
+ *                `groups` groups; w_tensor fp32 [groups]
+ *   x_packed, x_scales, x_tensor   X [tokens, n], quantised with the same offsets; x_tensor fp32 [groups]
+ *   offsets      int32 [groups + 1], groups <= 512; as above (offsets that are
+ *                not valid leave y untouched and GPTQ_ERR_INVALID_ARG in the
+ *                device status word)
+ * Rows of y that belong to no group are left as they were. */
+gptq_status gptq_fp4_grouped_matmul(gptq_fp4_format format, const uint8_t* w_packed, const uint8_t* w_scales, const float* w_tensor,
+                                    int32_t groups, int64_t rows, int32_t n, const uint8_t* x_packed, const uint8_t* x_scales,
+                                    const float* x_tensor, int64_t tokens, const int32_t* offsets, void* y, gptq_dtype ydt,
+                                    int64_t ldy, void* stream);
 
 #ifdef __cplusplus
 }

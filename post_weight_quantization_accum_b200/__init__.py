@@ -4,13 +4,18 @@ The functions below carry the names of the C entry points in include/gptq.h
 and only marshal arguments: torch supplies device memory and the current CUDA
 stream, the library's kernels do all of the work.  ``quantize_layer`` chains the
 four calls for one linear layer (the usual entry point for a user);
-``gptq2d_round`` is the two-sided rounding of the GPTQ-2D abstract.
+``gptq2d_round`` is the two-sided rounding of the GPTQ-2D abstract.  The 4-bit
+floating-point operators (``gptq_fp4_quantize``, ``gptq_fp4_matmul``,
+``gptq_fp4_grouped_matmul``, and ``fp4_linear``, which chains them) are in
+``fp4.py``.
 """
 import ctypes
 
 import torch
 
 from ._lib import GPTQ_BF16, GPTQ_F32, LIB, GptqError, TraceEntry, check  # noqa: F401
+from .fp4 import (FP4_BLOCK, FP4_FORMATS, fp4_check_matrix, fp4_check_quantize_args, fp4_linear,  # noqa: F401
+                  gptq_fp4_grouped_matmul, gptq_fp4_matmul, gptq_fp4_quantize)
 
 __all__ = [
     "GptqError",
@@ -23,6 +28,12 @@ __all__ = [
     "gptq2d_round",
     "gptq2d_check_args",
     "gptq2d_factor",
+    "gptq_fp4_quantize",
+    "gptq_fp4_matmul",
+    "gptq_fp4_grouped_matmul",
+    "fp4_linear",
+    "fp4_check_quantize_args",
+    "fp4_check_matrix",
     "gptq_get_device_status",
     "gptq_set_wait_limit_ns",
     "gptq_set_column_loop",

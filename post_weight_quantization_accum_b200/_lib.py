@@ -22,6 +22,7 @@ STATUS = {
     6: "GPTQ_ERR_TIMEOUT",
 }
 GPTQ_F32, GPTQ_BF16 = 0, 1
+GPTQ_MXFP4, GPTQ_NVFP4 = 0, 1
 
 # name -> (restype, argtypes); mirrors include/gptq.h
 _P = ctypes.c_void_p
@@ -58,6 +59,19 @@ _SIGS = {
     "gptq2d_round": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, _P, _P, ctypes.c_float,
                                     ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, ctypes.c_size_t,
                                     _P]),
+    "gptq_fp4_row_bytes": (ctypes.c_int64, [ctypes.c_int32]),
+    "gptq_fp4_scale_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_int32,
+                                               ctypes.c_int32]),
+    "gptq_fp4_quantize_workspace_size": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int,
+                                                           ctypes.c_int32, ctypes.c_int32]),
+    "gptq_fp4_quantize": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64, _P,
+                                         ctypes.c_int64, _P, ctypes.c_int32, ctypes.c_int, ctypes.c_int32, _P, _P, _P,
+                                         _P, _P, ctypes.c_size_t, _P]),
+    "gptq_fp4_matmul": (ctypes.c_int, [ctypes.c_int, _P, _P, _P, ctypes.c_int64, ctypes.c_int32, _P, _P, _P,
+                                       ctypes.c_int64, _P, ctypes.c_int, ctypes.c_int64, _P]),
+    "gptq_fp4_grouped_matmul": (ctypes.c_int, [ctypes.c_int, _P, _P, _P, ctypes.c_int32, ctypes.c_int64,
+                                               ctypes.c_int32, _P, _P, _P, ctypes.c_int64, _P, _P, ctypes.c_int,
+                                               ctypes.c_int64, _P]),
 }
 
 

@@ -1,6 +1,6 @@
 // C ABI of the library: argument validation, per-device state and dispatch to
-// the kernels in hessian.cu, hinv.cu, quantize.cu, pack.cu, matvec.cu and round2d.cu.  Nothing here
-// allocates device memory; every scratch byte comes from the caller.
+// the kernels in hessian.cu, hinv.cu, quantize.cu, pack.cu, matvec.cu, round2d.cu, fp4_quantize.cu and
+// fp4_matmul.cu.  Nothing here allocates device memory; every scratch byte comes from the caller.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "fp4.cuh"
 
 namespace gptq {
 
@@ -37,6 +38,13 @@ gptq_status dequant_matvec(const uint32_t* packed, const float* scales, const ui
 size_t round2d_workspace_size(int64_t m, int64_t n);
 gptq_status round2d(const void* W, int w_bf16, int64_t m, int64_t n, const float* UL, const float* UR, float scale,
                     int clamp, int qmin, int qmax, int32_t* codes, float* E, void* ws, cudaStream_t st);
+size_t fp4_quantize_workspace_size(int64_t rows, int n, bool nv, int groups, bool ragged);
+gptq_status fp4_quantize(const void* X, int x_bf16, int64_t x_rows, int n, int64_t ldx, const int32_t* row_index,
+                         int64_t rows, const int32_t* offsets, int groups, bool nv, int given, float* tensor_scale,
+                         uint8_t* packed, uint8_t* scales, float* deq, void* ws, cudaStream_t st);
+gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const float* wt, int groups, int64_t rows,
+                       int n, const uint8_t* xq, const uint8_t* xscales, const float* xt, int64_t tokens,
+                       const int32_t* offsets, void* y, int y_bf16, int64_t ldy, cudaStream_t st);
 
 // Status words of each device: [0] failures of asynchronous kernels (bounded
 // waits), [1] the factorization status of gptq_prepare_hinv.
@@ -415,6 +423,92 @@ gptq_status gptq2d_round(const void* W, gptq_dtype wdt, int64_t m, int64_t n, co
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < need) return GPTQ_ERR_INVALID_ARG;
   return round2d(W, wdt == GPTQ_BF16 ? 1 : 0, m, n, UL, UR, scale, clamp, qmin, qmax, codes, E, ws,
                  as_stream(stream));
+}
+
+}  // extern "C"
+
+namespace {
+constexpr int64_t kMaxFp4Rows = (int64_t(1) << 31) - 257;  // rows are TMA coordinates, a tile may reach past them
+bool valid_format(gptq_fp4_format f) { return f == GPTQ_MXFP4 || f == GPTQ_NVFP4; }
+bool valid_groups(int64_t rows, int32_t groups, bool ragged) {
+  return groups >= 1 && (ragged ? groups <= kFp4MaxGroups : rows % groups == 0);
+}
+
+gptq_status check_product(gptq_fp4_format format, const uint8_t* w_packed, const uint8_t* ws, const float* w_tensor, int32_t groups,
+                          int64_t rows, int32_t n, const uint8_t* x_packed, const uint8_t* x_scales, const float* x_tensor,
+                          int64_t tokens, const void* y, gptq_dtype ydt, int64_t ldy) {
+  if (!valid_format(format) || rows < 0 || n < 1 || n > kMaxN || tokens < 0 || tokens > kMaxFp4Rows || groups < 1 ||
+      groups > kFp4MaxGroups || rows > kMaxFp4Rows / groups || (ydt != GPTQ_F32 && ydt != GPTQ_BF16) || ldy < rows)
+    return GPTQ_ERR_INVALID_ARG;
+  if (rows == 0 || tokens == 0) return GPTQ_OK;
+  if (w_packed == nullptr || ws == nullptr || x_packed == nullptr || x_scales == nullptr || y == nullptr || !aligned(w_packed, 16) ||
+      !aligned(ws, 16) || !aligned(x_packed, 16) || !aligned(x_scales, 16) || !aligned(y, ydt == GPTQ_BF16 ? 2 : 4))
+    return GPTQ_ERR_INVALID_ARG;
+  const bool nv = format == GPTQ_NVFP4;  // mxfp4 has no tensor scales
+  if (nv != (w_tensor != nullptr) || nv != (x_tensor != nullptr) || !aligned(w_tensor, 4) || !aligned(x_tensor, 4)) return GPTQ_ERR_INVALID_ARG;
+  return GPTQ_OK;
+}
+}  // namespace
+
+extern "C" {
+
+int64_t gptq_fp4_row_bytes(int32_t n) { return n < 1 || n > kMaxN ? 0 : fp4_pitch(n); }
+
+size_t gptq_fp4_scale_bytes(int64_t rows, int32_t n, gptq_fp4_format format, int32_t groups, int32_t ragged) {
+  if (rows < 0 || rows > kMaxFp4Rows || n < 1 || n > kMaxN || !valid_format(format) ||
+      !valid_groups(rows, groups, ragged != 0))
+    return 0;
+  return static_cast<size_t>(fp4_bands(rows, groups, ragged != 0)) * fp4_quads(n, format == GPTQ_NVFP4) * kFp4TileBytes;
+}
+
+size_t gptq_fp4_quantize_workspace_size(int64_t rows, int32_t n, gptq_fp4_format format, int32_t groups,
+                                        int32_t ragged) {
+  if (rows < 0 || rows > kMaxFp4Rows || n < 1 || n > kMaxN || !valid_format(format) ||
+      !valid_groups(rows, groups, ragged != 0))
+    return 0;
+  return fp4_quantize_workspace_size(rows, n, format == GPTQ_NVFP4, groups, ragged != 0);
+}
+
+gptq_status gptq_fp4_quantize(const void* X, gptq_dtype xdt, int64_t x_rows, int32_t n, int64_t ldx,
+                              const int32_t* row_index, int64_t rows, const int32_t* offsets, int32_t groups,
+                              gptq_fp4_format format, int32_t given, float* tensor_scale, uint8_t* packed,
+                              uint8_t* scales, float* deq, void* ws, size_t ws_bytes, void* stream) {
+  if ((xdt != GPTQ_F32 && xdt != GPTQ_BF16) || !valid_format(format) || rows < 0 || rows > kMaxFp4Rows || x_rows < 0 ||
+      x_rows > kMaxFp4Rows || n < 1 || n > kMaxN || ldx < n || (given != 0 && given != 1) ||
+      !valid_groups(rows, groups, offsets != nullptr) || (row_index == nullptr && x_rows < rows))
+    return GPTQ_ERR_INVALID_ARG;
+  const bool nv = format == GPTQ_NVFP4;
+  if (nv != (tensor_scale != nullptr) || (!nv && given) || !aligned(tensor_scale, 4)) return GPTQ_ERR_INVALID_ARG;
+  if (rows > 0 && (X == nullptr || packed == nullptr || scales == nullptr)) return GPTQ_ERR_INVALID_ARG;
+  if (rows == 0 && !(nv && !given)) return GPTQ_OK;
+  if (!aligned(X, xdt == GPTQ_BF16 ? 2 : 4) || !aligned(packed, 16) || !aligned(scales, 16) || !aligned(deq, 4) ||
+      !aligned(row_index, 4) || !aligned(offsets, 4))
+    return GPTQ_ERR_INVALID_ARG;
+  if ((fp4_bands(rows, groups, offsets != nullptr) + 1) * ((n + 255) / 256) > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  const size_t need = given ? 0 : fp4_quantize_workspace_size(rows, n, nv, groups, offsets != nullptr);
+  if (need > 0 && (ws == nullptr || !aligned(ws, 256) || ws_bytes < need)) return GPTQ_ERR_INVALID_ARG;
+  return fp4_quantize(X, xdt == GPTQ_BF16 ? 1 : 0, x_rows, n, ldx, row_index, rows, offsets, groups, nv, given,
+                      tensor_scale, packed, scales, deq, ws, as_stream(stream));
+}
+
+gptq_status gptq_fp4_matmul(gptq_fp4_format format, const uint8_t* w_packed, const uint8_t* w_scales, const float* w_tensor,
+                            int64_t rows, int32_t n, const uint8_t* x_packed, const uint8_t* x_scales, const float* x_tensor,
+                            int64_t tokens, void* y, gptq_dtype ydt, int64_t ldy, void* stream) {
+  const gptq_status s = check_product(format, w_packed, w_scales, w_tensor, 1, rows, n, x_packed, x_scales, x_tensor, tokens, y, ydt, ldy);
+  if (s != GPTQ_OK || rows == 0 || tokens == 0) return s;
+  return fp4_matmul(format == GPTQ_NVFP4, w_packed, w_scales, w_tensor, 1, rows, n, x_packed, x_scales, x_tensor, tokens, nullptr, y,
+                    ydt == GPTQ_BF16 ? 1 : 0, ldy, as_stream(stream));
+}
+
+gptq_status gptq_fp4_grouped_matmul(gptq_fp4_format format, const uint8_t* w_packed, const uint8_t* w_scales, const float* w_tensor,
+                                    int32_t groups, int64_t rows, int32_t n, const uint8_t* x_packed, const uint8_t* x_scales,
+                                    const float* x_tensor, int64_t tokens, const int32_t* offsets, void* y, gptq_dtype ydt,
+                                    int64_t ldy, void* stream) {
+  const gptq_status s = check_product(format, w_packed, w_scales, w_tensor, groups, rows, n, x_packed, x_scales, x_tensor, tokens, y, ydt, ldy);
+  if (s != GPTQ_OK || rows == 0 || tokens == 0) return s;
+  if (offsets == nullptr || !aligned(offsets, 4)) return GPTQ_ERR_INVALID_ARG;
+  return fp4_matmul(format == GPTQ_NVFP4, w_packed, w_scales, w_tensor, groups, rows, n, x_packed, x_scales, x_tensor, tokens, offsets, y,
+                    ydt == GPTQ_BF16 ? 1 : 0, ldy, as_stream(stream));
 }
 
 }  // extern "C"
