@@ -445,6 +445,9 @@ gptq_status check_product(gptq_fp4_format format, const uint8_t* w_packed, const
       !aligned(ws, 16) || !aligned(x_packed, 16) || !aligned(x_scales, 16) || !aligned(y, ydt == GPTQ_BF16 ? 2 : 4))
     return GPTQ_ERR_INVALID_ARG;
   const bool nv = format == GPTQ_NVFP4;  // mxfp4 has no tensor scales
+  const int64_t quads = fp4_quads(n, nv);  // scale tiles are TMA rows
+  if (fp4_bands(groups * rows, groups, false) * quads > INT32_MAX - 8 || fp4_bands(tokens, groups, true) * quads > INT32_MAX - 8)
+    return GPTQ_ERR_UNSUPPORTED;
   if (nv != (w_tensor != nullptr) || nv != (x_tensor != nullptr) || !aligned(w_tensor, 4) || !aligned(x_tensor, 4)) return GPTQ_ERR_INVALID_ARG;
   return GPTQ_OK;
 }

@@ -57,38 +57,48 @@ struct MatmulArgs {
   uint64_t wait_ns;
 };
 
-// kind::mxf4nvf4 with a scale every 16 columns (E4M3), kind::mxf4 every 32 (2^e).
-template <bool NV>
+// D (+)= A B^T with block scales: kind::mxf4nvf4 has a scale every 16 columns
+// (E4M3), kind::mxf4 every 32 (2^e).  CTAS = 2: the pair form (the even CTA
+// issues; each CTA holds half of A's rows and half of B's, and the scales of
+// its own A rows and of all B rows).
+#define GPTQ_FP4_MMA(GROUP, KIND)                                                                              \
+  asm volatile(                                                                                                \
+      "{\n\t.reg .pred p;\n\t"                                                                                \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                                              \
+      "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),        \
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                                  \
+      : "memory")
+template <bool NV, int CTAS>
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                         uint32_t sfb, uint32_t accumulate) {
-  if (NV)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+  if (NV && CTAS == 1)
+    GPTQ_FP4_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
+  else if (NV)
+    GPTQ_FP4_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+  else if (CTAS == 1)
+    GPTQ_FP4_MMA("1", "mxf4.block_scale.scale_vec::2X");
   else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    GPTQ_FP4_MMA("2", "mxf4.block_scale.scale_vec::2X");
 }
+#undef GPTQ_FP4_MMA
 
 // Instruction descriptor of the block-scaled kinds: E2M1 operands along K,
-// scale type (0 E4M3, 1 2^e), M = 128, N tokens; `pair` picks the byte pair of
-// the 32-bit scale cell (mxfp4 uses two bytes an MMA).
-__device__ __forceinline__ uint32_t fp4_idesc(bool nv, uint32_t n, uint32_t pair) {
-  return (pair * 2) << 4 | 1u << 7 | 1u << 10 | (n >> 3) << 17 | (nv ? 0u : 1u) << 23 | 1u << 27 | (pair * 2) << 29;
+// scale type (0 E4M3, 1 2^e), M = 128 a CTA, N tokens; `pair` picks the byte
+// pair of the 32-bit scale cell (mxfp4 uses two bytes an MMA).
+__device__ __forceinline__ uint32_t fp4_idesc(bool nv, uint32_t ctas, uint32_t n, uint32_t pair) {
+  return (pair * 2) << 4 | 1u << 7 | 1u << 10 | (n >> 3) << 17 | (nv ? 0u : 1u) << 23 | ctas << 27 | (pair * 2) << 29;
 }
 
 // A scale tile (512 bytes of shared memory, 32 rows of 16 bytes) to four
-// tensor-memory columns, the same for each quarter of the lanes.
+// tensor-memory columns, the same for each quarter of the lanes (CTAS = 2: in
+// both CTAs, each from its own shared memory).
+template <int CTAS>
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem) {
   const uint64_t desc = static_cast<uint64_t>((smem >> 4) & 0x3FFFu) | 8ull << 32 | 1ull << 46;  // 8 rows apart: 128 bytes
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  if (CTAS == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -259,14 +269,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t tsa = tmem + kSfCol + stage * kSfStride, tsb = tsa + 16;
           const int q = min(kStageQuads, quads - kb * kStageQuads);
           for (int i = 0; i < q; ++i) {
-            copy_scales(tsa + 4 * i, ssa + i * kFp4TileBytes);
-            for (int h = 0; h < halves; ++h) copy_scales(tsb + 8 * i + 4 * h, ssb + h * kSfBytes + i * kFp4TileBytes);
+            copy_scales<1>(tsa + 4 * i, ssa + i * kFp4TileBytes);
+            for (int h = 0; h < halves; ++h) copy_scales<1>(tsb + 8 * i + 4 * h, ssb + h * kSfBytes + i * kFp4TileBytes);
           }
           const int m = min(kStageK / 64, mmas - kb * (kStageK / 64));
           for (int i = 0; i < m; ++i) {
             const int qi = i / kQuadMmas;
-            mma_fp4<NV>(tmem, smem_desc_sw128(sa + 32 * i, 16, 1024), smem_desc_sw128(sb + 32 * i, 16, 1024),
-                        fp4_idesc(NV, x.cols, i % kQuadMmas), tsa + 4 * qi, tsb + 8 * qi, kb > 0 || i > 0);
+            mma_fp4<NV, 1>(tmem, smem_desc_sw128(sa + 32 * i, 16, 1024), smem_desc_sw128(sb + 32 * i, 16, 1024),
+                        fp4_idesc(NV, 1, x.cols, i % kQuadMmas), tsa + 4 * qi, tsb + 8 * qi, kb > 0 || i > 0);
           }
           mma_commit(empty + stage);
           if (++stage == kStages) {
@@ -324,6 +334,346 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ---------------------------------------------------------------------------
+// The kernel for many tokens: CTA pairs, 256 weight rows x up to 256 tokens
+// ---------------------------------------------------------------------------
+
+constexpr int kPairRows = 256;
+constexpr int kPairStages = 5;
+constexpr int kPairBBytes = kBBytes / 2;  // this CTA's half of the tokens
+constexpr int kPairStageBytes = kABytes + kPairBBytes + 3 * kSfBytes;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
+constexpr int kStageOutBytes = 32 * 64;  // a warp's 32 tokens x 32 features in bf16
+constexpr size_t kPairSmemBytes =
+    1024 + size_t(kPairStages) * kPairStageBytes + kPairEpiWarps * kStageOutBytes + 256 + kTableBytes;
+// Tensor memory: two accumulators that overlap in columns [96, 256), and three
+// sets of scales.  The epilogue empties the overlap first.
+constexpr uint32_t kAccShift = 96;
+constexpr uint32_t kPairSfCol = kAccShift + kTokens, kPairSfStride = 48, kPairSfSets = 3;
+static_assert(kPairSfCol + kPairSfSets * kPairSfStride <= kTmemCols, "tensor memory");
+
+// 32 features x 32 tokens (v[j]: token j of this lane's feature) to y: through
+// shared memory as rows of 64 bytes (bf16), or straight (fp32: a row of 32
+// lanes is a line).  Only `tokens` rows and `features` lanes exist.
+__device__ __forceinline__ void store_block(const uint32_t (&v)[32], float tw, float tx, __nv_bfloat16* out, int64_t ldy,
+                                            int tokens, int64_t features, bool vec, uint8_t* stg) {
+  const int lane = threadIdx.x & 31;
+  if (vec && features >= 32) {
+    uint16_t* s = reinterpret_cast<uint16_t*>(stg) + lane;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[j]) * tw * tx, __uint_as_float(v[j + 1]) * tw * tx);
+      s[32 * j] = __bfloat16_as_ushort(p.x);
+      s[32 * j + 32] = __bfloat16_as_ushort(p.y);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = 8 * i + lane / 4;
+      if (tok < tokens)
+        *reinterpret_cast<uint4*>(out + tok * ldy + 8 * (lane % 4)) = *reinterpret_cast<const uint4*>(stg + 512 * i + 16 * lane);
+    }
+    __syncwarp();
+  } else if (lane < features) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < tokens) out[j * ldy + lane] = __float2bfloat16_rn(__uint_as_float(v[j]) * tw * tx);
+  }
+}
+__device__ __forceinline__ void store_block(const uint32_t (&v)[32], float tw, float tx, float* out, int64_t ldy, int tokens,
+                                            int64_t features, bool, uint8_t*) {
+  const int lane = threadIdx.x & 31;
+  if (lane < features) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < tokens) out[j * ldy + lane] = __uint_as_float(v[j]) * tw * tx;
+  }
+}
+
+// Where a role is in the sequence of (tile, K stage) that the CTA works off.
+struct Walk {
+  Tile x;
+  int64_t item;
+  int kb;
+  uint32_t stage, phase;  // of the operand ring
+};
+
+template <bool NV, typename OUT>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    fp4_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                    const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap, MatmulArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* staging = smem + size_t(kPairStages) * kPairStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kPairEpiWarps * kStageOutBytes);
+  uint64_t* empty = full + kPairStages;
+  uint64_t* acc_full = empty + kPairStages;  // one: a tile's products are complete
+  uint64_t* acc_free = acc_full + 1;         // the overlap of a tile's accumulator has been read
+  uint64_t* drain = acc_free + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* table = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);
+  const GroupTable t{table, table + kFp4MaxGroups + 1, table + 2 * (kFp4MaxGroups + 1)};
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  constexpr int kBlk = NV ? 16 : 32;
+  constexpr int kStageQuads = kStageK / (4 * kBlk);
+  constexpr int kQuadMmas = kBlk / 16;
+  constexpr uint32_t kStageSf = kStageQuads * kFp4TileBytes;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(full + s, 1);   // the even CTA's expect-tx arrival (and both CTAs' bytes)
+      mbar_init(empty + s, 1);  // a commit each use
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_free, 2 * kPairEpiWarps);  // the epilogue warps of both CTAs
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&wmap);
+    prefetch_tensormap(&xmap);
+    prefetch_tensormap(&wsmap);
+    prefetch_tensormap(&xsmap);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before either is used across the pair
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
+  pdl_wait();
+  bool ok_groups = true;
+  if (a.offsets != nullptr) {
+    ok_groups = build_groups(t, a.offsets, a.groups, a.tokens, kTokens);
+    if (!ok_groups && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, GPTQ_ERR_INVALID_ARG);
+  } else {
+    if (threadIdx.x == 0) {
+      t.off[0] = t.band[0] = t.tile[0] = 0;
+      t.off[1] = static_cast<int>(a.tokens);
+      t.band[1] = static_cast<int>((a.tokens + kFp4Band - 1) / kFp4Band);
+      t.tile[1] = static_cast<int>((a.tokens + kTokens - 1) / kTokens);
+    }
+    __syncthreads();
+  }
+  const int wtiles = static_cast<int>((a.rows + kPairRows - 1) / kPairRows);
+  const int wbands = static_cast<int>((a.rows + kRows - 1) / kRows);
+  const int64_t items = ok_groups ? static_cast<int64_t>(t.tile[a.groups]) * wtiles : 0;
+  const int quads = fp4_quads(a.n, NV);
+  const int mmas = (a.n + 63) / 64;
+  const int kstages = (a.n + kStageK - 1) / kStageK;
+
+  auto tile_of = [&](int64_t item) {
+    Tile x;
+    const int tt = static_cast<int>(item / wtiles);
+    x.wtile = static_cast<int>(item - static_cast<int64_t>(tt) * wtiles);
+    x.g = find_group(t.tile, a.groups, tt);
+    const int j = tt - t.tile[x.g];
+    x.token = t.off[x.g] + j * kTokens;
+    x.count = min(kTokens, t.off[x.g + 1] - x.token);
+    x.cols = (x.count + 15) / 16 * 16;
+    x.xband = t.band[x.g] + j * (kTokens / kFp4Band);
+    return x;
+  };
+  auto start = [&](Walk& w) {
+    w.item = pair;
+    w.kb = 0;
+    w.stage = w.phase = 0;
+    if (w.item < items) w.x = tile_of(w.item);
+  };
+  auto next = [&](Walk& w) {
+    if (++w.stage == kPairStages) {
+      w.stage = 0;
+      w.phase ^= 1u;
+    }
+    if (++w.kb == kstages) {
+      w.kb = 0;
+      w.item += pairs;
+      if (w.item < items) w.x = tile_of(w.item);
+    }
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- producer (both CTAs) ----------------
+      Walk w;
+      uint32_t issued = 0, issued_parity = 0;
+      for (start(w); w.item < items; next(w)) {
+        if (!mbar_wait(empty + w.stage, w.phase ^ 1u, a.wait_ns)) {
+          set_status(a.status, GPTQ_ERR_TIMEOUT);
+          *abort_flag = 1;
+          break;
+        }
+        if (*abort_flag) break;
+        const int half = w.x.cols / 2;  // tokens of this CTA
+        const int boxes = (half + kBoxRows - 1) / kBoxRows;
+        const int bands = w.x.cols > kFp4Band ? 2 : 1;
+        // the odd CTA's rows may not exist: it then loads the last band's scales for nothing
+        const int wband = min(2 * w.x.wtile + static_cast<int>(rank), wbands - 1);
+        uint8_t* sa = smem + size_t(w.stage) * kPairStageBytes;
+        uint8_t* sb = sa + kABytes;
+        uint8_t* ssa = sb + kPairBBytes;
+        uint8_t* ssb = ssa + kSfBytes;
+        const uint32_t bar = smem_cluster_addr(full + w.stage, 0);
+        if (rank == 0)
+          mbar_arrive_expect_tx(full + w.stage, 2 * (kABytes + boxes * (kBoxRows * kStageK / 2) + (1 + bands) * kStageSf));
+        const int kx = w.kb * (kStageK / 2);
+        tma_load_2d_pair(sa, &wmap, bar, kx, static_cast<int>(w.x.g * a.rows) + w.x.wtile * kPairRows + static_cast<int>(rank) * kRows);
+        for (int b = 0; b < boxes; ++b)
+          tma_load_2d_pair(sb + b * (kBoxRows * kStageK / 2), &xmap, bar, kx, w.x.token + static_cast<int>(rank) * half + b * kBoxRows);
+        tma_load_2d_pair(ssa, &wsmap, bar, 0, (w.x.g * wbands + wband) * quads + w.kb * kStageQuads);
+        for (int h = 0; h < bands; ++h)
+          tma_load_2d_pair(ssb + h * kSfBytes, &xsmap, bar, 0, (static_cast<int>(w.x.xband) + h) * quads + w.kb * kStageQuads);
+        issued |= 1u << w.stage;
+        issued_parity = (issued_parity & ~(1u << w.stage)) | (w.phase << w.stage);
+      }
+      if (rank == 0) {  // every stage that was armed has received both CTAs' bytes
+        for (int s = 0; s < kPairStages; ++s)
+          if (issued & (1u << s))
+            if (!mbar_wait(full + s, (issued_parity >> s) & 1u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ---------------- MMA issuer (even CTA) ----------------
+      // A stage's scales are copied to tensor memory before the products of
+      // the stage ahead of it are issued, so that the copy runs beside them.
+      Walk w, s;  // products; scale copies, up to one stage ahead
+      uint32_t done = 0, copied = 0;  // stages whose products are issued; whose scales are
+      uint32_t tiles = 0;
+      bool ok = true;
+      start(w);
+      start(s);
+      auto fail = [&] {
+        set_status(a.status, GPTQ_ERR_TIMEOUT);
+        *abort_flag = 1;
+        ok = false;
+      };
+      auto copy = [&] {  // s's stage is full
+        if (copied >= kPairSfSets) {  // the products that read this set last are complete
+          const uint32_t use = copied - kPairSfSets;
+          if (!mbar_wait(empty + use % kPairStages, use / kPairStages & 1u, a.wait_ns) || *abort_flag) return fail();
+        }
+        tc_fence_after();
+        const uint32_t ssa = smem_u32(smem + size_t(s.stage) * kPairStageBytes) + kABytes + kPairBBytes, ssb = ssa + kSfBytes;
+        const uint32_t tsa = tmem + kPairSfCol + copied % kPairSfSets * kPairSfStride, tsb = tsa + 16;
+        const int q = min(kStageQuads, quads - s.kb * kStageQuads);
+        for (int i = 0; i < q; ++i) {
+          copy_scales<2>(tsa + 4 * i, ssa + i * kFp4TileBytes);
+          copy_scales<2>(tsb + 8 * i, ssb + i * kFp4TileBytes);
+          if (s.x.cols > kFp4Band) copy_scales<2>(tsb + 8 * i + 4, ssb + kSfBytes + i * kFp4TileBytes);
+        }
+        ++copied;
+        next(s);
+      };
+      while (ok && w.item < items) {
+        if (w.kb == 0) {  // a new tile: the overlap with the last one has been read
+          if (tiles > 0 && (!mbar_wait(acc_free, (tiles - 1) & 1u, a.wait_ns) || *abort_flag)) {
+            fail();
+            break;
+          }
+        }
+        if (copied == done) {
+          if (!mbar_wait(full + s.stage, s.phase, a.wait_ns) || *abort_flag) {
+            fail();
+            break;
+          }
+          copy();
+          if (!ok) break;
+        }
+        if (s.item < items && copied == done + 1 && mbar_test_wait(full + s.stage, s.phase)) {
+          copy();
+          if (!ok) break;
+        }
+        tc_fence_after();
+        const uint32_t sa = smem_u32(smem + size_t(w.stage) * kPairStageBytes), sb = sa + kABytes;
+        const uint32_t tsa = tmem + kPairSfCol + done % kPairSfSets * kPairSfStride, tsb = tsa + 16;
+        const uint32_t acc = tmem + (tiles & 1u) * kAccShift;
+        const int m = min(kStageK / 64, mmas - w.kb * (kStageK / 64));
+        for (int i = 0; i < m; ++i) {
+          const int qi = i / kQuadMmas;
+          mma_fp4<NV, 2>(acc, smem_desc_sw128(sa + 32 * i, 16, 1024), smem_desc_sw128(sb + 32 * i, 16, 1024),
+                         fp4_idesc(NV, 2, w.x.cols, i % kQuadMmas), tsa + 4 * qi, tsb + 8 * qi, w.kb > 0 || i > 0);
+        }
+        mma_commit_pair(empty + w.stage, 0x3);
+        ++done;
+        if (w.kb == kstages - 1) {
+          mma_commit_pair(acc_full, 0x3);
+          ++tiles;
+        }
+        next(w);
+      }
+      mma_commit_pair(drain, 0x1);
+      if (!mbar_wait(drain, 0u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
+    }
+  } else {
+    // ---------------- epilogue (both CTAs) ----------------
+    const int quad = warp & 3;            // the tensor-memory lanes of this warp
+    const int turn = (warp - 2) >> 2;     // which of the two warps with these lanes
+    uint8_t* stg = staging + (warp - 2) * kStageOutBytes;
+    const bool vec = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.ldy * sizeof(OUT) % 16 == 0;
+    uint32_t tiles = 0;
+    for (int64_t item = pair; item < items; item += pairs, ++tiles) {
+      const Tile x = tile_of(item);
+      int ok = 1;
+      if (lane == 0) {
+        ok = mbar_wait(acc_full, tiles & 1u, a.wait_ns) && !*abort_flag;
+        if (!ok) {
+          set_status(a.status, GPTQ_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      const float tw = a.wt != nullptr ? a.wt[x.g] : 1.0f, tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
+      const int64_t r0 = static_cast<int64_t>(x.wtile) * kPairRows + rank * kRows + quad * 32;
+      OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r0;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (tiles & 1u) * kAccShift;
+      // chunks of 32 tokens, those in the overlap first: columns [96, 256) of
+      // the first accumulator, [0, 160) of the second
+      const int first = tiles & 1u ? 0 : 3;
+      uint32_t v[3][32];
+      int c[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        c[i] = (first + turn + 2 * i) % 8;
+        if (32 * c[i] < x.count) tmem_ld_32x32b_x32(acc + 32 * c[i], v[i]);
+      }
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(acc_free, 0));
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (32 * c[i] < x.count)
+          store_block(v[i], tw, tx, out + 32 * c[i] * a.ldy, a.ldy, x.count - 32 * c[i], a.rows - r0, vec, stg);
+      const int last = (first + turn + 6) % 8;
+      if (32 * last < x.count) {
+        tmem_ld_32x32b_x32(acc + 32 * last, v[0]);
+        tmem_ld_wait();
+        store_block(v[0], tw, tx, out + 32 * last * a.ldy, a.ldy, x.count - 32 * last, a.rows - r0, vec, stg);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // neither CTA leaves while the pair still uses its memory
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
 template <bool NV, typename OUT>
 gptq_status launch_matmul(const CUtensorMap& wmap, const CUtensorMap& xmap, const MatmulArgs& a, int64_t items,
                           const DeviceInfo* info, cudaStream_t st) {
@@ -338,6 +688,31 @@ gptq_status launch_matmul(const CUtensorMap& wmap, const CUtensorMap& xmap, cons
   if (launch_pdl(fp4_matmul_kernel<NV, OUT>, grid, kThreads, kSmemBytes, st, wmap, xmap, a) != cudaSuccess)
     return GPTQ_ERR_CUDA;
   return launch_status();
+}
+
+template <bool NV, typename OUT>
+gptq_status launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const CUtensorMap& wsmap,
+                        const CUtensorMap& xsmap, const MatmulArgs& a, int64_t tiles, const DeviceInfo* info,
+                        cudaStream_t st) {
+  static std::atomic<bool> attr_set[64] = {};  // per device, shared by host threads
+  if (!attr_set[info->device]) {
+    if (cudaFuncSetAttribute(fp4_pair_kernel<NV, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kPairSmemBytes)) != cudaSuccess)
+      return GPTQ_ERR_CUDA;
+    attr_set[info->device] = true;
+  }
+  const int64_t items = tiles * ceil_div(a.rows, kPairRows);
+  const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(items, std::max(1, info->sm_count / 2)));
+  return launch_cluster_pdl(fp4_pair_kernel<NV, OUT>, grid, kPairThreads, kPairSmemBytes, 2, st, wmap, xmap, wsmap, xsmap,
+                            a) == cudaSuccess
+             ? launch_status()
+             : GPTQ_ERR_CUDA;
+}
+
+// A tensor map of scale tiles: 512 bytes a row.
+bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t tiles, bool nv) {
+  return make_tensor_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales, kFp4TileBytes / 4, static_cast<uint64_t>(tiles),
+                            kFp4TileBytes, kFp4TileBytes / 4, kStageK / (4 * fp4_block(nv)), CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 }  // namespace
@@ -370,6 +745,18 @@ gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const
   a.wait_ns = wait_limit_ns();
   // token tiles: each group's last one may be part full
   const int64_t tiles = offsets == nullptr ? ceil_div(tokens, kTokens) : tokens / kTokens + std::min<int64_t>(groups, tokens);
+  if (tokens > kFp4Band * static_cast<int64_t>(groups)) {
+    CUtensorMap wsmap, xsmap;
+    const int64_t quads = fp4_quads(n, nv);
+    if (!scale_map(&wsmap, wscales, fp4_bands(groups * rows, groups, false) * quads, nv) ||
+        !scale_map(&xsmap, xscales, fp4_bands(tokens, groups, offsets != nullptr) * quads, nv))
+      return GPTQ_ERR_CUDA;
+    if (nv)
+      return y_bf16 ? launch_pair<true, __nv_bfloat16>(wmap, xmap, wsmap, xsmap, a, tiles, info, st)
+                    : launch_pair<true, float>(wmap, xmap, wsmap, xsmap, a, tiles, info, st);
+    return y_bf16 ? launch_pair<false, __nv_bfloat16>(wmap, xmap, wsmap, xsmap, a, tiles, info, st)
+                  : launch_pair<false, float>(wmap, xmap, wsmap, xsmap, a, tiles, info, st);
+  }
   const int64_t items = tiles * ceil_div(rows, kRows);
   if (nv)
     return y_bf16 ? launch_matmul<true, __nv_bfloat16>(wmap, xmap, a, items, info, st)
