@@ -111,6 +111,21 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Waits for a barrier's phase until the limit or until another role of the CTA
+// has given up; the first to run out records the timeout.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag, int* status) {
+  const uint64_t t0 = global_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > limit_ns) {
+      set_status(status, GPTQ_ERR_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
 struct Tile {
   int g;
   int token;   // first token (row of X)
@@ -402,7 +417,8 @@ struct Walk {
 template <bool NV, typename OUT>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                    const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap, MatmulArgs a) {
+                    const __grid_constant__ CUtensorMap xwide, const __grid_constant__ CUtensorMap wsmap,
+                    const __grid_constant__ CUtensorMap xsmap, MatmulArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + size_t(kPairStages) * kPairStageBytes;
@@ -416,7 +432,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   int* table = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);
   const GroupTable t{table, table + kFp4MaxGroups + 1, table + 2 * (kFp4MaxGroups + 1)};
 
-  const int warp = threadIdx.x / 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // the same register for the whole warp
   const int lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();
   const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
@@ -437,6 +453,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     fence_barrier_init();
     prefetch_tensormap(&wmap);
     prefetch_tensormap(&xmap);
+    prefetch_tensormap(&xwide);
     prefetch_tensormap(&wsmap);
     prefetch_tensormap(&xsmap);
   }
@@ -501,118 +518,133 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   };
 
+  // A role's wait: the whole warp goes by it.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+      if (lane == 0) ok = wait_slow(bar, parity, a.wait_ns, abort_flag, a.status);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    return ok;
+  };
+
+  // The producer and the MMA warp run their loops as whole warps, so that
+  // addresses and descriptors stay in uniform registers, and one lane issues.
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- producer (both CTAs) ----------------
-      Walk w;
-      uint32_t issued = 0, issued_parity = 0;
-      for (start(w); w.item < items; next(w)) {
-        if (!mbar_wait(empty + w.stage, w.phase ^ 1u, a.wait_ns)) {
-          set_status(a.status, GPTQ_ERR_TIMEOUT);
-          *abort_flag = 1;
-          break;
-        }
-        if (*abort_flag) break;
-        const int half = w.x.cols / 2;  // tokens of this CTA
-        const int boxes = (half + kBoxRows - 1) / kBoxRows;
-        const int bands = w.x.cols > kFp4Band ? 2 : 1;
-        // the odd CTA's rows may not exist: it then loads the last band's scales for nothing
-        const int wband = min(2 * w.x.wtile + static_cast<int>(rank), wbands - 1);
-        uint8_t* sa = smem + size_t(w.stage) * kPairStageBytes;
-        uint8_t* sb = sa + kABytes;
-        uint8_t* ssa = sb + kPairBBytes;
-        uint8_t* ssb = ssa + kSfBytes;
-        const uint32_t bar = smem_cluster_addr(full + w.stage, 0);
-        if (rank == 0)
-          mbar_arrive_expect_tx(full + w.stage, 2 * (kABytes + boxes * (kBoxRows * kStageK / 2) + (1 + bands) * kStageSf));
-        const int kx = w.kb * (kStageK / 2);
-        tma_load_2d_pair(sa, &wmap, bar, kx, static_cast<int>(w.x.g * a.rows) + w.x.wtile * kPairRows + static_cast<int>(rank) * kRows);
-        for (int b = 0; b < boxes; ++b)
-          tma_load_2d_pair(sb + b * (kBoxRows * kStageK / 2), &xmap, bar, kx, w.x.token + static_cast<int>(rank) * half + b * kBoxRows);
-        tma_load_2d_pair(ssa, &wsmap, bar, 0, (w.x.g * wbands + wband) * quads + w.kb * kStageQuads);
-        for (int h = 0; h < bands; ++h)
-          tma_load_2d_pair(ssb + h * kSfBytes, &xsmap, bar, 0, (static_cast<int>(w.x.xband) + h) * quads + w.kb * kStageQuads);
-        issued |= 1u << w.stage;
-        issued_parity = (issued_parity & ~(1u << w.stage)) | (w.phase << w.stage);
+    // ---------------- producer (both CTAs) ----------------
+    Walk w;
+    uint32_t issued = 0, issued_parity = 0;
+    const bool leader = elect_one();
+    for (start(w); w.item < items; next(w)) {
+      if (!wait(empty + w.stage, w.phase ^ 1u)) break;
+      const int half = w.x.cols / 2;  // tokens of this CTA
+      // one box of 128 rows, or boxes of 32 where that loads no more
+      const int boxes = half > 96 ? 0 : (half + kBoxRows - 1) / kBoxRows;
+      const uint32_t bbytes = boxes == 0 ? kPairBBytes : boxes * (kBoxRows * kStageK / 2);
+      // the odd CTA's rows may not exist: it then loads the last band's scales for nothing
+      const int wband = min(2 * w.x.wtile + static_cast<int>(rank), wbands - 1);
+      uint8_t* sa = smem + size_t(w.stage) * kPairStageBytes;
+      uint8_t* sb = sa + kABytes;
+      uint8_t* ssa = sb + kPairBBytes;
+      uint8_t* ssb = ssa + kStageSf;
+      const uint32_t bar = smem_cluster_addr(full + w.stage, 0);
+      const int kx = w.kb * (kStageK / 2);
+      const int wy = static_cast<int>(w.x.g * a.rows) + w.x.wtile * kPairRows + static_cast<int>(rank) * kRows;
+      const int xy = w.x.token + static_cast<int>(rank) * half;
+      if (leader) {
+        if (rank == 0) mbar_arrive_expect_tx(full + w.stage, 2 * (kABytes + bbytes + 3 * kStageSf));
+        tma_load_2d_pair(sa, &wmap, bar, kx, wy);
+        if (boxes == 0)
+          tma_load_2d_pair(sb, &xwide, bar, kx, xy);
+        else
+          for (int b = 0; b < boxes; ++b) tma_load_2d_pair(sb + b * (kBoxRows * kStageK / 2), &xmap, bar, kx, xy + b * kBoxRows);
+        tma_load_3d_pair(ssa, &wsmap, bar, 0, w.kb * kStageQuads, w.x.g * wbands + wband);
+        tma_load_3d_pair(ssb, &xsmap, bar, 0, w.kb * kStageQuads, static_cast<int>(w.x.xband));
       }
-      if (rank == 0) {  // every stage that was armed has received both CTAs' bytes
-        for (int s = 0; s < kPairStages; ++s)
-          if (issued & (1u << s))
-            if (!mbar_wait(full + s, (issued_parity >> s) & 1u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
-      }
+      __syncwarp();
+      issued |= 1u << w.stage;
+      issued_parity = (issued_parity & ~(1u << w.stage)) | (w.phase << w.stage);
+    }
+    if (rank == 0 && leader) {  // every stage that was armed has received both CTAs' bytes
+      for (int s = 0; s < kPairStages; ++s)
+        if (issued & (1u << s))
+          if (!mbar_wait(full + s, (issued_parity >> s) & 1u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // ---------------- MMA issuer (even CTA) ----------------
       // A stage's scales are copied to tensor memory before the products of
       // the stage ahead of it are issued, so that the copy runs beside them.
       Walk w, s;  // products; scale copies, up to one stage ahead
       uint32_t done = 0, copied = 0;  // stages whose products are issued; whose scales are
-      uint32_t tiles = 0;
-      bool ok = true;
+      uint32_t tiles = 0, set = 0, sset = 0;  // sets of scale columns of w and s
+      const bool leader = elect_one();
+      const uint32_t ring = smem_u32(smem);
+      const uint32_t sf_col = tmem + kPairSfCol;
       start(w);
       start(s);
-      auto fail = [&] {
-        set_status(a.status, GPTQ_ERR_TIMEOUT);
-        *abort_flag = 1;
-        ok = false;
-      };
       auto copy = [&] {  // s's stage is full
         if (copied >= kPairSfSets) {  // the products that read this set last are complete
           const uint32_t use = copied - kPairSfSets;
-          if (!mbar_wait(empty + use % kPairStages, use / kPairStages & 1u, a.wait_ns) || *abort_flag) return fail();
+          if (!wait(empty + use % kPairStages, use / kPairStages & 1u)) return false;
         }
         tc_fence_after();
-        const uint32_t ssa = smem_u32(smem + size_t(s.stage) * kPairStageBytes) + kABytes + kPairBBytes, ssb = ssa + kSfBytes;
-        const uint32_t tsa = tmem + kPairSfCol + copied % kPairSfSets * kPairSfStride, tsb = tsa + 16;
-        const int q = min(kStageQuads, quads - s.kb * kStageQuads);
-        for (int i = 0; i < q; ++i) {
-          copy_scales<2>(tsa + 4 * i, ssa + i * kFp4TileBytes);
-          copy_scales<2>(tsb + 8 * i, ssb + i * kFp4TileBytes);
-          if (s.x.cols > kFp4Band) copy_scales<2>(tsb + 8 * i + 4, ssb + kSfBytes + i * kFp4TileBytes);
+        const uint32_t ssa = ring + s.stage * kPairStageBytes + kABytes + kPairBBytes, ssb = ssa + kStageSf;
+        const uint32_t tsa = sf_col + sset * kPairSfStride, tsb = tsa + 16;
+        const int q = quads - s.kb * kStageQuads;
+        const bool two = s.x.cols > kFp4Band;
+        if (leader) {
+#pragma unroll
+          for (int i = 0; i < kStageQuads; ++i) {
+            if (i < q) {
+              copy_scales<2>(tsa + 4 * i, ssa + i * kFp4TileBytes);
+              copy_scales<2>(tsb + 8 * i, ssb + i * kFp4TileBytes);
+              if (two) copy_scales<2>(tsb + 8 * i + 4, ssb + kStageSf + i * kFp4TileBytes);
+            }
+          }
         }
+        __syncwarp();
         ++copied;
+        sset = sset == kPairSfSets - 1 ? 0 : sset + 1;
         next(s);
+        return true;
       };
-      while (ok && w.item < items) {
-        if (w.kb == 0) {  // a new tile: the overlap with the last one has been read
-          if (tiles > 0 && (!mbar_wait(acc_free, (tiles - 1) & 1u, a.wait_ns) || *abort_flag)) {
-            fail();
-            break;
-          }
-        }
+      while (w.item < items) {
+        // a new tile: the overlap with the last one has been read
+        if (w.kb == 0 && tiles > 0 && !wait(acc_free, (tiles - 1) & 1u)) break;
         if (copied == done) {
-          if (!mbar_wait(full + s.stage, s.phase, a.wait_ns) || *abort_flag) {
-            fail();
-            break;
-          }
-          copy();
-          if (!ok) break;
+          if (!wait(full + s.stage, s.phase) || !copy()) break;
         }
-        if (s.item < items && copied == done + 1 && mbar_test_wait(full + s.stage, s.phase)) {
-          copy();
-          if (!ok) break;
-        }
+        if (s.item < items && __all_sync(0xffffffffu, mbar_test_wait(full + s.stage, s.phase)) && !copy()) break;
         tc_fence_after();
-        const uint32_t sa = smem_u32(smem + size_t(w.stage) * kPairStageBytes), sb = sa + kABytes;
-        const uint32_t tsa = tmem + kPairSfCol + done % kPairSfSets * kPairSfStride, tsb = tsa + 16;
+        const uint32_t sa = ring + w.stage * kPairStageBytes, sb = sa + kABytes;
+        const uint32_t tsa = sf_col + set * kPairSfStride, tsb = tsa + 16;
         const uint32_t acc = tmem + (tiles & 1u) * kAccShift;
-        const int m = min(kStageK / 64, mmas - w.kb * (kStageK / 64));
-        for (int i = 0; i < m; ++i) {
-          const int qi = i / kQuadMmas;
-          mma_fp4<NV, 2>(acc, smem_desc_sw128(sa + 32 * i, 16, 1024), smem_desc_sw128(sb + 32 * i, 16, 1024),
-                         fp4_idesc(NV, 2, w.x.cols, i % kQuadMmas), tsa + 4 * qi, tsb + 8 * qi, w.kb > 0 || i > 0);
+        const int m = mmas - w.kb * (kStageK / 64);
+        const uint32_t more = w.kb > 0;
+        const uint64_t adesc = smem_desc_sw128(sa, 16, 1024), bdesc = smem_desc_sw128(sb, 16, 1024);
+        const uint32_t idesc = fp4_idesc(NV, 2, w.x.cols, 0), pairs_of = fp4_idesc(NV, 2, 0, 1) ^ fp4_idesc(NV, 2, 0, 0);
+        if (leader) {
+#pragma unroll
+          for (int i = 0; i < kStageK / 64; ++i) {  // 64 columns of K: 32 bytes, two units of a descriptor's address
+            const int qi = i / kQuadMmas;
+            if (i < m)
+              mma_fp4<NV, 2>(acc, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pairs_of : idesc, tsa + 4 * qi,
+                             tsb + 8 * qi, i > 0 ? 1u : more);
+          }
+          mma_commit_pair(empty + w.stage, 0x3);
+          if (w.kb == kstages - 1) mma_commit_pair(acc_full, 0x3);
         }
-        mma_commit_pair(empty + w.stage, 0x3);
+        __syncwarp();
         ++done;
-        if (w.kb == kstages - 1) {
-          mma_commit_pair(acc_full, 0x3);
-          ++tiles;
-        }
+        set = set == kPairSfSets - 1 ? 0 : set + 1;
+        if (w.kb == kstages - 1) ++tiles;
         next(w);
       }
-      mma_commit_pair(drain, 0x1);
-      if (!mbar_wait(drain, 0u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
+      if (leader) {
+        mma_commit_pair(drain, 0x1);
+        if (!mbar_wait(drain, 0u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
+      }
     }
   } else {
     // ---------------- epilogue (both CTAs) ----------------
@@ -623,16 +655,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint32_t tiles = 0;
     for (int64_t item = pair; item < items; item += pairs, ++tiles) {
       const Tile x = tile_of(item);
-      int ok = 1;
-      if (lane == 0) {
-        ok = mbar_wait(acc_full, tiles & 1u, a.wait_ns) && !*abort_flag;
-        if (!ok) {
-          set_status(a.status, GPTQ_ERR_TIMEOUT);
-          *abort_flag = 1;
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
+      if (!wait(acc_full, tiles & 1u)) break;
       tc_fence_after();
       const float tw = a.wt != nullptr ? a.wt[x.g] : 1.0f, tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
       const int64_t r0 = static_cast<int64_t>(x.wtile) * kPairRows + rank * kRows + quad * 32;
@@ -691,8 +714,8 @@ gptq_status launch_matmul(const CUtensorMap& wmap, const CUtensorMap& xmap, cons
 }
 
 template <bool NV, typename OUT>
-gptq_status launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const CUtensorMap& wsmap,
-                        const CUtensorMap& xsmap, const MatmulArgs& a, int64_t tiles, const DeviceInfo* info,
+gptq_status launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const CUtensorMap& xwide,
+                        const CUtensorMap& wsmap, const CUtensorMap& xsmap, const MatmulArgs& a, int64_t tiles, const DeviceInfo* info,
                         cudaStream_t st) {
   static std::atomic<bool> attr_set[64] = {};  // per device, shared by host threads
   if (!attr_set[info->device]) {
@@ -703,16 +726,19 @@ gptq_status launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const 
   }
   const int64_t items = tiles * ceil_div(a.rows, kPairRows);
   const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(items, std::max(1, info->sm_count / 2)));
-  return launch_cluster_pdl(fp4_pair_kernel<NV, OUT>, grid, kPairThreads, kPairSmemBytes, 2, st, wmap, xmap, wsmap, xsmap,
-                            a) == cudaSuccess
+  return launch_cluster_pdl(fp4_pair_kernel<NV, OUT>, grid, kPairThreads, kPairSmemBytes, 2, st, wmap, xmap, xwide, wsmap,
+                            xsmap, a) == cudaSuccess
              ? launch_status()
              : GPTQ_ERR_CUDA;
 }
 
-// A tensor map of scale tiles: 512 bytes a row.
-bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t tiles, bool nv) {
-  return make_tensor_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales, kFp4TileBytes / 4, static_cast<uint64_t>(tiles),
-                            kFp4TileBytes, kFp4TileBytes / 4, kStageK / (4 * fp4_block(nv)), CU_TENSOR_MAP_SWIZZLE_NONE);
+// Scale tiles as bytes x quads x bands, `bands` bands a box.
+bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t quads, int64_t bands, bool nv, uint32_t box_bands) {
+  return make_tensor_map_3d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales,
+                            {kFp4TileBytes / 4, static_cast<uint64_t>(quads), static_cast<uint64_t>(bands)},
+                            {kFp4TileBytes, static_cast<uint64_t>(quads) * kFp4TileBytes},
+                            {kFp4TileBytes / 4, static_cast<uint32_t>(kStageK / (4 * fp4_block(nv))), box_bands},
+                            CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 }  // namespace
@@ -746,16 +772,18 @@ gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const
   // token tiles: each group's last one may be part full
   const int64_t tiles = offsets == nullptr ? ceil_div(tokens, kTokens) : tokens / kTokens + std::min<int64_t>(groups, tokens);
   if (tokens > kFp4Band * static_cast<int64_t>(groups)) {
-    CUtensorMap wsmap, xsmap;
+    CUtensorMap xwide, wsmap, xsmap;
     const int64_t quads = fp4_quads(n, nv);
-    if (!scale_map(&wsmap, wscales, fp4_bands(groups * rows, groups, false) * quads, nv) ||
-        !scale_map(&xsmap, xscales, fp4_bands(tokens, groups, offsets != nullptr) * quads, nv))
+    if (!make_tensor_map_2d(&xwide, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, pitch, tokens, pitch, kStageK / 2, kTokens / 2,
+                            CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !scale_map(&wsmap, wscales, quads, fp4_bands(groups * rows, groups, false), nv, 1) ||
+        !scale_map(&xsmap, xscales, quads, offsets != nullptr ? fp4_bands(tokens, groups, true) : ceil_div(tokens, kFp4Band), nv, 2))
       return GPTQ_ERR_CUDA;
     if (nv)
-      return y_bf16 ? launch_pair<true, __nv_bfloat16>(wmap, xmap, wsmap, xsmap, a, tiles, info, st)
-                    : launch_pair<true, float>(wmap, xmap, wsmap, xsmap, a, tiles, info, st);
-    return y_bf16 ? launch_pair<false, __nv_bfloat16>(wmap, xmap, wsmap, xsmap, a, tiles, info, st)
-                  : launch_pair<false, float>(wmap, xmap, wsmap, xsmap, a, tiles, info, st);
+      return y_bf16 ? launch_pair<true, __nv_bfloat16>(wmap, xmap, xwide, wsmap, xsmap, a, tiles, info, st)
+                    : launch_pair<true, float>(wmap, xmap, xwide, wsmap, xsmap, a, tiles, info, st);
+    return y_bf16 ? launch_pair<false, __nv_bfloat16>(wmap, xmap, xwide, wsmap, xsmap, a, tiles, info, st)
+                  : launch_pair<false, float>(wmap, xmap, xwide, wsmap, xsmap, a, tiles, info, st);
   }
   const int64_t items = tiles * ceil_div(rows, kRows);
   if (nv)
