@@ -91,6 +91,12 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
+// A value that every lane of a converged warp holds, in the form in which the
+// compiler knows that (it can then live in a uniform register, which is where
+// the asynchronous instructions take their operands from).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Waits for the phase with the given parity to complete, for at most
 // `limit_ns` nanoseconds of global time.  Returns false if it ran out.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {

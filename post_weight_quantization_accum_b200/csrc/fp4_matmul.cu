@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // the same register for the whole warp
   const int lane = threadIdx.x % 32;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = uniform(cluster_ctarank());
   const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   constexpr int kBlk = NV ? 16 : 32;
   constexpr int kStageQuads = kStageK / (4 * kBlk);
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers exist before either is used across the pair
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   pdl_trigger();
   pdl_wait();
   bool ok_groups = true;
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
   const int wtiles = static_cast<int>((a.rows + kPairRows - 1) / kPairRows);
   const int wbands = static_cast<int>((a.rows + kRows - 1) / kRows);
-  const int64_t items = ok_groups ? static_cast<int64_t>(t.tile[a.groups]) * wtiles : 0;
+  const int64_t items = ok_groups ? static_cast<int64_t>(uniform(t.tile[a.groups])) * wtiles : 0;
   const int quads = fp4_quads(a.n, NV);
   const int mmas = (a.n + 63) / 64;
   const int kstages = (a.n + kStageK - 1) / kStageK;
@@ -492,12 +492,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     Tile x;
     const int tt = static_cast<int>(item / wtiles);
     x.wtile = static_cast<int>(item - static_cast<int64_t>(tt) * wtiles);
-    x.g = find_group(t.tile, a.groups, tt);
-    const int j = tt - t.tile[x.g];
-    x.token = t.off[x.g] + j * kTokens;
-    x.count = min(kTokens, t.off[x.g + 1] - x.token);
+    x.g = uniform(find_group(t.tile, a.groups, tt));
+    const int j = tt - uniform(t.tile[x.g]);
+    x.token = uniform(t.off[x.g]) + j * kTokens;
+    x.count = min(kTokens, uniform(t.off[x.g + 1]) - x.token);
     x.cols = (x.count + 15) / 16 * 16;
-    x.xband = t.band[x.g] + j * (kTokens / kFp4Band);
+    x.xband = uniform(t.band[x.g]) + j * (kTokens / kFp4Band);
     return x;
   };
   auto start = [&](Walk& w) {
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // ---------------- producer (both CTAs) ----------------
     Walk w;
     uint32_t issued = 0, issued_parity = 0;
-    const bool leader = elect_one();
+    const uint32_t full0 = uniform(smem_cluster_addr(full, 0));  // the even CTA's barriers
     for (start(w); w.item < items; next(w)) {
       if (!wait(empty + w.stage, w.phase ^ 1u)) break;
       const int half = w.x.cols / 2;  // tokens of this CTA
@@ -547,11 +547,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       uint8_t* sb = sa + kABytes;
       uint8_t* ssa = sb + kPairBBytes;
       uint8_t* ssb = ssa + kStageSf;
-      const uint32_t bar = smem_cluster_addr(full + w.stage, 0);
+      const uint32_t bar = full0 + 8 * w.stage;
       const int kx = w.kb * (kStageK / 2);
       const int wy = static_cast<int>(w.x.g * a.rows) + w.x.wtile * kPairRows + static_cast<int>(rank) * kRows;
       const int xy = w.x.token + static_cast<int>(rank) * half;
-      if (leader) {
+      if (elect_one()) {
         if (rank == 0) mbar_arrive_expect_tx(full + w.stage, 2 * (kABytes + bbytes + 3 * kStageSf));
         tma_load_2d_pair(sa, &wmap, bar, kx, wy);
         if (boxes == 0)
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       issued |= 1u << w.stage;
       issued_parity = (issued_parity & ~(1u << w.stage)) | (w.phase << w.stage);
     }
-    if (rank == 0 && leader) {  // every stage that was armed has received both CTAs' bytes
+    if (rank == 0 && lane == 0) {  // every stage that was armed has received both CTAs' bytes
       for (int s = 0; s < kPairStages; ++s)
         if (issued & (1u << s))
           if (!mbar_wait(full + s, (issued_parity >> s) & 1u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
@@ -573,75 +573,63 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     if (rank == 0) {
       // ---------------- MMA issuer (even CTA) ----------------
-      // A stage's scales are copied to tensor memory before the products of
-      // the stage ahead of it are issued, so that the copy runs beside them.
-      Walk w, s;  // products; scale copies, up to one stage ahead
-      uint32_t done = 0, copied = 0;  // stages whose products are issued; whose scales are
-      uint32_t tiles = 0, set = 0, sset = 0;  // sets of scale columns of w and s
-      const bool leader = elect_one();
+      // Per stage twelve scale copies (nvfp4) and four products, in line: a
+      // copy costs 10 cycles of the tensor pipe, a product 130.  Whole stages
+      // take a path without conditions, which are what issuing costs.
+      Walk w;
+      uint32_t done = 0, tiles = 0, set = 0;  // stages and tiles issued; the scale columns in turn
       const uint32_t ring = smem_u32(smem);
-      const uint32_t sf_col = tmem + kPairSfCol;
-      start(w);
-      start(s);
-      auto copy = [&] {  // s's stage is full
-        if (copied >= kPairSfSets) {  // the products that read this set last are complete
-          const uint32_t use = copied - kPairSfSets;
-          if (!wait(empty + use % kPairStages, use / kPairStages & 1u)) return false;
+      const uint32_t pair_bits = fp4_idesc(NV, 2, 0, 1) ^ fp4_idesc(NV, 2, 0, 0);
+      for (start(w); w.item < items; next(w)) {
+        // a new tile: the overlap with the last one has been read
+        if (w.kb == 0 && tiles > 0 && !wait(acc_free, (tiles - 1) & 1u)) break;
+        if (!wait(full + w.stage, w.phase)) break;
+        if (done >= kPairSfSets) {  // the products that read this set of scale columns last are complete
+          const uint32_t use = done - kPairSfSets;
+          if (!wait(empty + use % kPairStages, use / kPairStages & 1u)) break;
         }
         tc_fence_after();
-        const uint32_t ssa = ring + s.stage * kPairStageBytes + kABytes + kPairBBytes, ssb = ssa + kStageSf;
-        const uint32_t tsa = sf_col + sset * kPairSfStride, tsb = tsa + 16;
-        const int q = quads - s.kb * kStageQuads;
-        const bool two = s.x.cols > kFp4Band;
-        if (leader) {
+        const uint32_t sa = ring + w.stage * kPairStageBytes;
+        const uint32_t ssa = sa + kABytes + kPairBBytes, ssb = ssa + kStageSf;
+        const uint32_t tsa = tmem + kPairSfCol + set * kPairSfStride, tsb = tsa + 16;
+        const uint32_t acc = tmem + (tiles & 1u) * kAccShift;
+        const uint32_t more = w.kb > 0;
+        const uint64_t adesc = smem_desc_sw128(sa, 16, 1024), bdesc = smem_desc_sw128(sa + kABytes, 16, 1024);
+        const uint32_t idesc = fp4_idesc(NV, 2, w.x.cols, 0);
+        const int m = mmas - w.kb * (kStageK / 64), q = quads - w.kb * kStageQuads;
+        const bool two = w.x.cols > kFp4Band, last = w.kb == kstages - 1;
+        if (elect_one()) {
+          // 64 columns of K are 32 bytes, two units of a descriptor's address
+          if (m >= kStageK / 64) {
 #pragma unroll
-          for (int i = 0; i < kStageQuads; ++i) {
-            if (i < q) {
+            for (int i = 0; i < kStageQuads; ++i) {
+              copy_scales<2>(tsa + 4 * i, ssa + i * kFp4TileBytes);
+              copy_scales<2>(tsb + 8 * i, ssb + i * kFp4TileBytes);
+              copy_scales<2>(tsb + 8 * i + 4, ssb + kStageSf + i * kFp4TileBytes);  // (for nothing up to 128 tokens)
+            }
+#pragma unroll
+            for (int i = 0; i < kStageK / 64; ++i)
+              mma_fp4<NV, 2>(acc, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
+                             tsa + i / kQuadMmas * 4, tsb + i / kQuadMmas * 8, i > 0 ? 1u : more);
+          } else {
+            for (int i = 0; i < q; ++i) {
               copy_scales<2>(tsa + 4 * i, ssa + i * kFp4TileBytes);
               copy_scales<2>(tsb + 8 * i, ssb + i * kFp4TileBytes);
               if (two) copy_scales<2>(tsb + 8 * i + 4, ssb + kStageSf + i * kFp4TileBytes);
             }
-          }
-        }
-        __syncwarp();
-        ++copied;
-        sset = sset == kPairSfSets - 1 ? 0 : sset + 1;
-        next(s);
-        return true;
-      };
-      while (w.item < items) {
-        // a new tile: the overlap with the last one has been read
-        if (w.kb == 0 && tiles > 0 && !wait(acc_free, (tiles - 1) & 1u)) break;
-        if (copied == done) {
-          if (!wait(full + s.stage, s.phase) || !copy()) break;
-        }
-        if (s.item < items && __all_sync(0xffffffffu, mbar_test_wait(full + s.stage, s.phase)) && !copy()) break;
-        tc_fence_after();
-        const uint32_t sa = ring + w.stage * kPairStageBytes, sb = sa + kABytes;
-        const uint32_t tsa = sf_col + set * kPairSfStride, tsb = tsa + 16;
-        const uint32_t acc = tmem + (tiles & 1u) * kAccShift;
-        const int m = mmas - w.kb * (kStageK / 64);
-        const uint32_t more = w.kb > 0;
-        const uint64_t adesc = smem_desc_sw128(sa, 16, 1024), bdesc = smem_desc_sw128(sb, 16, 1024);
-        const uint32_t idesc = fp4_idesc(NV, 2, w.x.cols, 0), pairs_of = fp4_idesc(NV, 2, 0, 1) ^ fp4_idesc(NV, 2, 0, 0);
-        if (leader) {
-#pragma unroll
-          for (int i = 0; i < kStageK / 64; ++i) {  // 64 columns of K: 32 bytes, two units of a descriptor's address
-            const int qi = i / kQuadMmas;
-            if (i < m)
-              mma_fp4<NV, 2>(acc, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pairs_of : idesc, tsa + 4 * qi,
-                             tsb + 8 * qi, i > 0 ? 1u : more);
+            for (int i = 0; i < m; ++i)
+              mma_fp4<NV, 2>(acc, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
+                             tsa + i / kQuadMmas * 4, tsb + i / kQuadMmas * 8, i > 0 ? 1u : more);
           }
           mma_commit_pair(empty + w.stage, 0x3);
-          if (w.kb == kstages - 1) mma_commit_pair(acc_full, 0x3);
+          if (last) mma_commit_pair(acc_full, 0x3);
         }
         __syncwarp();
         ++done;
         set = set == kPairSfSets - 1 ? 0 : set + 1;
-        if (w.kb == kstages - 1) ++tiles;
-        next(w);
+        tiles += last;
       }
-      if (leader) {
+      if (elect_one()) {
         mma_commit_pair(drain, 0x1);
         if (!mbar_wait(drain, 0u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
       }
