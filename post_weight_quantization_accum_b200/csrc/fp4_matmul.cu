@@ -368,17 +368,34 @@ constexpr uint32_t kAccShift = 96;
 constexpr uint32_t kPairSfCol = kAccShift + kTokens, kPairSfStride = 48, kPairSfSets = 3;
 static_assert(kPairSfCol + kPairSfSets * kPairSfStride <= kTmemCols, "tensor memory");
 
+// The two tensor scales of a group as factors of its sums: their product, or
+// each in turn where the product would leave the normal numbers.
+struct Scale {
+  float k;
+  float before;  // 1 where k is the product
+};
+__device__ __forceinline__ Scale tile_scale(const MatmulArgs& a, int g) {
+  if (a.wt == nullptr) return {1.0f, 1.0f};
+  const float tw = a.wt[g], tx = a.xt[g], k = tw * tx;
+  if (k >= 1.17549435e-38f && k <= 3.40282347e38f) return {k, 1.0f};
+  return {tx, tw};
+}
+
 // 32 features x 32 tokens (v[j]: token j of this lane's feature) to y: through
 // shared memory as rows of 64 bytes (bf16), or straight (fp32: a row of 32
 // lanes is a line).  Only `tokens` rows and `features` lanes exist.
-__device__ __forceinline__ void store_block(const uint32_t (&v)[32], float tw, float tx, __nv_bfloat16* out, int64_t ldy,
-                                            int tokens, int64_t features, bool vec, uint8_t* stg) {
+__device__ __forceinline__ void store_block(uint32_t (&v)[32], Scale k, __nv_bfloat16* out, int64_t ldy, int tokens,
+                                            int64_t features, bool vec, uint8_t* stg) {
   const int lane = threadIdx.x & 31;
+  if (k.before != 1.0f) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * k.before);
+  }
   if (vec && features >= 32) {
     uint16_t* s = reinterpret_cast<uint16_t*>(stg) + lane;
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[j]) * tw * tx, __uint_as_float(v[j + 1]) * tw * tx);
+      const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[j]) * k.k, __uint_as_float(v[j + 1]) * k.k);
       s[32 * j] = __bfloat16_as_ushort(p.x);
       s[32 * j + 32] = __bfloat16_as_ushort(p.y);
     }
@@ -393,26 +410,18 @@ __device__ __forceinline__ void store_block(const uint32_t (&v)[32], float tw, f
   } else if (lane < features) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (j < tokens) out[j * ldy + lane] = __float2bfloat16_rn(__uint_as_float(v[j]) * tw * tx);
+      if (j < tokens) out[j * ldy + lane] = __float2bfloat16_rn(__uint_as_float(v[j]) * k.k);
   }
 }
-__device__ __forceinline__ void store_block(const uint32_t (&v)[32], float tw, float tx, float* out, int64_t ldy, int tokens,
+__device__ __forceinline__ void store_block(uint32_t (&v)[32], Scale k, float* out, int64_t ldy, int tokens,
                                             int64_t features, bool, uint8_t*) {
   const int lane = threadIdx.x & 31;
   if (lane < features) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (j < tokens) out[j * ldy + lane] = __uint_as_float(v[j]) * tw * tx;
+      if (j < tokens) out[j * ldy + lane] = __uint_as_float(v[j]) * k.before * k.k;
   }
 }
-
-// Where a role is in the sequence of (tile, K stage) that the CTA works off.
-struct Walk {
-  Tile x;
-  int64_t item;
-  int kb;
-  uint32_t stage, phase;  // of the operand ring
-};
 
 template <bool NV, typename OUT>
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -492,115 +501,102 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     Tile x;
     const int tt = static_cast<int>(item / wtiles);
     x.wtile = static_cast<int>(item - static_cast<int64_t>(tt) * wtiles);
-    x.g = uniform(find_group(t.tile, a.groups, tt));
-    const int j = tt - uniform(t.tile[x.g]);
-    x.token = uniform(t.off[x.g]) + j * kTokens;
-    x.count = min(kTokens, uniform(t.off[x.g + 1]) - x.token);
+    x.g = find_group(t.tile, a.groups, tt);
+    const int j = tt - t.tile[x.g];
+    x.token = t.off[x.g] + j * kTokens;
+    x.count = min(kTokens, t.off[x.g + 1] - x.token);
     x.cols = (x.count + 15) / 16 * 16;
-    x.xband = uniform(t.band[x.g]) + j * (kTokens / kFp4Band);
+    x.xband = t.band[x.g] + j * (kTokens / kFp4Band);
     return x;
   };
-  auto start = [&](Walk& w) {
-    w.item = pair;
-    w.kb = 0;
-    w.stage = w.phase = 0;
-    if (w.item < items) w.x = tile_of(w.item);
-  };
-  auto next = [&](Walk& w) {
-    if (++w.stage == kPairStages) {
-      w.stage = 0;
-      w.phase ^= 1u;
-    }
-    if (++w.kb == kstages) {
-      w.kb = 0;
-      w.item += pairs;
-      if (w.item < items) w.x = tile_of(w.item);
-    }
-  };
-
-  // A role's wait: the whole warp goes by it.
+  // A single thread's wait.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!__all_sync(0xffffffffu, ok)) {
-      if (lane == 0) ok = wait_slow(bar, parity, a.wait_ns, abort_flag, a.status);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-    }
-    return ok;
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, a.wait_ns, abort_flag, a.status);
   };
 
-  // The producer and the MMA warp run their loops as whole warps, so that
-  // addresses and descriptors stay in uniform registers, and one lane issues.
   if (warp == 0) {
-    // ---------------- producer (both CTAs) ----------------
-    Walk w;
-    uint32_t issued = 0, issued_parity = 0;
-    const uint32_t full0 = uniform(smem_cluster_addr(full, 0));  // the even CTA's barriers
-    for (start(w); w.item < items; next(w)) {
-      if (!wait(empty + w.stage, w.phase ^ 1u)) break;
-      const int half = w.x.cols / 2;  // tokens of this CTA
-      // one box of 128 rows, or boxes of 32 where that loads no more
-      const int boxes = half > 96 ? 0 : (half + kBoxRows - 1) / kBoxRows;
-      const uint32_t bbytes = boxes == 0 ? kPairBBytes : boxes * (kBoxRows * kStageK / 2);
-      // the odd CTA's rows may not exist: it then loads the last band's scales for nothing
-      const int wband = min(2 * w.x.wtile + static_cast<int>(rank), wbands - 1);
-      uint8_t* sa = smem + size_t(w.stage) * kPairStageBytes;
-      uint8_t* sb = sa + kABytes;
-      uint8_t* ssa = sb + kPairBBytes;
-      uint8_t* ssb = ssa + kStageSf;
-      const uint32_t bar = full0 + 8 * w.stage;
-      const int kx = w.kb * (kStageK / 2);
-      const int wy = static_cast<int>(w.x.g * a.rows) + w.x.wtile * kPairRows + static_cast<int>(rank) * kRows;
-      const int xy = w.x.token + static_cast<int>(rank) * half;
-      if (elect_one()) {
-        if (rank == 0) mbar_arrive_expect_tx(full + w.stage, 2 * (kABytes + bbytes + 3 * kStageSf));
-        tma_load_2d_pair(sa, &wmap, bar, kx, wy);
-        if (boxes == 0)
-          tma_load_2d_pair(sb, &xwide, bar, kx, xy);
-        else
-          for (int b = 0; b < boxes; ++b) tma_load_2d_pair(sb + b * (kBoxRows * kStageK / 2), &xmap, bar, kx, xy + b * kBoxRows);
-        tma_load_3d_pair(ssa, &wsmap, bar, 0, w.kb * kStageQuads, w.x.g * wbands + wband);
-        tma_load_3d_pair(ssb, &xsmap, bar, 0, w.kb * kStageQuads, static_cast<int>(w.x.xband));
+    if (elect_one()) {
+      // ---------------- producer (both CTAs) ----------------
+      uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
+      const uint32_t full0 = smem_cluster_addr(full, 0);  // the even CTA's barriers
+      bool ok = true;
+      for (int64_t item = pair; ok && item < items; item += pairs) {
+        const Tile x = tile_of(item);
+        const int half = x.cols / 2;  // tokens of this CTA
+        // one box of 128 rows, or boxes of 32 where that loads no more
+        const int boxes = half > 96 ? 0 : (half + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = 2 * (kABytes + (boxes == 0 ? kPairBBytes : boxes * (kBoxRows * kStageK / 2)) + 3 * kStageSf);
+        // the odd CTA's rows may not exist: it then loads the last band's scales for nothing
+        const int wband = x.g * wbands + min(2 * x.wtile + static_cast<int>(rank), wbands - 1);
+        const int xband = static_cast<int>(x.xband);
+        const int wy = static_cast<int>(x.g * a.rows) + x.wtile * kPairRows + static_cast<int>(rank) * kRows;
+        const int xy = x.token + static_cast<int>(rank) * half;
+        for (int kb = 0; kb < kstages; ++kb) {
+          ok = wait(empty + stage, phase ^ 1u);
+          if (!ok) break;
+          uint8_t* sa = smem + stage * kPairStageBytes;
+          const uint32_t bar = full0 + 8 * stage;
+          if (rank == 0) mbar_arrive_expect_tx(full + stage, bytes);
+          tma_load_2d_pair(sa, &wmap, bar, kb * (kStageK / 2), wy);
+          if (boxes == 0)
+            tma_load_2d_pair(sa + kABytes, &xwide, bar, kb * (kStageK / 2), xy);
+          else
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d_pair(sa + kABytes + b * (kBoxRows * kStageK / 2), &xmap, bar, kb * (kStageK / 2), xy + b * kBoxRows);
+          tma_load_3d_pair(sa + kABytes + kPairBBytes, &wsmap, bar, 0, kb * kStageQuads, wband);
+          tma_load_3d_pair(sa + kABytes + kPairBBytes + kStageSf, &xsmap, bar, 0, kb * kStageQuads, xband);
+          issued |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == kPairStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
       }
-      __syncwarp();
-      issued |= 1u << w.stage;
-      issued_parity = (issued_parity & ~(1u << w.stage)) | (w.phase << w.stage);
-    }
-    if (rank == 0 && lane == 0) {  // every stage that was armed has received both CTAs' bytes
-      for (int s = 0; s < kPairStages; ++s)
-        if (issued & (1u << s))
-          if (!mbar_wait(full + s, (issued_parity >> s) & 1u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
+      if (rank == 0) {  // every stage that was armed has received both CTAs' bytes
+        for (int s = 0; s < kPairStages; ++s)
+          if (issued & (1u << s))
+            if (!mbar_wait(full + s, (issued_parity >> s) & 1u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
+      }
     }
   } else if (warp == 1) {
-    if (rank == 0) {
+    if (rank == 0 && elect_one()) {
       // ---------------- MMA issuer (even CTA) ----------------
       // Per stage twelve scale copies (nvfp4) and four products, in line: a
       // copy costs 10 cycles of the tensor pipe, a product 130.  Whole stages
-      // take a path without conditions, which are what issuing costs.
-      Walk w;
-      uint32_t done = 0, tiles = 0, set = 0;  // stages and tiles issued; the scale columns in turn
+      // take a path without conditions, as those are what issuing costs.
+      uint32_t stage = 0, phase = 0, tiles = 0;
+      uint32_t set = 0;                    // scale columns, in turn
+      uint32_t late = 0, late_phase = 0;   // the stage whose products last read them
+      uint32_t ahead = 0;                  // stages issued, up to the sets
       const uint32_t ring = smem_u32(smem);
       const uint32_t pair_bits = fp4_idesc(NV, 2, 0, 1) ^ fp4_idesc(NV, 2, 0, 0);
-      for (start(w); w.item < items; next(w)) {
-        // a new tile: the overlap with the last one has been read
-        if (w.kb == 0 && tiles > 0 && !wait(acc_free, (tiles - 1) & 1u)) break;
-        if (!wait(full + w.stage, w.phase)) break;
-        if (done >= kPairSfSets) {  // the products that read this set of scale columns last are complete
-          const uint32_t use = done - kPairSfSets;
-          if (!wait(empty + use % kPairStages, use / kPairStages & 1u)) break;
-        }
-        tc_fence_after();
-        const uint32_t sa = ring + w.stage * kPairStageBytes;
-        const uint32_t ssa = sa + kABytes + kPairBBytes, ssb = ssa + kStageSf;
-        const uint32_t tsa = tmem + kPairSfCol + set * kPairSfStride, tsb = tsa + 16;
+      const int whole = mmas / (kStageK / 64);
+      bool ok = true;
+      for (int64_t item = pair; ok && item < items; item += pairs, ++tiles) {
+        const Tile x = tile_of(item);
+        const uint32_t idesc = fp4_idesc(NV, 2, x.cols, 0);
         const uint32_t acc = tmem + (tiles & 1u) * kAccShift;
-        const uint32_t more = w.kb > 0;
-        const uint64_t adesc = smem_desc_sw128(sa, 16, 1024), bdesc = smem_desc_sw128(sa + kABytes, 16, 1024);
-        const uint32_t idesc = fp4_idesc(NV, 2, w.x.cols, 0);
-        const int m = mmas - w.kb * (kStageK / 64), q = quads - w.kb * kStageQuads;
-        const bool two = w.x.cols > kFp4Band, last = w.kb == kstages - 1;
-        if (elect_one()) {
+        // the overlap with the last tile's accumulator has been read
+        if (tiles > 0 && !(ok = wait(acc_free, (tiles - 1) & 1u))) break;
+        for (int kb = 0; kb < kstages; ++kb) {
+          if (ahead == kPairSfSets) {
+            if (!(ok = wait(empty + late, late_phase))) break;
+            if (++late == kPairStages) {
+              late = 0;
+              late_phase ^= 1u;
+            }
+          } else {
+            ++ahead;
+          }
+          if (!(ok = wait(full + stage, phase))) break;
+          tc_fence_after();
+          const uint32_t sa = ring + stage * kPairStageBytes;
+          const uint32_t ssa = sa + kABytes + kPairBBytes, ssb = ssa + kStageSf;
+          const uint32_t tsa = tmem + kPairSfCol + set * kPairSfStride, tsb = tsa + 16;
+          const uint64_t adesc = smem_desc_sw128(sa, 16, 1024), bdesc = smem_desc_sw128(sa + kABytes, 16, 1024);
           // 64 columns of K are 32 bytes, two units of a descriptor's address
-          if (m >= kStageK / 64) {
+          if (kb < whole) {
 #pragma unroll
             for (int i = 0; i < kStageQuads; ++i) {
               copy_scales<2>(tsa + 4 * i, ssa + i * kFp4TileBytes);
@@ -610,29 +606,29 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int i = 0; i < kStageK / 64; ++i)
               mma_fp4<NV, 2>(acc, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
-                             tsa + i / kQuadMmas * 4, tsb + i / kQuadMmas * 8, i > 0 ? 1u : more);
+                             tsa + i / kQuadMmas * 4, tsb + i / kQuadMmas * 8, i > 0 || kb > 0);
           } else {
+            const int q = quads - kb * kStageQuads, m = mmas - kb * (kStageK / 64);
             for (int i = 0; i < q; ++i) {
               copy_scales<2>(tsa + 4 * i, ssa + i * kFp4TileBytes);
               copy_scales<2>(tsb + 8 * i, ssb + i * kFp4TileBytes);
-              if (two) copy_scales<2>(tsb + 8 * i + 4, ssb + kStageSf + i * kFp4TileBytes);
+              copy_scales<2>(tsb + 8 * i + 4, ssb + kStageSf + i * kFp4TileBytes);
             }
             for (int i = 0; i < m; ++i)
               mma_fp4<NV, 2>(acc, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
-                             tsa + i / kQuadMmas * 4, tsb + i / kQuadMmas * 8, i > 0 ? 1u : more);
+                             tsa + i / kQuadMmas * 4, tsb + i / kQuadMmas * 8, i > 0 || kb > 0);
           }
-          mma_commit_pair(empty + w.stage, 0x3);
-          if (last) mma_commit_pair(acc_full, 0x3);
+          mma_commit_pair(empty + stage, 0x3);
+          set = set == kPairSfSets - 1 ? 0 : set + 1;
+          if (++stage == kPairStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
-        __syncwarp();
-        ++done;
-        set = set == kPairSfSets - 1 ? 0 : set + 1;
-        tiles += last;
+        if (ok) mma_commit_pair(acc_full, 0x3);
       }
-      if (elect_one()) {
-        mma_commit_pair(drain, 0x1);
-        if (!mbar_wait(drain, 0u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
-      }
+      mma_commit_pair(drain, 0x1);
+      if (!mbar_wait(drain, 0u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
     }
   } else {
     // ---------------- epilogue (both CTAs) ----------------
@@ -643,36 +639,40 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint32_t tiles = 0;
     for (int64_t item = pair; item < items; item += pairs, ++tiles) {
       const Tile x = tile_of(item);
-      if (!wait(acc_full, tiles & 1u)) break;
+      int ok = 1;
+      if (lane == 0) ok = wait(acc_full, tiles & 1u);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       tc_fence_after();
-      const float tw = a.wt != nullptr ? a.wt[x.g] : 1.0f, tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
       const int64_t r0 = static_cast<int64_t>(x.wtile) * kPairRows + rank * kRows + quad * 32;
-      OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r0;
       const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (tiles & 1u) * kAccShift;
       // chunks of 32 tokens, those in the overlap first: columns [96, 256) of
       // the first accumulator, [0, 160) of the second
-      const int first = tiles & 1u ? 0 : 3;
-      uint32_t v[3][32];
-      int c[3];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        c[i] = (first + turn + 2 * i) % 8;
-        if (32 * c[i] < x.count) tmem_ld_32x32b_x32(acc + 32 * c[i], v[i]);
-      }
+      const int first = (tiles & 1u ? 0 : 3) + turn;
+      uint32_t v0[32], v1[32], v2[32];
+      tmem_ld_32x32b_x32(acc + first % 8 * 32, v0);
+      tmem_ld_32x32b_x32(acc + (first + 2) % 8 * 32, v1);
+      tmem_ld_32x32b_x32(acc + (first + 4) % 8 * 32, v2);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(acc_free, 0));
+      const Scale k = tile_scale(a, x.g);
+      OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r0;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {  // (rolled: the code of one block stays in the instruction cache)
+        const int c = (first + 2 * i) % 8 * 32;
+        if (c < x.count) store_block(v0, k, out + c * a.ldy, a.ldy, x.count - c, a.rows - r0, vec, stg);
 #pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (32 * c[i] < x.count)
-          store_block(v[i], tw, tx, out + 32 * c[i] * a.ldy, a.ldy, x.count - 32 * c[i], a.rows - r0, vec, stg);
-      const int last = (first + turn + 6) % 8;
-      if (32 * last < x.count) {
-        tmem_ld_32x32b_x32(acc + 32 * last, v[0]);
-        tmem_ld_wait();
-        store_block(v[0], tw, tx, out + 32 * last * a.ldy, a.ldy, x.count - 32 * last, a.rows - r0, vec, stg);
+        for (int j = 0; j < 32; ++j) {
+          v0[j] = v1[j];
+          v1[j] = v2[j];
+        }
+        if (i == 0) {
+          tmem_ld_32x32b_x32(acc + (first + 6) % 8 * 32, v2);
+          tmem_ld_wait();
+        }
       }
+      tc_fence_before();
     }
   }
   tc_fence_before();
