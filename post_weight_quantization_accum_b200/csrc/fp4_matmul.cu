@@ -53,6 +53,7 @@ struct MatmulArgs {
   int n;
   void* y;
   int64_t ldy;
+  int y_tma;  // y can be written by TMA (bf16, rows on 16 bytes)
   int* status;
   uint64_t wait_ns;
 };
@@ -381,53 +382,85 @@ __device__ __forceinline__ Scale tile_scale(const MatmulArgs& a, int g) {
   return {tx, tw};
 }
 
-// 32 features x 32 tokens (v[j]: token j of this lane's feature) to y: through
-// shared memory as rows of 64 bytes (bf16), or straight (fp32: a row of 32
-// lanes is a line).  Only `tokens` rows and `features` lanes exist.
-__device__ __forceinline__ void store_block(uint32_t (&v)[32], Scale k, __nv_bfloat16* out, int64_t ldy, int tokens,
-                                            int64_t features, bool vec, uint8_t* stg) {
-  const int lane = threadIdx.x & 31;
-  if (k.before != 1.0f) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * k.before);
+// A warp's block of 32 features x 32 tokens, from tensor memory to y.  bf16:
+// read as matrix fragments, transposed by stmatrix into rows of 64 bytes (32
+// features of a token, 64-byte swizzle) and written by a TMA store; the end of
+// a group's rows, and a y that TMA cannot address, row by row.  fp32: a lane a
+// feature, each row of 32 lanes a line.
+template <typename OUT>
+struct Block;
+
+struct Out {
+  const CUtensorMap* map;
+  bool tma;
+  uint8_t* stg;      // this warp's 2 KB
+  int64_t ldy;
+};
+
+template <>
+struct Block<__nv_bfloat16> {
+  static __device__ __forceinline__ void load(uint32_t taddr, uint32_t (&v)[32]) {
+    tmem_ld_16x256b_x4(taddr, v);
+    tmem_ld_16x256b_x4(taddr + (16u << 16), v + 16);
   }
-  if (vec && features >= 32) {
-    uint16_t* s = reinterpret_cast<uint16_t*>(stg) + lane;
+  static __device__ __forceinline__ void store(uint32_t (&v)[32], Scale k, const Out& o, __nv_bfloat16* y, int token,
+                                               int feature, int tokens, int64_t features) {
+    const int lane = threadIdx.x & 31;
+    if (k.before != 1.0f) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[j]) * k.k, __uint_as_float(v[j + 1]) * k.k);
-      s[32 * j] = __bfloat16_as_ushort(p.x);
-      s[32 * j + 32] = __bfloat16_as_ushort(p.y);
+      for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * k.before);
     }
-    __syncwarp();
+    uint32_t p[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int tok = 8 * i + lane / 4;
-      if (tok < tokens)
-        *reinterpret_cast<uint4*>(out + tok * ldy + 8 * (lane % 4)) = *reinterpret_cast<const uint4*>(stg + 512 * i + 16 * lane);
+    for (int j = 0; j < 16; ++j) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[2 * j]) * k.k, __uint_as_float(v[2 * j + 1]) * k.k);
+      p[j] = *reinterpret_cast<const uint32_t*>(&b);
     }
+    if (lane == 0) bulk_wait_read();  // the last block's store has read the buffer
     __syncwarp();
-  } else if (lane < features) {
+    const uint32_t at = smem_u32(o.stg) + (lane % 8) * 64;  // row 8 i + lane % 8, matrix (feature eight) lane / 8
+    const uint32_t swz = ((lane / 8) ^ (lane / 2 % 4)) * 16;
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < tokens) out[j * ldy + lane] = __float2bfloat16_rn(__uint_as_float(v[j]) * k.k);
+    for (int i = 0; i < 4; ++i) stmatrix_x4_trans(at + 512 * i + swz, p[2 * i], p[2 * i + 1], p[8 + 2 * i], p[8 + 2 * i + 1]);
+    if (o.tma && tokens >= 32) {
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(o.map, o.stg, feature, token);
+        bulk_commit();
+      }
+    } else {
+      __syncwarp();
+      if (lane < features) {
+        for (int j = 0; j < min(tokens, 32); ++j) {
+          const int chunk = (lane / 8) ^ (j / 2 % 4);
+          y[j * o.ldy + lane] = *reinterpret_cast<const __nv_bfloat16*>(o.stg + 64 * j + 16 * chunk + 2 * (lane % 8));
+        }
+      }
+      __syncwarp();
+    }
   }
-}
-__device__ __forceinline__ void store_block(uint32_t (&v)[32], Scale k, float* out, int64_t ldy, int tokens,
-                                            int64_t features, bool, uint8_t*) {
-  const int lane = threadIdx.x & 31;
-  if (lane < features) {
+};
+
+template <>
+struct Block<float> {
+  static __device__ __forceinline__ void load(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld_32x32b_x32(taddr, v); }
+  static __device__ __forceinline__ void store(uint32_t (&v)[32], Scale k, const Out& o, float* y, int, int, int tokens,
+                                               int64_t features) {
+    const int lane = threadIdx.x & 31;
+    if (lane < features) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < tokens) out[j * ldy + lane] = __uint_as_float(v[j]) * k.before * k.k;
+      for (int j = 0; j < 32; ++j)
+        if (j < tokens) y[j * o.ldy + lane] = __uint_as_float(v[j]) * k.before * k.k;
+    }
   }
-}
+};
 
 template <bool NV, typename OUT>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                     const __grid_constant__ CUtensorMap xwide, const __grid_constant__ CUtensorMap wsmap,
-                    const __grid_constant__ CUtensorMap xsmap, MatmulArgs a) {
+                    const __grid_constant__ CUtensorMap xsmap, const __grid_constant__ CUtensorMap ymap, MatmulArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + size_t(kPairStages) * kPairStageBytes;
@@ -572,13 +605,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const uint32_t ring = smem_u32(smem);
       const uint32_t pair_bits = fp4_idesc(NV, 2, 0, 1) ^ fp4_idesc(NV, 2, 0, 0);
       const int whole = mmas / (kStageK / 64);
+      // the overlap with the last tile's accumulator has been read (waited for
+      // when the new tile's first scales are on their way)
+      auto free_acc = [&](uint32_t tiles) {
+        if (tiles > 0 && !wait(acc_free, (tiles - 1) & 1u)) return false;
+        tc_fence_after();
+        return true;
+      };
       bool ok = true;
       for (int64_t item = pair; ok && item < items; item += pairs, ++tiles) {
         const Tile x = tile_of(item);
         const uint32_t idesc = fp4_idesc(NV, 2, x.cols, 0);
         const uint32_t acc = tmem + (tiles & 1u) * kAccShift;
-        // the overlap with the last tile's accumulator has been read
-        if (tiles > 0 && !(ok = wait(acc_free, (tiles - 1) & 1u))) break;
         for (int kb = 0; kb < kstages; ++kb) {
           if (ahead == kPairSfSets) {
             if (!(ok = wait(empty + late, late_phase))) break;
@@ -603,6 +641,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               copy_scales<2>(tsb + 8 * i, ssb + i * kFp4TileBytes);
               copy_scales<2>(tsb + 8 * i + 4, ssb + kStageSf + i * kFp4TileBytes);  // (for nothing up to 128 tokens)
             }
+            if (kb == 0 && !(ok = free_acc(tiles))) break;
 #pragma unroll
             for (int i = 0; i < kStageK / 64; ++i)
               mma_fp4<NV, 2>(acc, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
@@ -614,6 +653,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               copy_scales<2>(tsb + 8 * i, ssb + i * kFp4TileBytes);
               copy_scales<2>(tsb + 8 * i + 4, ssb + kStageSf + i * kFp4TileBytes);
             }
+            if (kb == 0 && !(ok = free_acc(tiles))) break;
             for (int i = 0; i < m; ++i)
               mma_fp4<NV, 2>(acc, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
                              tsa + i / kQuadMmas * 4, tsb + i / kQuadMmas * 8, i > 0 || kb > 0);
@@ -634,8 +674,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // ---------------- epilogue (both CTAs) ----------------
     const int quad = warp & 3;            // the tensor-memory lanes of this warp
     const int turn = (warp - 2) >> 2;     // which of the two warps with these lanes
-    uint8_t* stg = staging + (warp - 2) * kStageOutBytes;
-    const bool vec = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.ldy * sizeof(OUT) % 16 == 0;
+    const Out o{&ymap, a.y_tma != 0, staging + (warp - 2) * kStageOutBytes, a.ldy};
     uint32_t tiles = 0;
     for (int64_t item = pair; item < items; item += pairs, ++tiles) {
       const Tile x = tile_of(item);
@@ -649,31 +688,33 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       // the first accumulator, [0, 160) of the second
       const int first = (tiles & 1u ? 0 : 3) + turn;
       uint32_t v0[32], v1[32], v2[32];
-      tmem_ld_32x32b_x32(acc + first % 8 * 32, v0);
-      tmem_ld_32x32b_x32(acc + (first + 2) % 8 * 32, v1);
-      tmem_ld_32x32b_x32(acc + (first + 4) % 8 * 32, v2);
+      Block<OUT>::load(acc + first % 8 * 32, v0);
+      Block<OUT>::load(acc + (first + 2) % 8 * 32, v1);
+      Block<OUT>::load(acc + (first + 4) % 8 * 32, v2);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(acc_free, 0));
+      if (lane == 0) mbar_arrive_cluster_relaxed(smem_cluster_addr(acc_free, 0));
       const Scale k = tile_scale(a, x.g);
       OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r0;
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {  // (rolled: the code of one block stays in the instruction cache)
         const int c = (first + 2 * i) % 8 * 32;
-        if (c < x.count) store_block(v0, k, out + c * a.ldy, a.ldy, x.count - c, a.rows - r0, vec, stg);
+        if (c < x.count && r0 < a.rows)
+          Block<OUT>::store(v0, k, o, out + c * a.ldy, x.token + c, static_cast<int>(r0), x.count - c, a.rows - r0);
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           v0[j] = v1[j];
           v1[j] = v2[j];
         }
         if (i == 0) {
-          tmem_ld_32x32b_x32(acc + (first + 6) % 8 * 32, v2);
+          Block<OUT>::load(acc + (first + 6) % 8 * 32, v2);
           tmem_ld_wait();
         }
       }
       tc_fence_before();
     }
+    if (lane == 0) bulk_wait();
   }
   tc_fence_before();
   __syncthreads();
@@ -703,7 +744,7 @@ gptq_status launch_matmul(const CUtensorMap& wmap, const CUtensorMap& xmap, cons
 
 template <bool NV, typename OUT>
 gptq_status launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const CUtensorMap& xwide,
-                        const CUtensorMap& wsmap, const CUtensorMap& xsmap, const MatmulArgs& a, int64_t tiles, const DeviceInfo* info,
+                        const CUtensorMap& wsmap, const CUtensorMap& xsmap, const CUtensorMap& ymap, const MatmulArgs& a, int64_t tiles, const DeviceInfo* info,
                         cudaStream_t st) {
   static std::atomic<bool> attr_set[64] = {};  // per device, shared by host threads
   if (!attr_set[info->device]) {
@@ -715,7 +756,7 @@ gptq_status launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const 
   const int64_t items = tiles * ceil_div(a.rows, kPairRows);
   const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(items, std::max(1, info->sm_count / 2)));
   return launch_cluster_pdl(fp4_pair_kernel<NV, OUT>, grid, kPairThreads, kPairSmemBytes, 2, st, wmap, xmap, xwide, wsmap,
-                            xsmap, a) == cudaSuccess
+                            xsmap, ymap, a) == cudaSuccess
              ? launch_status()
              : GPTQ_ERR_CUDA;
 }
@@ -755,23 +796,28 @@ gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const
   a.n = n;
   a.y = y;
   a.ldy = ldy;
+  a.y_tma = 0;
   a.status = info->status;
   a.wait_ns = wait_limit_ns();
   // token tiles: each group's last one may be part full
   const int64_t tiles = offsets == nullptr ? ceil_div(tokens, kTokens) : tokens / kTokens + std::min<int64_t>(groups, tokens);
   if (tokens > kFp4Band * static_cast<int64_t>(groups)) {
-    CUtensorMap xwide, wsmap, xsmap;
+    CUtensorMap xwide, wsmap, xsmap, ymap = xmap;  // (ymap unused where y_tma is 0)
     const int64_t quads = fp4_quads(n, nv);
     if (!make_tensor_map_2d(&xwide, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, pitch, tokens, pitch, kStageK / 2, kTokens / 2,
                             CU_TENSOR_MAP_SWIZZLE_128B) ||
         !scale_map(&wsmap, wscales, quads, fp4_bands(groups * rows, groups, false), nv, 1) ||
         !scale_map(&xsmap, xscales, quads, offsets != nullptr ? fp4_bands(tokens, groups, true) : ceil_div(tokens, kFp4Band), nv, 2))
       return GPTQ_ERR_CUDA;
+    a.y_tma = y_bf16 && reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy % 8 == 0;
+    if (a.y_tma && !make_tensor_map_2d(&ymap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, rows, tokens, ldy * 2, 32, 32,
+                                       CU_TENSOR_MAP_SWIZZLE_64B))
+      return GPTQ_ERR_CUDA;
     if (nv)
-      return y_bf16 ? launch_pair<true, __nv_bfloat16>(wmap, xmap, xwide, wsmap, xsmap, a, tiles, info, st)
-                    : launch_pair<true, float>(wmap, xmap, xwide, wsmap, xsmap, a, tiles, info, st);
-    return y_bf16 ? launch_pair<false, __nv_bfloat16>(wmap, xmap, xwide, wsmap, xsmap, a, tiles, info, st)
-                  : launch_pair<false, float>(wmap, xmap, xwide, wsmap, xsmap, a, tiles, info, st);
+      return y_bf16 ? launch_pair<true, __nv_bfloat16>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, tiles, info, st)
+                    : launch_pair<true, float>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, tiles, info, st);
+    return y_bf16 ? launch_pair<false, __nv_bfloat16>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, tiles, info, st)
+                  : launch_pair<false, float>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, tiles, info, st);
   }
   const int64_t items = tiles * ceil_div(rows, kRows);
   if (nv)
