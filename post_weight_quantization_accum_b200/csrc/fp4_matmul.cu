@@ -7,16 +7,15 @@
 // scales are multiplied in by the tensor cores (tcgen05.mma .block_scale), the
 // sums are fp32, the tensor scales are multiplied in at the end.
 //
-// Roles are turned round against the usual: the 128 rows of an MMA are rows of
-// W and its N columns are tokens, so that a single token is an MMA of N = 16
-// and every group's last tile only as wide as its tokens, and 32 lanes of an
-// accumulator column are 32 neighbouring outputs of one token.
+// Roles are turned round against the usual: the M rows of an MMA are rows of W
+// and its N columns are tokens, so that a single token is an MMA of N = 16 and
+// every group's last tile only as wide as its tokens.  TMA brings 256 columns
+// of K a stage (128 bytes a row, 128-byte swizzle) and the stage's scale
+// tiles; tcgen05.cp takes those to tensor memory.
 //
-// One CTA a tile of 128 weight rows x up to 256 tokens, persistent over the
-// tiles; TMA brings 256 columns of K a stage (128 bytes a row, 128-byte
-// swizzle), bulk copies bring the stage's scale tiles, tcgen05.cp takes those
-// to tensor memory (each stage has its own columns there, so that no copy
-// meets a product that still reads the last ones).
+// Two kernels: few tokens a group (fp4_stream_kernel, bound by streaming W)
+// and many (fp4_pair_kernel, bound by the tensor cores and the shared memory
+// that feeds them).
 #include <algorithm>
 #include <atomic>
 
@@ -25,20 +24,13 @@
 namespace gptq {
 namespace {
 
-constexpr int kRows = 128;    // weight rows of a tile
-constexpr int kTokens = 256;  // tokens of a tile at most
+constexpr int kRows = 128;    // weight rows of a CTA's tile
+constexpr int kTokens = 256;  // tokens of a pair's tile at most
 constexpr int kStageK = 256;  // columns of K a stage (128 bytes)
-constexpr int kStages = 4;
 constexpr int kBoxRows = 32;  // token rows a TMA box
+constexpr int kBoxBytes = kBoxRows * kStageK / 2;
 constexpr int kABytes = kRows * kStageK / 2;
-constexpr int kBBytes = kTokens * kStageK / 2;
 constexpr int kSfBytes = kStageK / 64 * kFp4TileBytes;  // scales of 128 rows of a stage (nvfp4; half of it with mxfp4)
-constexpr int kStageBytes = kABytes + kBBytes + 3 * kSfBytes;
-constexpr int kThreads = 192;  // producer, MMA, 4 epilogue warps
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSfCol = 256, kSfStride = 64;  // scales of stage s at kSfCol + s * kSfStride: 16 columns of W's, 32 of X's
-constexpr int kTableBytes = 3 * (kFp4MaxGroups + 1) * 4;
-constexpr size_t kSmemBytes = 1024 + size_t(kStages) * kStageBytes + 256 + kTableBytes;
 constexpr uint64_t kDrainNs = 2000000000ull;
 
 struct MatmulArgs {
@@ -102,16 +94,6 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
-__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
 // Waits for a barrier's phase until the limit or until another role of the CTA
 // has given up; the first to run out records the timeout.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag, int* status) {
@@ -129,245 +111,13 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint64_t 
 
 struct Tile {
   int g;
-  int token;   // first token (row of X)
-  int count;   // tokens of the tile
-  int cols;    // MMA columns: count rounded up to 16
+  int token;      // first token (row of X)
+  int count;      // tokens of the tile
+  int cols;       // MMA columns: count rounded up to 16
   int64_t xband;  // first band of X's scales
-  int wtile;   // tile of W's rows in the group
+  int xcol;       // tensor-memory column (32 tokens each) of the first token in that band
+  int wtile;      // tile of W's rows in the group
 };
-
-template <bool NV, typename OUT>
-__global__ void __launch_bounds__(kThreads, 1)
-    fp4_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, MatmulArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + size_t(kStages) * kStageBytes);
-  uint64_t* empty = full + kStages;
-  uint64_t* acc_full = empty + kStages;
-  uint64_t* acc_empty = acc_full + 1;
-  uint64_t* drain = acc_empty + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* table = reinterpret_cast<int*>(smem + size_t(kStages) * kStageBytes + 256);
-  const GroupTable t{table, table + kFp4MaxGroups + 1, table + 2 * (kFp4MaxGroups + 1)};
-
-  const int warp = threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  constexpr int kBlk = NV ? 16 : 32;
-  constexpr int kStageQuads = kStageK / (4 * kBlk);  // scale tiles of a stage along K
-  constexpr int kQuadMmas = kBlk / 16;               // MMAs a scale tile serves
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + s, 1);
-      mbar_init(empty + s, 1);
-    }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 4);
-    mbar_init(drain, 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-    prefetch_tensormap(&wmap);
-    prefetch_tensormap(&xmap);
-  }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  pdl_trigger();
-  pdl_wait();
-  bool ok_groups = true;
-  if (a.offsets != nullptr) {
-    ok_groups = build_groups(t, a.offsets, a.groups, a.tokens, kTokens);
-    if (!ok_groups && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, GPTQ_ERR_INVALID_ARG);
-  } else {
-    if (threadIdx.x == 0) {
-      t.off[0] = t.band[0] = t.tile[0] = 0;
-      t.off[1] = static_cast<int>(a.tokens);
-      t.band[1] = static_cast<int>((a.tokens + kFp4Band - 1) / kFp4Band);
-      t.tile[1] = static_cast<int>((a.tokens + kTokens - 1) / kTokens);
-    }
-    __syncthreads();
-  }
-  const int wtiles = static_cast<int>((a.rows + kRows - 1) / kRows);
-  const int64_t items = ok_groups ? static_cast<int64_t>(t.tile[a.groups]) * wtiles : 0;
-  const int quads = fp4_quads(a.n, NV);
-  const int mmas = (a.n + 63) / 64;
-  const int kstages = (a.n + kStageK - 1) / kStageK;
-
-  auto tile_of = [&](int64_t item) {
-    Tile x;
-    const int tt = static_cast<int>(item / wtiles);
-    x.wtile = static_cast<int>(item - static_cast<int64_t>(tt) * wtiles);
-    x.g = find_group(t.tile, a.groups, tt);
-    const int j = tt - t.tile[x.g];
-    x.token = t.off[x.g] + j * kTokens;
-    x.count = min(kTokens, t.off[x.g + 1] - x.token);
-    x.cols = (x.count + 15) / 16 * 16;
-    x.xband = t.band[x.g] + j * (kTokens / kFp4Band);
-    return x;
-  };
-
-  if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- producer ----------------
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, issued_parity = 0;
-      for (int64_t item = blockIdx.x; item < items && !*abort_flag; item += gridDim.x) {
-        const Tile x = tile_of(item);
-        const int boxes = (x.cols + kBoxRows - 1) / kBoxRows;
-        const int halves = x.cols > kFp4Band ? 2 : 1;
-        const int wy = static_cast<int>(x.g * a.rows) + x.wtile * kRows;
-        const uint8_t* wsc = a.wscales + (static_cast<int64_t>(x.g) * wtiles + x.wtile) * quads * kFp4TileBytes;
-        const uint8_t* xsc = a.xscales + x.xband * quads * kFp4TileBytes;
-        for (int kb = 0; kb < kstages; ++kb) {
-          if (!mbar_wait(empty + stage, phase ^ 1u, a.wait_ns)) {
-            set_status(a.status, GPTQ_ERR_TIMEOUT);
-            *abort_flag = 1;
-            break;
-          }
-          if (*abort_flag) break;
-          uint8_t* sa = smem + size_t(stage) * kStageBytes;
-          uint8_t* sb = sa + kABytes;
-          uint8_t* ssa = sb + kBBytes;
-          uint8_t* ssb = ssa + kSfBytes;
-          const uint32_t sf = static_cast<uint32_t>(min(kStageQuads, quads - kb * kStageQuads) * kFp4TileBytes);
-          const int64_t sf_at = static_cast<int64_t>(kb) * kStageQuads * kFp4TileBytes;
-          mbar_arrive_expect_tx(full + stage, kABytes + boxes * (kBoxRows * kStageK / 2) + (1 + halves) * sf);
-          tma_load_2d(sa, &wmap, full + stage, kb * (kStageK / 2), wy);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(sb + b * (kBoxRows * kStageK / 2), &xmap, full + stage, kb * (kStageK / 2), x.token + b * kBoxRows);
-          bulk_load(ssa, wsc + sf_at, sf, full + stage);
-          for (int h = 0; h < halves; ++h)
-            bulk_load(ssb + h * kSfBytes, xsc + h * static_cast<int64_t>(quads) * kFp4TileBytes + sf_at, sf, full + stage);
-          issued |= 1u << stage;
-          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-      }
-      // every stage that was armed has received its bytes
-      for (int s = 0; s < kStages; ++s)
-        if (issued & (1u << s))
-          if (!mbar_wait(full + s, (issued_parity >> s) & 1u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer ----------------
-      int stage = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x, acc_phase ^= 1u) {
-        const Tile x = tile_of(item);
-        const int halves = x.cols > kFp4Band ? 2 : 1;
-        if (!mbar_wait(acc_empty, acc_phase ^ 1u, a.wait_ns) || *abort_flag) {
-          set_status(a.status, GPTQ_ERR_TIMEOUT);
-          *abort_flag = 1;
-          break;
-        }
-        tc_fence_after();
-        for (int kb = 0; kb < kstages; ++kb) {
-          if (!mbar_wait(full + stage, phase, a.wait_ns) || *abort_flag) {
-            set_status(a.status, GPTQ_ERR_TIMEOUT);
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + size_t(stage) * kStageBytes);
-          const uint32_t sb = sa + kABytes, ssa = sb + kBBytes, ssb = ssa + kSfBytes;
-          const uint32_t tsa = tmem + kSfCol + stage * kSfStride, tsb = tsa + 16;
-          const int q = min(kStageQuads, quads - kb * kStageQuads);
-          for (int i = 0; i < q; ++i) {
-            copy_scales<1>(tsa + 4 * i, ssa + i * kFp4TileBytes);
-            for (int h = 0; h < halves; ++h) copy_scales<1>(tsb + 8 * i + 4 * h, ssb + h * kSfBytes + i * kFp4TileBytes);
-          }
-          const int m = min(kStageK / 64, mmas - kb * (kStageK / 64));
-          for (int i = 0; i < m; ++i) {
-            const int qi = i / kQuadMmas;
-            mma_fp4<NV, 1>(tmem, smem_desc_sw128(sa + 32 * i, 16, 1024), smem_desc_sw128(sb + 32 * i, 16, 1024),
-                        fp4_idesc(NV, 1, x.cols, i % kQuadMmas), tsa + 4 * qi, tsb + 8 * qi, kb > 0 || i > 0);
-          }
-          mma_commit(empty + stage);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-        if (!ok) break;
-        mma_commit(acc_full);
-      }
-      mma_commit(drain);
-      if (!mbar_wait(drain, 0u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
-    }
-  } else {
-    // ---------------- epilogue ----------------
-    const int quad = warp & 3;  // the tensor-memory lanes of this warp
-    uint32_t acc_phase = 0;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x, acc_phase ^= 1u) {
-      const Tile x = tile_of(item);
-      int ok = 1;
-      if (lane == 0) {
-        ok = mbar_wait(acc_full, acc_phase, a.wait_ns) && !*abort_flag;
-        if (!ok) {
-          set_status(a.status, GPTQ_ERR_TIMEOUT);
-          *abort_flag = 1;
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      tc_fence_after();
-      const float tw = a.wt != nullptr ? a.wt[x.g] : 1.0f, tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
-      const int64_t r = static_cast<int64_t>(x.wtile) * kRows + quad * 32 + lane;
-      OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
-      for (int c = 0; c < x.count; c += 32) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, v);
-        tmem_ld_wait();
-        if (r < a.rows) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c + j < x.count) store_out(out + static_cast<int64_t>(c + j) * a.ldy, __uint_as_float(v[j]) * tw * tx);
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty);
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    __syncwarp();
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// The kernel for many tokens: CTA pairs, 256 weight rows x up to 256 tokens
-// ---------------------------------------------------------------------------
-
-constexpr int kPairRows = 256;
-constexpr int kPairStages = 5;
-constexpr int kPairBBytes = kBBytes / 2;  // this CTA's half of the tokens
-constexpr int kPairStageBytes = kABytes + kPairBBytes + 3 * kSfBytes;
-constexpr int kPairEpiWarps = 8;
-constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
-constexpr int kStageOutBytes = 32 * 64;  // a warp's 32 tokens x 32 features in bf16
-constexpr size_t kPairSmemBytes =
-    1024 + size_t(kPairStages) * kPairStageBytes + kPairEpiWarps * kStageOutBytes + 256 + kTableBytes;
-// Tensor memory: two accumulators that overlap in columns [96, 256), and three
-// sets of scales.  The epilogue empties the overlap first.
-constexpr uint32_t kAccShift = 96;
-constexpr uint32_t kPairSfCol = kAccShift + kTokens, kPairSfStride = 48, kPairSfSets = 3;
-static_assert(kPairSfCol + kPairSfSets * kPairSfStride <= kTmemCols, "tensor memory");
 
 // The two tensor scales of a group as factors of its sums: their product, or
 // each in turn where the product would leave the normal numbers.
@@ -381,6 +131,288 @@ __device__ __forceinline__ Scale tile_scale(const MatmulArgs& a, int g) {
   if (k >= 1.17549435e-38f && k <= 3.40282347e38f) return {k, 1.0f};
   return {tx, tw};
 }
+
+__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// One group of all tokens, or the groups of the offsets, in tiles of `width`.
+__device__ __forceinline__ bool group_table(const GroupTable& t, const MatmulArgs& a, int width) {
+  if (a.offsets != nullptr) {
+    const bool ok = build_groups(t, a.offsets, a.groups, a.tokens, width);
+    if (!ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, GPTQ_ERR_INVALID_ARG);
+    return ok;
+  }
+  if (threadIdx.x == 0) {
+    t.off[0] = t.band[0] = t.tile[0] = 0;
+    t.off[1] = static_cast<int>(a.tokens);
+    t.band[1] = static_cast<int>((a.tokens + kFp4Band - 1) / kFp4Band);
+    t.tile[1] = static_cast<int>((a.tokens + width - 1) / width);
+  }
+  __syncthreads();
+  return true;
+}
+
+__device__ __forceinline__ Tile tile_at(const GroupTable& t, const MatmulArgs& a, int wtiles, int width, int64_t item) {
+  Tile x;
+  const int tt = static_cast<int>(item / wtiles);
+  x.wtile = static_cast<int>(item - static_cast<int64_t>(tt) * wtiles);
+  x.g = find_group(t.tile, a.groups, tt);
+  const int first = (tt - t.tile[x.g]) * width;  // of the group's rows
+  x.token = t.off[x.g] + first;
+  x.count = min(width, t.off[x.g + 1] - x.token);
+  x.cols = (x.count + 15) / 16 * 16;
+  x.xband = t.band[x.g] + first / kFp4Band;
+  x.xcol = first % kFp4Band / 32;
+  return x;
+}
+
+// ---------------------------------------------------------------------------
+// The kernel for few tokens: one tile of 128 weight rows x up to `width` tokens
+// a CTA, its K range split over the CTAs of a cluster
+// ---------------------------------------------------------------------------
+//
+// Bound by HBM: each weight is read once (128 * 4096 codes and their scales
+// are 288 KB of nvfp4).  Two CTAs share an SM, so that one streams while the
+// other starts or ends, and a layer with too few row tiles for the chip is cut
+// along K; the cluster's CTAs then add up their sums in rank order through
+// each other's shared memory, so the result does not depend on timing.
+
+constexpr int kStreamThreads = 192;  // producer, MMA, 4 epilogue warps
+constexpr int kStreamMaxStages = 4;
+
+struct StreamShape {
+  int width;   // tokens of a tile: 16, 32, 64 or 128
+  int stages;
+  int splits;  // CTAs of a cluster
+};
+__host__ __device__ inline int stream_stage_bytes(int width) {
+  return kABytes + (width < kBoxRows ? kBoxRows : width) * (kStageK / 2) + 2 * kSfBytes;
+}
+__host__ __device__ inline int table_bytes(int groups) { return 3 * (groups + 1) * 4; }
+
+constexpr size_t kStreamMaxSmem = 1024 + 3 * (2 * kABytes + 2 * kSfBytes) + 128 + 12 * (kFp4MaxGroups + 1);
+
+template <bool NV, typename OUT>
+__global__ void __launch_bounds__(kStreamThreads, 2)
+    fp4_stream_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                      const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap, MatmulArgs a,
+                      StreamShape shape) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int stage_bytes = stream_stage_bytes(shape.width), bbytes = stage_bytes - kABytes - 2 * kSfBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + shape.stages * stage_bytes);
+  uint64_t* empty = full + kStreamMaxStages;
+  uint64_t* acc_full = empty + kStreamMaxStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* table = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 128);
+  const GroupTable t{table, table + a.groups + 1, table + 2 * (a.groups + 1)};
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
+  const int lane = threadIdx.x % 32;
+  constexpr int kBlk = NV ? 16 : 32;
+  constexpr int kStageQuads = kStageK / (4 * kBlk);
+  constexpr int kQuadMmas = kBlk / 16;
+  constexpr uint32_t kStageSf = kStageQuads * kFp4TileBytes;
+  const uint32_t tmem_cols = shape.width + shape.stages * 32 > 128 ? 256 : 128;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < shape.stages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    mbar_init(acc_full, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&wmap);
+    prefetch_tensormap(&xmap);
+    prefetch_tensormap(&wsmap);
+    prefetch_tensormap(&xsmap);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
+  pdl_wait();
+  const bool ok_groups = group_table(t, a, shape.width);
+  const int wtiles = static_cast<int>((a.rows + kRows - 1) / kRows);
+  const int64_t items = ok_groups ? static_cast<int64_t>(t.tile[a.groups]) * wtiles : 0;
+  const int64_t item = blockIdx.x / shape.splits;
+  const int rank = blockIdx.x % shape.splits;  // in the cluster
+  const int quads = fp4_quads(a.n, NV);
+  const int mmas = (a.n + 63) / 64;
+  const int kstages = (a.n + kStageK - 1) / kStageK;
+  const int k0 = kstages * rank / shape.splits, k1 = kstages * (rank + 1) / shape.splits;
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, a.wait_ns, abort_flag, a.status);
+  };
+
+  if (item < items) {
+    const Tile x = tile_at(t, a, wtiles, shape.width, item);
+    if (warp == 0) {
+      if (elect_one()) {
+        // ---------------- producer ----------------
+        const int boxes = (x.cols + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = kABytes + boxes * kBoxBytes + 2 * kStageSf;
+        const int wy = static_cast<int>(x.g * a.rows) + x.wtile * kRows, wband = x.g * wtiles + x.wtile;
+        uint32_t stage = 0, phase = 0;
+        int issued = 0;
+        for (int kb = k0; kb < k1; ++kb, ++issued) {
+          if (!wait(empty + stage, phase ^ 1u)) break;
+          uint8_t* sa = smem + stage * stage_bytes;
+          uint8_t* sf = sa + kABytes + bbytes;
+          mbar_arrive_expect_tx(full + stage, bytes);
+          tma_load_2d(sa, &wmap, full + stage, kb * (kStageK / 2), wy);
+          tma_load_3d(sf, &wsmap, full + stage, 0, kb * kStageQuads, wband);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(sa + kABytes + b * kBoxBytes, &xmap, full + stage, kb * (kStageK / 2), x.token + b * kBoxRows);
+          tma_load_3d(sf + kStageSf, &xsmap, full + stage, 0, kb * kStageQuads, static_cast<int>(x.xband));
+          if (++stage == static_cast<uint32_t>(shape.stages)) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        // every stage that was armed has received its bytes: the last use of each
+        for (int u = max(0, issued - shape.stages); u < issued; ++u)
+          if (!mbar_wait(full + u % shape.stages, u / shape.stages & 1u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
+      }
+    } else if (warp == 1) {
+      if (elect_one()) {
+        // ---------------- MMA issuer ----------------
+        uint32_t stage = 0, phase = 0;
+        const uint32_t ring = smem_u32(smem);
+        const uint32_t idesc = fp4_idesc(NV, 1, x.cols, 0);
+        const uint32_t pair_bits = fp4_idesc(NV, 1, 0, 1) ^ fp4_idesc(NV, 1, 0, 0);
+        const int whole = mmas / (kStageK / 64);
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!wait(full + stage, phase)) break;
+          tc_fence_after();
+          const uint32_t sa = ring + stage * stage_bytes;
+          const uint32_t ssa = sa + kABytes + bbytes, ssb = ssa + kStageSf;
+          // each ring stage has its own scale columns, 16 of W's and 16 of X's:
+          // the stage is full again only after the products that read them
+          const uint32_t tsa = tmem + shape.width + stage * 32, tsb = tsa + 16, tsx = tsb + x.xcol;
+          const uint64_t adesc = smem_desc_sw128(sa, 16, 1024), bdesc = smem_desc_sw128(sa + kABytes, 16, 1024);
+          if (kb < whole) {
+#pragma unroll
+            for (int i = 0; i < kStageQuads; ++i) {
+              copy_scales<1>(tsa + 4 * i, ssa + i * kFp4TileBytes);
+              copy_scales<1>(tsb + 4 * i, ssb + i * kFp4TileBytes);
+            }
+#pragma unroll
+            for (int i = 0; i < kStageK / 64; ++i)
+              mma_fp4<NV, 1>(tmem, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
+                             tsa + i / kQuadMmas * 4, tsx + i / kQuadMmas * 4, i > 0 || kb > k0);
+          } else {
+            const int q = quads - kb * kStageQuads, m = mmas - kb * (kStageK / 64);
+            for (int i = 0; i < q; ++i) {
+              copy_scales<1>(tsa + 4 * i, ssa + i * kFp4TileBytes);
+              copy_scales<1>(tsb + 4 * i, ssb + i * kFp4TileBytes);
+            }
+            for (int i = 0; i < m; ++i)
+              mma_fp4<NV, 1>(tmem, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
+                             tsa + i / kQuadMmas * 4, tsx + i / kQuadMmas * 4, i > 0 || kb > k0);
+          }
+          mma_commit(empty + stage);
+          if (++stage == static_cast<uint32_t>(shape.stages)) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        mma_commit(acc_full);  // (after an abort too: what was issued completes)
+        if (!mbar_wait(acc_full, 0u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
+      }
+    } else {
+      // ---------------- epilogue ----------------
+      const int quad = warp & 3;  // the tensor-memory lanes of this warp
+      int ok = 1;
+      if (lane == 0) ok = wait(acc_full, 0u);
+      ok = __shfl_sync(0xffffffffu, ok, 0) && !*abort_flag;
+      const int64_t r = static_cast<int64_t>(x.wtile) * kRows + quad * 32 + lane;
+      if (ok) {
+        tc_fence_after();
+        const Scale k = tile_scale(a, x.g);
+        OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
+        // (the ring is free: the products that read it are complete)
+        float* sums = reinterpret_cast<float*>(smem) + quad * 32 + lane;
+#pragma unroll 1
+        for (int c = 0; c < x.count; c += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, v);
+          tmem_ld_wait();
+          if (shape.splits > 1) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < x.count) sums[(c + j) * kRows] = __uint_as_float(v[j]);
+          } else if (r < a.rows) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < x.count)
+                store_out(out + static_cast<int64_t>(c + j) * a.ldy, __uint_as_float(v[j]) * k.before * k.k);
+          }
+        }
+        tc_fence_before();
+      }
+    }
+    __syncwarp();
+    if (shape.splits > 1) {
+      cluster_sync_all();
+      // token j's sums over the ranks, in rank order, by rank j % splits.  A
+      // CTA that gave up has no sums: the status word says so.
+      if (warp >= 2) {
+        const int f = threadIdx.x - 64;
+        const int64_t r = static_cast<int64_t>(x.wtile) * kRows + f;
+        const Scale k = tile_scale(a, x.g);
+        OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
+        for (int j = rank; j < x.count; j += shape.splits) {
+          float part[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (q < shape.splits) part[q] = ld_cluster_f32(smem_cluster_addr(smem, q) + (j * kRows + f) * 4);
+          float v = part[0];
+#pragma unroll
+          for (int q = 1; q < 8; ++q)
+            if (q < shape.splits) v += part[q];
+          if (r < a.rows) store_out(out + static_cast<int64_t>(j) * a.ldy, v * k.before * k.k);
+        }
+      }
+      cluster_sync_all();  // no CTA leaves while another reads its sums
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, tmem_cols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The kernel for many tokens: CTA pairs, 256 weight rows x up to 256 tokens
+// ---------------------------------------------------------------------------
+
+constexpr int kPairRows = 256;
+constexpr int kPairStages = 5;
+constexpr int kPairBBytes = kTokens / 2 * kStageK / 2;  // this CTA's half of the tokens
+constexpr int kPairStageBytes = kABytes + kPairBBytes + 3 * kSfBytes;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
+constexpr int kStageOutBytes = 32 * 64;  // a warp's 32 tokens x 32 features in bf16
+constexpr size_t kPairSmemBytes = 1024 + size_t(kPairStages) * kPairStageBytes + kPairEpiWarps * kStageOutBytes + 256;
+// Tensor memory: two accumulators that overlap in columns [96, 256), and three
+// sets of scales (16 columns of W's, 32 of X's).  The epilogue empties the
+// overlap first.
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kAccShift = 96;
+constexpr uint32_t kPairSfCol = kAccShift + kTokens, kPairSfStride = 48, kPairSfSets = 3;
+static_assert(kPairSfCol + kPairSfSets * kPairSfStride <= kTmemCols, "tensor memory");
 
 // A warp's block of 32 features x 32 tokens, from tensor memory to y.  bf16:
 // read as matrix fragments, transposed by stmatrix into rows of 64 bytes (32
@@ -472,7 +504,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* table = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);
-  const GroupTable t{table, table + kFp4MaxGroups + 1, table + 2 * (kFp4MaxGroups + 1)};
+  const GroupTable t{table, table + a.groups + 1, table + 2 * (a.groups + 1)};
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // the same register for the whole warp
   const int lane = threadIdx.x % 32;
@@ -510,19 +542,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = uniform(*tmem_slot);
   pdl_trigger();
   pdl_wait();
-  bool ok_groups = true;
-  if (a.offsets != nullptr) {
-    ok_groups = build_groups(t, a.offsets, a.groups, a.tokens, kTokens);
-    if (!ok_groups && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, GPTQ_ERR_INVALID_ARG);
-  } else {
-    if (threadIdx.x == 0) {
-      t.off[0] = t.band[0] = t.tile[0] = 0;
-      t.off[1] = static_cast<int>(a.tokens);
-      t.band[1] = static_cast<int>((a.tokens + kFp4Band - 1) / kFp4Band);
-      t.tile[1] = static_cast<int>((a.tokens + kTokens - 1) / kTokens);
-    }
-    __syncthreads();
-  }
+  const bool ok_groups = group_table(t, a, kTokens);
   const int wtiles = static_cast<int>((a.rows + kPairRows - 1) / kPairRows);
   const int wbands = static_cast<int>((a.rows + kRows - 1) / kRows);
   const int64_t items = ok_groups ? static_cast<int64_t>(uniform(t.tile[a.groups])) * wtiles : 0;
@@ -530,18 +550,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int mmas = (a.n + 63) / 64;
   const int kstages = (a.n + kStageK - 1) / kStageK;
 
-  auto tile_of = [&](int64_t item) {
-    Tile x;
-    const int tt = static_cast<int>(item / wtiles);
-    x.wtile = static_cast<int>(item - static_cast<int64_t>(tt) * wtiles);
-    x.g = find_group(t.tile, a.groups, tt);
-    const int j = tt - t.tile[x.g];
-    x.token = t.off[x.g] + j * kTokens;
-    x.count = min(kTokens, t.off[x.g + 1] - x.token);
-    x.cols = (x.count + 15) / 16 * 16;
-    x.xband = t.band[x.g] + j * (kTokens / kFp4Band);
-    return x;
-  };
+  auto tile_of = [&](int64_t item) { return tile_at(t, a, wtiles, kTokens, item); };
   // A single thread's wait.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, a.wait_ns, abort_flag, a.status);
@@ -558,7 +567,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int half = x.cols / 2;  // tokens of this CTA
         // one box of 128 rows, or boxes of 32 where that loads no more
         const int boxes = half > 96 ? 0 : (half + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = 2 * (kABytes + (boxes == 0 ? kPairBBytes : boxes * (kBoxRows * kStageK / 2)) + 3 * kStageSf);
+        const uint32_t bytes = 2 * (kABytes + (boxes == 0 ? kPairBBytes : boxes * kBoxBytes) + 3 * kStageSf);
         // the odd CTA's rows may not exist: it then loads the last band's scales for nothing
         const int wband = x.g * wbands + min(2 * x.wtile + static_cast<int>(rank), wbands - 1);
         const int xband = static_cast<int>(x.xband);
@@ -575,7 +584,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             tma_load_2d_pair(sa + kABytes, &xwide, bar, kb * (kStageK / 2), xy);
           else
             for (int b = 0; b < boxes; ++b)
-              tma_load_2d_pair(sa + kABytes + b * (kBoxRows * kStageK / 2), &xmap, bar, kb * (kStageK / 2), xy + b * kBoxRows);
+              tma_load_2d_pair(sa + kABytes + b * kBoxBytes, &xmap, bar, kb * (kStageK / 2), xy + b * kBoxRows);
           tma_load_3d_pair(sa + kABytes + kPairBBytes, &wsmap, bar, 0, kb * kStageQuads, wband);
           tma_load_3d_pair(sa + kABytes + kPairBBytes + kStageSf, &xsmap, bar, 0, kb * kStageQuads, xband);
           issued |= 1u << stage;
@@ -726,36 +735,71 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
 }
 
+// How few tokens are laid out.  Tiles are as wide as the tokens; groups, whose
+// sizes the host does not know, take 64 or 128 (a group's second tile of 64
+// starts at the third scale column of its band; a narrower one would start
+// inside a column).  K is split so that the chip's SMs get about the same
+// number of stages: cost(S) = stages that the busiest SM works off.
+StreamShape stream_shape(int64_t tokens, int groups, bool ragged, int64_t rows, int n, int sms) {
+  StreamShape s;
+  const int64_t each = ragged ? std::max<int64_t>(64, 2 * ceil_div(tokens, groups)) : tokens;
+  s.width = each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : 128;
+  s.stages = s.width <= 32 ? 4 : 3;
+  const int kstages = static_cast<int>(ceil_div(n, kStageK));
+  const int64_t tiles = (ragged ? std::min<int64_t>(groups, tokens) : ceil_div(tokens, s.width)) * ceil_div(rows, kRows);
+  int64_t best = INT64_MAX;
+  s.splits = 1;
+  for (int k = 1; k <= 8 && k <= kstages; ++k) {
+    const int64_t cost = ceil_div(tiles * k, sms) * ceil_div(kstages, k);
+    if (cost < best) {
+      best = cost;
+      s.splits = k;
+    }
+    if (tiles * (k + 1) > 2 * sms) break;  // more would not run side by side
+  }
+  return s;
+}
+
 template <bool NV, typename OUT>
-gptq_status launch_matmul(const CUtensorMap& wmap, const CUtensorMap& xmap, const MatmulArgs& a, int64_t items,
-                          const DeviceInfo* info, cudaStream_t st) {
+gptq_status launch_stream(const CUtensorMap& wmap, const CUtensorMap& xmap, const CUtensorMap& wsmap,
+                          const CUtensorMap& xsmap, const MatmulArgs& a, const DeviceInfo* info, cudaStream_t st) {
   static std::atomic<bool> attr_set[64] = {};  // per device, shared by host threads
   if (!attr_set[info->device]) {
-    if (cudaFuncSetAttribute(fp4_matmul_kernel<NV, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSmemBytes)) != cudaSuccess)
+    if (cudaFuncSetAttribute(fp4_stream_kernel<NV, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kStreamMaxSmem)) != cudaSuccess)
       return GPTQ_ERR_CUDA;
     attr_set[info->device] = true;
   }
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, info->sm_count));
-  if (launch_pdl(fp4_matmul_kernel<NV, OUT>, grid, kThreads, kSmemBytes, st, wmap, xmap, a) != cudaSuccess)
-    return GPTQ_ERR_CUDA;
-  return launch_status();
+  const bool ragged = a.offsets != nullptr;
+  const StreamShape s = stream_shape(a.tokens, a.groups, ragged, a.rows, a.n, info->sm_count);
+  // token tiles: each group's last one may be part full
+  const int64_t tiles = ragged ? a.tokens / s.width + std::min<int64_t>(a.groups, a.tokens) : ceil_div(a.tokens, s.width);
+  const int64_t ctas = tiles * ceil_div(a.rows, kRows) * s.splits;
+  if (ctas > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  const size_t smem = 1024 + static_cast<size_t>(s.stages) * stream_stage_bytes(s.width) + 128 + table_bytes(a.groups);
+  return launch_cluster_pdl(fp4_stream_kernel<NV, OUT>, static_cast<unsigned>(ctas), kStreamThreads, smem, s.splits, st,
+                            wmap, xmap, wsmap, xsmap, a, s) == cudaSuccess
+             ? launch_status()
+             : GPTQ_ERR_CUDA;
 }
 
 template <bool NV, typename OUT>
 gptq_status launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const CUtensorMap& xwide,
-                        const CUtensorMap& wsmap, const CUtensorMap& xsmap, const CUtensorMap& ymap, const MatmulArgs& a, int64_t tiles, const DeviceInfo* info,
+                        const CUtensorMap& wsmap, const CUtensorMap& xsmap, const CUtensorMap& ymap, const MatmulArgs& a, const DeviceInfo* info,
                         cudaStream_t st) {
   static std::atomic<bool> attr_set[64] = {};  // per device, shared by host threads
   if (!attr_set[info->device]) {
     if (cudaFuncSetAttribute(fp4_pair_kernel<NV, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kPairSmemBytes)) != cudaSuccess)
+                             static_cast<int>(kPairSmemBytes + table_bytes(kFp4MaxGroups))) != cudaSuccess)
       return GPTQ_ERR_CUDA;
     attr_set[info->device] = true;
   }
+  const bool ragged = a.offsets != nullptr;
+  // token tiles: each group's last one may be part full
+  const int64_t tiles = ragged ? a.tokens / kTokens + std::min<int64_t>(a.groups, a.tokens) : ceil_div(a.tokens, kTokens);
   const int64_t items = tiles * ceil_div(a.rows, kPairRows);
   const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(items, std::max(1, info->sm_count / 2)));
-  return launch_cluster_pdl(fp4_pair_kernel<NV, OUT>, grid, kPairThreads, kPairSmemBytes, 2, st, wmap, xmap, xwide, wsmap,
+  return launch_cluster_pdl(fp4_pair_kernel<NV, OUT>, grid, kPairThreads, kPairSmemBytes + table_bytes(a.groups), 2, st, wmap, xmap, xwide, wsmap,
                             xsmap, ymap, a) == cudaSuccess
              ? launch_status()
              : GPTQ_ERR_CUDA;
@@ -799,32 +843,33 @@ gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const
   a.y_tma = 0;
   a.status = info->status;
   a.wait_ns = wait_limit_ns();
-  // token tiles: each group's last one may be part full
-  const int64_t tiles = offsets == nullptr ? ceil_div(tokens, kTokens) : tokens / kTokens + std::min<int64_t>(groups, tokens);
-  if (tokens > kFp4Band * static_cast<int64_t>(groups)) {
-    CUtensorMap xwide, wsmap, xsmap, ymap = xmap;  // (ymap unused where y_tma is 0)
-    const int64_t quads = fp4_quads(n, nv);
-    if (!make_tensor_map_2d(&xwide, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, pitch, tokens, pitch, kStageK / 2, kTokens / 2,
-                            CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !scale_map(&wsmap, wscales, quads, fp4_bands(groups * rows, groups, false), nv, 1) ||
-        !scale_map(&xsmap, xscales, quads, offsets != nullptr ? fp4_bands(tokens, groups, true) : ceil_div(tokens, kFp4Band), nv, 2))
-      return GPTQ_ERR_CUDA;
-    a.y_tma = y_bf16 && reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy % 8 == 0;
-    if (a.y_tma && !make_tensor_map_2d(&ymap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, rows, tokens, ldy * 2, 32, 32,
-                                       CU_TENSOR_MAP_SWIZZLE_64B))
-      return GPTQ_ERR_CUDA;
+  const int64_t quads = fp4_quads(n, nv);
+  const int64_t xbands = offsets != nullptr ? fp4_bands(tokens, groups, true) : ceil_div(tokens, kFp4Band);
+  const bool many = tokens > kFp4Band * static_cast<int64_t>(groups);
+  CUtensorMap wsmap, xsmap;
+  if (!scale_map(&wsmap, wscales, quads, fp4_bands(groups * rows, groups, false), nv, 1) ||
+      !scale_map(&xsmap, xscales, quads, xbands, nv, many ? 2 : 1))
+    return GPTQ_ERR_CUDA;
+  if (!many) {
     if (nv)
-      return y_bf16 ? launch_pair<true, __nv_bfloat16>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, tiles, info, st)
-                    : launch_pair<true, float>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, tiles, info, st);
-    return y_bf16 ? launch_pair<false, __nv_bfloat16>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, tiles, info, st)
-                  : launch_pair<false, float>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, tiles, info, st);
+      return y_bf16 ? launch_stream<true, __nv_bfloat16>(wmap, xmap, wsmap, xsmap, a, info, st)
+                    : launch_stream<true, float>(wmap, xmap, wsmap, xsmap, a, info, st);
+    return y_bf16 ? launch_stream<false, __nv_bfloat16>(wmap, xmap, wsmap, xsmap, a, info, st)
+                  : launch_stream<false, float>(wmap, xmap, wsmap, xsmap, a, info, st);
   }
-  const int64_t items = tiles * ceil_div(rows, kRows);
+  CUtensorMap xwide, ymap = xmap;  // (ymap unused where y_tma is 0)
+  if (!make_tensor_map_2d(&xwide, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, pitch, tokens, pitch, kStageK / 2, kTokens / 2,
+                          CU_TENSOR_MAP_SWIZZLE_128B))
+    return GPTQ_ERR_CUDA;
+  a.y_tma = y_bf16 && reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy % 8 == 0;
+  if (a.y_tma && !make_tensor_map_2d(&ymap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, rows, tokens, ldy * 2, 32, 32,
+                                     CU_TENSOR_MAP_SWIZZLE_64B))
+    return GPTQ_ERR_CUDA;
   if (nv)
-    return y_bf16 ? launch_matmul<true, __nv_bfloat16>(wmap, xmap, a, items, info, st)
-                  : launch_matmul<true, float>(wmap, xmap, a, items, info, st);
-  return y_bf16 ? launch_matmul<false, __nv_bfloat16>(wmap, xmap, a, items, info, st)
-                : launch_matmul<false, float>(wmap, xmap, a, items, info, st);
+    return y_bf16 ? launch_pair<true, __nv_bfloat16>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st)
+                  : launch_pair<true, float>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st);
+  return y_bf16 ? launch_pair<false, __nv_bfloat16>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st)
+                : launch_pair<false, float>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st);
 }
 
 }  // namespace gptq
