@@ -27,7 +27,8 @@
  * (knowledge note, "Common Confusions"), gptq_dequant_matvec (inference with
  * the packed weights), gptq2d_round (GPTQ-2D, the two-sided task of the
  * GPTQ-2D abstract on the "Daily Papers" page) and the 4-bit floating-point
- * operators: gptq_fp4_quantize, gptq_fp4_matmul, gptq_fp4_grouped_matmul.
+ * operators: gptq_fp4_quantize, gptq_fp4_matmul, gptq_fp4_grouped_matmul and
+ * gptq_fp4_linear, which chains them.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -490,7 +491,8 @@ gptq_status gptq_fp4_quantize(const void* X, gptq_dtype xdt, int64_t x_rows, int
  *   y            [tokens, ldy] (ydt = GPTQ_F32 or GPTQ_BF16), first `rows`
  *                columns written, ldy >= rows
  * Packed and scales 16-byte aligned.  Deterministic; asynchronous on `stream`.
- * Errors: GPTQ_ERR_INVALID_ARG before any launch; GPTQ_ERR_CUDA. */
+ * Errors: GPTQ_ERR_INVALID_ARG before any launch, GPTQ_ERR_UNSUPPORTED for more
+ * tiles than a grid or a TMA dimension has, GPTQ_ERR_CUDA. */
 gptq_status gptq_fp4_matmul(gptq_fp4_format format, const uint8_t* w_packed, const uint8_t* w_scales, const float* w_tensor,
                             int64_t rows, int32_t n, const uint8_t* x_packed, const uint8_t* x_scales, const float* x_tensor,
                             int64_t tokens, void* y, gptq_dtype ydt, int64_t ldy, void* stream);
@@ -508,6 +510,26 @@ gptq_status gptq_fp4_grouped_matmul(gptq_fp4_format format, const uint8_t* w_pac
                                     int32_t groups, int64_t rows, int32_t n, const uint8_t* x_packed, const uint8_t* x_scales,
                                     const float* x_tensor, int64_t tokens, const int32_t* offsets, void* y, gptq_dtype ydt,
                                     int64_t ldy, void* stream);
+
+/* Bytes of workspace gptq_fp4_linear needs; 0 for sizes that are refused. */
+size_t gptq_fp4_linear_workspace_size(int64_t tokens, int32_t n, gptq_fp4_format format, int32_t groups,
+                                      int32_t ragged);
+
+/* gptq_fp4_quantize of X followed by the product with W, in one call: what a
+ * 4-bit layer does at inference.  The quantised X lives in the workspace.
+ *   w_packed, w_scales, w_tensor, groups, rows, n  W, as for the products
+ *   X, xdt, x_rows, ldx, row_index  as in gptq_fp4_quantize, `tokens` rows
+ *   offsets      NULL: groups == 1, every token with the one W; else the
+ *                tokens' groups, as in gptq_fp4_grouped_matmul
+ *   x_tensor     fp32 [groups] tensor scales of X to use, or NULL to make them
+ *   y, ydt, ldy  as for the products
+ *   ws           gptq_fp4_linear_workspace_size bytes, 256-byte aligned
+ * The result is that of the two calls, bit for bit.  Errors as theirs. */
+gptq_status gptq_fp4_linear(gptq_fp4_format format, const uint8_t* w_packed, const uint8_t* w_scales,
+                            const float* w_tensor, int32_t groups, int64_t rows, int32_t n, const void* X,
+                            gptq_dtype xdt, int64_t x_rows, int64_t ldx, const int32_t* row_index, int64_t tokens,
+                            const int32_t* offsets, const float* x_tensor, void* y, gptq_dtype ydt, int64_t ldy,
+                            void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

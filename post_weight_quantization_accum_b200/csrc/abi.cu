@@ -464,6 +464,21 @@ gptq_status check_product(gptq_fp4_format format, const uint8_t* w_packed, const
   if (nv != (w_tensor != nullptr) || nv != (x_tensor != nullptr) || !aligned(w_tensor, 4) || !aligned(x_tensor, 4)) return GPTQ_ERR_INVALID_ARG;
   return GPTQ_OK;
 }
+
+// The workspace of gptq_fp4_linear: codes, then (each on 256 bytes) scales,
+// tensor scales and the quantiser's own.
+struct LinearLayout {
+  size_t scales, tensor, partial, total;
+};
+LinearLayout linear_layout(int64_t tokens, int n, bool nv, int groups, bool ragged) {
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  LinearLayout l;
+  l.scales = up(static_cast<size_t>(tokens) * fp4_pitch(n));
+  l.tensor = l.scales + up(static_cast<size_t>(fp4_bands(tokens, groups, ragged)) * fp4_quads(n, nv) * kFp4TileBytes);
+  l.partial = l.tensor + up(static_cast<size_t>(groups) * 4);
+  l.total = l.partial + up(fp4_quantize_workspace_size(tokens, n, nv, groups, ragged));
+  return l;
+}
 }  // namespace
 
 extern "C" {
@@ -524,6 +539,41 @@ gptq_status gptq_fp4_grouped_matmul(gptq_fp4_format format, const uint8_t* w_pac
   if (s != GPTQ_OK || rows == 0 || tokens == 0) return s;
   if (offsets == nullptr || !aligned(offsets, 4)) return GPTQ_ERR_INVALID_ARG;
   return fp4_matmul(format == GPTQ_NVFP4, w_packed, w_scales, w_tensor, groups, rows, n, x_packed, x_scales, x_tensor, tokens, offsets, y,
+                    ydt == GPTQ_BF16 ? 1 : 0, ldy, as_stream(stream));
+}
+
+size_t gptq_fp4_linear_workspace_size(int64_t tokens, int32_t n, gptq_fp4_format format, int32_t groups,
+                                      int32_t ragged) {
+  if (tokens < 0 || tokens > kMaxFp4Rows || n < 1 || n > kMaxN || !valid_format(format) ||
+      !valid_groups(tokens, groups, ragged != 0) || (ragged == 0 && groups != 1))
+    return 0;
+  return linear_layout(tokens, n, format == GPTQ_NVFP4, groups, ragged != 0).total;
+}
+
+gptq_status gptq_fp4_linear(gptq_fp4_format format, const uint8_t* w_packed, const uint8_t* w_scales,
+                            const float* w_tensor, int32_t groups, int64_t rows, int32_t n, const void* X,
+                            gptq_dtype xdt, int64_t x_rows, int64_t ldx, const int32_t* row_index, int64_t tokens,
+                            const int32_t* offsets, const float* x_tensor, void* y, gptq_dtype ydt, int64_t ldy,
+                            void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_format(format) || tokens < 0 || tokens > kMaxFp4Rows || n < 1 || n > kMaxN ||
+      !valid_groups(tokens, groups, offsets != nullptr) || (offsets == nullptr && groups != 1) ||
+      (format == GPTQ_MXFP4 && x_tensor != nullptr))
+    return GPTQ_ERR_INVALID_ARG;
+  const bool nv = format == GPTQ_NVFP4;
+  const LinearLayout l = linear_layout(tokens, n, nv, groups, offsets != nullptr);
+  if (tokens > 0 && rows > 0 && (ws == nullptr || !aligned(ws, 256) || ws_bytes < l.total)) return GPTQ_ERR_INVALID_ARG;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  uint8_t* xq = base;
+  uint8_t* xs = base + l.scales;
+  float* xt = !nv ? nullptr : x_tensor != nullptr ? const_cast<float*>(x_tensor) : reinterpret_cast<float*>(base + l.tensor);
+  // every argument is checked before the first launch
+  const gptq_status s = check_product(format, w_packed, w_scales, w_tensor, groups, rows, n, xq, xs, xt, tokens, y, ydt, ldy);
+  if (s != GPTQ_OK || rows == 0 || tokens == 0) return s;
+  const gptq_status q = gptq_fp4_quantize(X, xdt, x_rows, n, ldx, row_index, tokens, offsets, groups, format,
+                                          x_tensor != nullptr ? 1 : 0, xt, xq, xs, nullptr, base + l.partial,
+                                          l.total - l.partial, stream);
+  if (q != GPTQ_OK) return q;
+  return fp4_matmul(nv, w_packed, w_scales, w_tensor, groups, rows, n, xq, xs, xt, tokens, offsets, y,
                     ydt == GPTQ_BF16 ? 1 : 0, ldy, as_stream(stream));
 }
 

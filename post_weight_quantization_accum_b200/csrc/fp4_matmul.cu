@@ -135,6 +135,31 @@ __device__ __forceinline__ Scale tile_scale(const MatmulArgs& a, int g) {
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Four features of a token, of which `left` exist.
+__device__ __forceinline__ void store_four(float* p, float4 v, Scale k, bool vec, int64_t left) {
+  const float4 o = make_float4(v.x * k.before * k.k, v.y * k.before * k.k, v.z * k.before * k.k, v.w * k.before * k.k);
+  if (vec) {
+    *reinterpret_cast<float4*>(p) = o;
+  } else {
+    if (left > 0) p[0] = o.x;
+    if (left > 1) p[1] = o.y;
+    if (left > 2) p[2] = o.z;
+    if (left > 3) p[3] = o.w;
+  }
+}
+__device__ __forceinline__ void store_four(__nv_bfloat16* p, float4 v, Scale k, bool vec, int64_t left) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * k.before * k.k, v.y * k.before * k.k);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.z * k.before * k.k, v.w * k.before * k.k);
+  if (vec) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    if (left > 0) p[0] = a.x;
+    if (left > 1) p[1] = a.y;
+    if (left > 2) p[2] = b.x;
+    if (left > 3) p[3] = b.y;
+  }
+}
+
 // One group of all tokens, or the groups of the offsets, in tiles of `width`.
 __device__ __forceinline__ bool group_table(const GroupTable& t, const MatmulArgs& a, int width) {
   if (a.offsets != nullptr) {
@@ -363,23 +388,37 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     __syncwarp();
     if (shape.splits > 1) {
       cluster_sync_all();
-      // token j's sums over the ranks, in rank order, by rank j % splits.  A
-      // CTA that gave up has no sums: the status word says so.
+      // A token's sums over the ranks, in rank order: a warp a token, a lane
+      // four features, four tokens in flight.  A CTA that gave up has no sums:
+      // the status word says so.
       if (warp >= 2) {
-        const int f = threadIdx.x - 64;
-        const int64_t r = static_cast<int64_t>(x.wtile) * kRows + f;
+        const int64_t r = static_cast<int64_t>(x.wtile) * kRows + 4 * lane;
         const Scale k = tile_scale(a, x.g);
         OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
-        for (int j = rank; j < x.count; j += shape.splits) {
-          float part[8];
+        const bool vec = r + 4 <= a.rows && a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+        uint32_t peer[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (q < shape.splits) part[q] = ld_cluster_f32(smem_cluster_addr(smem, q) + (j * kRows + f) * 4);
-          float v = part[0];
+        for (int q = 0; q < 8; ++q) peer[q] = smem_cluster_addr(smem, min(q, shape.splits - 1)) + 16 * lane;
+        const int step = 4 * shape.splits;  // the cluster's epilogue warps
+        for (int j0 = 4 * rank + warp - 2; j0 < x.count; j0 += 4 * step) {
+          float4 v[4];
 #pragma unroll
-          for (int q = 1; q < 8; ++q)
-            if (q < shape.splits) v += part[q];
-          if (r < a.rows) store_out(out + static_cast<int64_t>(j) * a.ldy, v * k.before * k.k);
+          for (int u = 0; u < 4; ++u)
+            if (j0 + u * step < x.count) v[u] = ld_cluster_f32x4(peer[0] + (j0 + u * step) * kRows * 4);
+#pragma unroll
+          for (int q = 1; q < 8; ++q) {
+            if (q < shape.splits) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (j0 + u * step < x.count) {
+                  const float4 p = ld_cluster_f32x4(peer[q] + (j0 + u * step) * kRows * 4);
+                  v[u] = make_float4(v[u].x + p.x, v[u].y + p.y, v[u].z + p.z, v[u].w + p.w);
+                }
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (j0 + u * step < x.count) store_four(out + static_cast<int64_t>(j0 + u * step) * a.ldy, v[u], k, vec, a.rows - r);
         }
       }
       cluster_sync_all();  // no CTA leaves while another reads its sums

@@ -6,6 +6,10 @@ rows x 4 blocks), ``tensor_scale`` fp32 [groups] ("nvfp4") or None ("mxfp4"),
 and the plain values ``rows``, ``n``, ``format``, ``groups``.  include/gptq.h
 defines the formats and layouts; the functions here check arguments, get
 outputs and workspaces from torch and call the library.
+
+A call runs on ``stream`` or, without one, on the current stream of the
+tensors' device (which need not be the current device); outputs belong to that
+stream.
 """
 import torch
 
@@ -15,34 +19,25 @@ FP4_FORMATS = {"mxfp4": GPTQ_MXFP4, "nvfp4": GPTQ_NVFP4}
 FP4_BLOCK = {"mxfp4": 32, "nvfp4": 16}
 MAX_GROUPS = 512  # of an offsets tensor
 _DTYPES = {torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16}
+# the handle of a device's current stream, without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-class _Place:
-    """Makes the tensors' device and the stream current while outputs are
-    allocated and the library is called; ``where`` is the stream's handle."""
-
-    def __init__(self, device, stream):
-        self.guard = None
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            self.guard = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        self.where = torch.cuda.current_stream().cuda_stream
-        return self
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+def _on(device, stream, call):
+    """call(handle) with the tensors' device and the stream current, so that
+    what it allocates belongs to them."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, not on {device}")
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return call(_raw_stream(device.index))
+    return call(_raw_stream(device.index))
 
 
 def _need(ok, why):
@@ -54,14 +49,21 @@ def _vector(t, name, dtype, length, device):
     """An argument that is a contiguous vector (length None: any)."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    _need(t.dim() == 1 and t.is_contiguous() and (length is None or t.numel() == length),
-          f"{name} must be a contiguous vector{'' if length is None else f' of {length}'}, got {tuple(t.shape)}")
-    _need(t.device == device, f"{name} is on {t.device}, the other tensors on {device}")
+    if t.dim() != 1 or not t.is_contiguous() or (length is not None and t.shape[0] != length):
+        raise ValueError(f"{name} must be a contiguous vector{'' if length is None else f' of {length}'}, "
+                         f"got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
 
 
 def _check_format(format):
     if format not in FP4_FORMATS:
         raise ValueError(f"format must be one of {sorted(FP4_FORMATS)}, got {format!r}")
+
+
+def _bands(rows, groups, ragged):
+    """Bands of 128 rows that the scales need (ragged: for any offsets)."""
+    return rows // 128 + groups if ragged else groups * ((rows // groups + 127) // 128)
 
 
 def fp4_check_quantize_args(X, format, tensor_scale=None, row_index=None, offsets=None):
@@ -70,37 +72,50 @@ def fp4_check_quantize_args(X, format, tensor_scale=None, row_index=None, offset
     _check_format(format)
     if X.dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {X.dtype}: fp32 or bf16")
-    _need(X.dim() in (2, 3), f"X must be [rows, n] or [groups, rows, n], got {tuple(X.shape)}")
-    _need(1 <= X.shape[-1] <= 65535, f"X must have 1 to 65535 columns, got {X.shape[-1]}")
-    if X.dim() == 3:
+    shape = X.shape
+    if len(shape) not in (2, 3):
+        raise ValueError(f"X must be [rows, n] or [groups, rows, n], got {tuple(shape)}")
+    if not 1 <= shape[-1] <= 65535:
+        raise ValueError(f"X must have 1 to 65535 columns, got {shape[-1]}")
+    if len(shape) == 3:
         _need(X.is_contiguous(), "a stack of matrices must be contiguous")
         _need(row_index is None and offsets is None, "row_index and offsets go with a matrix, not with a stack")
-        _need(X.shape[0] >= 1, "a stack needs at least one matrix")
-        rows, groups = X.shape[0] * X.shape[1], X.shape[0]
+        _need(shape[0] >= 1, "a stack needs at least one matrix")
+        rows, groups = shape[0] * shape[1], shape[0]
     else:
-        _need(X.stride(1) == 1 or X.shape[1] == 1, "X's rows must be contiguous")
-        _need(X.stride(0) >= X.shape[1] or X.shape[0] <= 1, "X's rows must not overlap")
-        rows, groups = X.shape[0], 1
+        if not X.is_contiguous():
+            _need(X.stride(1) == 1 or shape[1] == 1, "X's rows must be contiguous")
+            _need(X.stride(0) >= shape[1] or shape[0] <= 1, "X's rows must not overlap")
+        rows, groups = shape[0], 1
+    device = X.device
     if row_index is not None:
-        _vector(row_index, "row_index", torch.int32, None, X.device)
-        rows = row_index.numel()
+        _vector(row_index, "row_index", torch.int32, None, device)
+        rows = row_index.shape[0]
     if offsets is not None:
-        _vector(offsets, "offsets", torch.int32, None, X.device)
-        groups = offsets.numel() - 1
-        _need(1 <= groups <= MAX_GROUPS, f"offsets must have 2 to {MAX_GROUPS + 1} entries, got {offsets.numel()}")
+        _vector(offsets, "offsets", torch.int32, None, device)
+        groups = offsets.shape[0] - 1
+        if not 1 <= groups <= MAX_GROUPS:
+            raise ValueError(f"offsets must have 2 to {MAX_GROUPS + 1} entries, got {groups + 1}")
     if tensor_scale is not None:
         _need(format == "nvfp4", "mxfp4 has no tensor scale")
-        _vector(tensor_scale, "tensor_scale", torch.float32, groups, X.device)
+        _vector(tensor_scale, "tensor_scale", torch.float32, groups, device)
     return rows, groups
 
 
-def _output(out, name, shape, dtype, device):
-    t = out.get(name)
+def _output(X, out, name, shape, dtype):
+    t = out.get(name) if out else None
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous() and t.device == device,
-          f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+        return X.new_empty(shape, dtype=dtype)
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != X.device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {X.device}")
     return t
+
+
+def _aligned(ws, nbytes):
+    """(pointer, bytes) of the 256-byte aligned part of a workspace tensor."""
+    p = ws.data_ptr()
+    a = (p + 255) & ~255
+    return a, ws.numel() * ws.element_size() - (a - p)
 
 
 def gptq_fp4_quantize(X, format="nvfp4", tensor_scale=None, row_index=None, offsets=None, want_deq=False, out=None,
@@ -115,127 +130,169 @@ def gptq_fp4_quantize(X, format="nvfp4", tensor_scale=None, row_index=None, offs
     the rows' own maxima.  out: dict of outputs to write into.
     """
     rows, groups = fp4_check_quantize_args(X, format, tensor_scale, row_index, offsets)
-    dev = X.device
-    _need(dev.type == "cuda", f"X must be on a CUDA device, not on {dev}")
-    n, code, ragged = X.shape[-1], FP4_FORMATS[format], offsets is not None
-    nv = format == "nvfp4"
-    out = out or {}
+    shape, ragged, code = X.shape, offsets is not None, FP4_FORMATS[format]
+    n = shape[-1]
     block = 4 * FP4_BLOCK[format]
-    size = rows // groups
-    bands = rows // 128 + groups if ragged else groups * ((size + 127) // 128)
-    x_rows, ldx = (rows, n) if X.dim() == 3 else (X.shape[0], max(X.stride(0), n))
-    with _Place(dev, stream) as place:
-        q = {"packed": _output(out, "packed", (rows, 16 * ((n + 31) // 32)), torch.uint8, dev),
-             "scales": _output(out, "scales", (bands, (n + block - 1) // block, 512), torch.uint8, dev),
-             "tensor_scale": None, "rows": rows, "n": n, "format": format, "groups": groups}
-        if nv:
-            q["tensor_scale"] = tensor_scale if tensor_scale is not None else _output(
-                out, "tensor_scale", (groups,), torch.float32, dev)
-        if want_deq:
-            q["deq"] = _output(out, "deq", (rows, n), torch.float32, dev)
-        wp, wbytes = None, 0
-        if nv and tensor_scale is None:
-            wbytes = LIB.gptq_fp4_quantize_workspace_size(rows, n, code, groups, int(ragged))
+    stack = len(shape) == 3
+    x_rows, ldx = (rows, n) if stack else (shape[0], max(X.stride(0), n))
+
+    def call(where):
+        packed = _output(X, out, "packed", (rows, 16 * ((n + 31) // 32)), torch.uint8)
+        scales = _output(X, out, "scales", (_bands(rows, groups, ragged), (n + block - 1) // block, 512), torch.uint8)
+        t, wp, wbytes, deq = tensor_scale, None, 0, None
+        q = {"packed": packed, "scales": scales, "tensor_scale": t, "rows": rows, "n": n, "format": format,
+             "groups": groups}
+        if code == GPTQ_NVFP4 and t is None:
+            q["tensor_scale"] = t = _output(X, out, "tensor_scale", (groups,), torch.float32)
+            wbytes = LIB.gptq_fp4_quantize_workspace_size(rows, n, code, groups, ragged)
             if wbytes > 0:
-                ws = ws if ws is not None else torch.empty(wbytes + 256, dtype=torch.uint8, device=dev)
-                wp = (ws.data_ptr() + 255) & ~255
-                wbytes = ws.numel() - (wp - ws.data_ptr())
+                keep = ws if ws is not None else X.new_empty((wbytes + 256,), dtype=torch.uint8)
+                wp, wbytes = _aligned(keep, wbytes)
+        if want_deq:
+            q["deq"] = deq = _output(X, out, "deq", (rows, n), torch.float32)
         check("gptq_fp4_quantize",
-              LIB.gptq_fp4_quantize(_ptr(X), _DTYPES[X.dtype], x_rows, n, ldx, _ptr(row_index), rows, _ptr(offsets),
-                                    groups, code, int(tensor_scale is not None), _ptr(q["tensor_scale"]),
-                                    _ptr(q["packed"]), _ptr(q["scales"]), _ptr(q.get("deq")), wp, wbytes,
-                                    place.where))
-    return q
+              LIB.gptq_fp4_quantize(X.data_ptr(), _DTYPES[X.dtype], x_rows, n, ldx,
+                                    None if row_index is None else row_index.data_ptr(), rows,
+                                    None if offsets is None else offsets.data_ptr(), groups, code,
+                                    tensor_scale is not None, None if t is None else t.data_ptr(), packed.data_ptr(),
+                                    scales.data_ptr(), None if deq is None else deq.data_ptr(), wp, wbytes, where))
+        return q
+
+    return _on(X.device, stream, call)
 
 
 def fp4_check_matrix(q, name, ragged=False):
     """That the dict q holds a quantised matrix as include/gptq.h lays it out
     (ragged: its groups came from offsets)."""
-    missing = [k for k in ("packed", "scales", "tensor_scale", "rows", "n", "format", "groups") if k not in q]
-    _need(not missing, f"{name} is no quantised matrix: it lacks {missing}")
-    _check_format(q["format"])
-    rows, n, groups = q["rows"], q["n"], q["groups"]
-    block = 4 * FP4_BLOCK[q["format"]]
-    p, s, t = q["packed"], q["scales"], q["tensor_scale"]
-    bands = rows // 128 + groups if ragged else groups * ((rows // groups + 127) // 128)
-    _need(ragged or rows % groups == 0, f"{name} has {rows} rows, which is no multiple of its {groups} groups")
+    try:
+        p, s, t, rows, n, format, groups = (q["packed"], q["scales"], q["tensor_scale"], q["rows"], q["n"],
+                                            q["format"], q["groups"])
+    except KeyError as e:
+        raise ValueError(f"{name} is no quantised matrix: it lacks {e}") from None
+    _check_format(format)
+    block = 4 * FP4_BLOCK[format]
+    if not ragged and rows % groups != 0:
+        raise ValueError(f"{name} has {rows} rows, which is no multiple of its {groups} groups")
     if p.dtype != torch.uint8 or s.dtype != torch.uint8:
         raise TypeError(f"{name}'s codes and scales must be uint8")
-    _need(tuple(p.shape) == (rows, 16 * ((n + 31) // 32)) and p.is_contiguous(),
-          f"{name}['packed'] must be contiguous of shape {(rows, 16 * ((n + 31) // 32))}, got {tuple(p.shape)}")
-    _need(s.dim() == 3 and s.shape[0] >= bands and tuple(s.shape[1:]) == ((n + block - 1) // block, 512) and
-          s.is_contiguous(), f"{name}['scales'] must be contiguous of shape {(bands, (n + block - 1) // block, 512)}, "
-                             f"got {tuple(s.shape)}")
-    _need(s.device == p.device, f"{name}'s tensors are on different devices")
-    _need((t is not None) == (q["format"] == "nvfp4"), f"{name}: nvfp4 has tensor scales, mxfp4 none")
+    if p.shape != (rows, 16 * ((n + 31) // 32)) or not p.is_contiguous():
+        raise ValueError(f"{name}['packed'] must be contiguous of shape {(rows, 16 * ((n + 31) // 32))}, "
+                         f"got {tuple(p.shape)}")
+    bands, quads = _bands(rows, groups, ragged), (n + block - 1) // block
+    if s.dim() != 3 or s.shape[0] < bands or s.shape[1:] != (quads, 512) or not s.is_contiguous():
+        raise ValueError(f"{name}['scales'] must be contiguous of shape {(bands, quads, 512)}, got {tuple(s.shape)}")
+    device = p.device
+    if s.device != device:
+        raise ValueError(f"{name}'s tensors are on different devices")
+    if (t is not None) != (format == "nvfp4"):
+        raise ValueError(f"{name}: nvfp4 has tensor scales, mxfp4 none")
     if t is not None:
-        _vector(t, f"{name}['tensor_scale']", torch.float32, groups, p.device)
+        _vector(t, "a matrix's tensor_scale", torch.float32, groups, device)
+
+
+def _check_y(y, dtype, tokens, rows, device):
+    if y is None:
+        if dtype not in _DTYPES:
+            raise TypeError(f"unsupported output dtype {dtype}: fp32 or bf16")
+        return
+    if y.dtype not in _DTYPES:
+        raise TypeError(f"unsupported output dtype {y.dtype}: fp32 or bf16")
+    if (y.shape != (tokens, rows) or (y.stride(1) != 1 and rows != 1) or (y.stride(0) < rows and tokens > 1) or
+            y.device != device):
+        raise ValueError(f"y must be {(tokens, rows)} with contiguous rows on {device}")
 
 
 def _product(w, x, offsets, dtype, y, stream):
     fp4_check_matrix(w, "w")
-    fp4_check_matrix(x, "x", ragged=offsets is not None)
-    _need(w["format"] == x["format"], f"w is {w['format']}, x is {x['format']}")
-    _need(w["n"] == x["n"], f"w has {w['n']} columns, x has {x['n']}")
-    _need(w["groups"] == x["groups"], f"w has {w['groups']} groups, x has {x['groups']}")
-    dev = w["packed"].device
-    _need(x["packed"].device == dev, f"w is on {dev}, x on {x['packed'].device}")
-    groups, tokens = w["groups"], x["rows"]
+    fp4_check_matrix(x, "x", offsets is not None)
+    for key in ("format", "n", "groups"):
+        if w[key] != x[key]:
+            raise ValueError(f"w and x differ in {key}: {w[key]} and {x[key]}")
+    wp, xp, groups, tokens, n = w["packed"], x["packed"], w["groups"], x["rows"], w["n"]
+    if xp.device != wp.device:
+        raise ValueError(f"w is on {wp.device}, x on {xp.device}")
     rows = w["rows"] // groups
-    if y is None:
-        if dtype not in _DTYPES:
-            raise TypeError(f"unsupported output dtype {dtype}: fp32 or bf16")
-    else:
-        if y.dtype not in _DTYPES or (dtype is not None and y.dtype != dtype):
-            raise TypeError(f"unsupported output dtype {y.dtype}")
-        _need(tuple(y.shape) == (tokens, rows) and (y.stride(1) == 1 or rows == 1) and
-              (y.stride(0) >= rows or tokens <= 1) and y.device == dev,
-              f"y must be {(tokens, rows)} with contiguous rows on {dev}")
-    _need(dev.type == "cuda", f"the matrices must be on a CUDA device, not on {dev}")
-    with _Place(dev, stream) as place:
-        if y is None:
-            y = torch.empty((tokens, rows), dtype=dtype, device=dev)
-        ldy = max(y.stride(0), rows)
+    _check_y(y, dtype, tokens, rows, wp.device)
+
+    def call(where):
+        o = y if y is not None else wp.new_empty((tokens, rows), dtype=dtype)
+        wt, xt = w["tensor_scale"], x["tensor_scale"]
+        wt, xt = (None, None) if wt is None else (wt.data_ptr(), xt.data_ptr())
+        ldy = max(o.stride(0), rows)
         if offsets is None:
             check("gptq_fp4_matmul",
-                  LIB.gptq_fp4_matmul(FP4_FORMATS[w["format"]], _ptr(w["packed"]), _ptr(w["scales"]),
-                                      _ptr(w["tensor_scale"]), rows, w["n"], _ptr(x["packed"]), _ptr(x["scales"]),
-                                      _ptr(x["tensor_scale"]), tokens, _ptr(y), _DTYPES[y.dtype], ldy, place.where))
+                  LIB.gptq_fp4_matmul(FP4_FORMATS[w["format"]], wp.data_ptr(), w["scales"].data_ptr(), wt, rows, n,
+                                      xp.data_ptr(), x["scales"].data_ptr(), xt, tokens, o.data_ptr(),
+                                      _DTYPES[o.dtype], ldy, where))
         else:
             check("gptq_fp4_grouped_matmul",
-                  LIB.gptq_fp4_grouped_matmul(FP4_FORMATS[w["format"]], _ptr(w["packed"]), _ptr(w["scales"]),
-                                              _ptr(w["tensor_scale"]), groups, rows, w["n"], _ptr(x["packed"]),
-                                              _ptr(x["scales"]), _ptr(x["tensor_scale"]), tokens, _ptr(offsets),
-                                              _ptr(y), _DTYPES[y.dtype], ldy, place.where))
-    return y
+                  LIB.gptq_fp4_grouped_matmul(FP4_FORMATS[w["format"]], wp.data_ptr(), w["scales"].data_ptr(), wt,
+                                              groups, rows, n, xp.data_ptr(), x["scales"].data_ptr(), xt, tokens,
+                                              offsets.data_ptr(), o.data_ptr(), _DTYPES[o.dtype], ldy, where))
+        return o
+
+    return _on(wp.device, stream, call)
 
 
 def gptq_fp4_matmul(w, x, dtype=torch.float32, y=None, stream=None):
     """y[i, r] = sum_c W[r, c] X[i, c] of two quantised matrices (dicts of
     gptq_fp4_quantize, same format and width): [x rows, w rows] in `dtype`
-    (fp32 or bf16), or written into y."""
-    _need(w.get("groups") == 1, f"w has {w.get('groups')} groups: gptq_fp4_grouped_matmul takes them")
-    return _product(w, x, None, dtype if y is None else None, y, stream)
+    (fp32 or bf16), or written into y in its own."""
+    if w.get("groups") != 1:
+        raise ValueError(f"w has {w.get('groups')} groups: gptq_fp4_grouped_matmul takes them")
+    return _product(w, x, None, dtype, y, stream)
+
+
+def _check_experts(w, offsets):
+    _vector(offsets, "offsets", torch.int32, w["groups"] + 1, w["packed"].device)
+    if w["groups"] > MAX_GROUPS:
+        raise ValueError(f"at most {MAX_GROUPS} groups, w has {w['groups']}")
 
 
 def gptq_fp4_grouped_matmul(w, x, offsets, dtype=torch.float32, y=None, stream=None):
     """The product of each group of x's rows (offsets as x was quantised with)
     with its own matrix of the stack w ([groups, rows, n] quantised): y
     [x rows, rows].  Rows of y outside the offsets are left as they were."""
-    _vector(offsets, "offsets", torch.int32, None, w["packed"].device)
-    _need(offsets.numel() == w["groups"] + 1, f"offsets has {offsets.numel()} entries for {w['groups']} groups")
-    _need(w["groups"] <= MAX_GROUPS, f"at most {MAX_GROUPS} groups, w has {w['groups']}")
-    return _product(w, x, offsets, dtype if y is None else None, y, stream)
+    _check_experts(w, offsets)
+    return _product(w, x, offsets, dtype, y, stream)
 
 
-def fp4_linear(w, X, dtype=None, tensor_scale=None, row_index=None, offsets=None, y=None, stream=None):
+def fp4_linear(w, X, dtype=None, tensor_scale=None, row_index=None, offsets=None, y=None, ws=None, stream=None):
     """A 4-bit layer on X [tokens, n] (fp32 or bf16): X is quantised to w's
     format and multiplied with w, in `dtype` (default: X's).  With offsets (and
     a row_index that gathers the rows), each group of rows goes through its own
-    matrix of the stack w, as a layer of experts does."""
-    x = gptq_fp4_quantize(X, w["format"], tensor_scale=tensor_scale, row_index=row_index, offsets=offsets,
-                          stream=stream)
-    dtype = X.dtype if dtype is None else dtype
-    if offsets is None:
-        return gptq_fp4_matmul(w, x, dtype=dtype, y=y, stream=stream)
-    return gptq_fp4_grouped_matmul(w, x, offsets, dtype=dtype, y=y, stream=stream)
+    matrix of the stack w, as a layer of experts does.  The same result as
+    gptq_fp4_quantize and a product, in one call of the library."""
+    fp4_check_matrix(w, "w")
+    wp, n, groups, format = w["packed"], w["n"], w["groups"], w["format"]
+    if X.dim() != 2 or X.shape[1] != n:
+        raise ValueError(f"X must be [tokens, {n}], got {tuple(X.shape)}")
+    tokens, x_groups = fp4_check_quantize_args(X, format, tensor_scale, row_index, offsets)
+    if offsets is not None:
+        _check_experts(w, offsets)
+    if x_groups != groups:
+        raise ValueError(f"w has {groups} groups: give the rows' offsets")
+    if X.device != wp.device:
+        raise ValueError(f"w is on {wp.device}, X on {X.device}")
+    rows = w["rows"] // groups
+    if dtype is None:
+        dtype = X.dtype
+    _check_y(y, dtype, tokens, rows, wp.device)
+    code = FP4_FORMATS[format]
+
+    def call(where):
+        o = y if y is not None else X.new_empty((tokens, rows), dtype=dtype)
+        nbytes = LIB.gptq_fp4_linear_workspace_size(tokens, n, code, groups, offsets is not None)
+        keep = ws if ws is not None else X.new_empty((nbytes + 256,), dtype=torch.uint8)
+        base, nbytes = _aligned(keep, nbytes)
+        wt = w["tensor_scale"]
+        check("gptq_fp4_linear",
+              LIB.gptq_fp4_linear(code, wp.data_ptr(), w["scales"].data_ptr(), None if wt is None else wt.data_ptr(),
+                                  groups, rows, n, X.data_ptr(), _DTYPES[X.dtype], X.shape[0], max(X.stride(0), n),
+                                  None if row_index is None else row_index.data_ptr(), tokens,
+                                  None if offsets is None else offsets.data_ptr(),
+                                  None if tensor_scale is None else tensor_scale.data_ptr(), o.data_ptr(),
+                                  _DTYPES[o.dtype], max(o.stride(0), rows), base, nbytes, where))
+        return o
+
+    return _on(wp.device, stream, call)
