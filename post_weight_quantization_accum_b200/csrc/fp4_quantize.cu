@@ -7,18 +7,22 @@
 //
 // The quotients are exact: which code is nearest is decided on the real
 // numbers, not on rounded ones.  With mxfp4 dividing by s only moves the
-// exponent.  With nvfp4 the quotient is bracketed: x r_lo <= x / (s t) <= x r_hi
-// with r_lo, r_hi a float or two below and above 1 / (s t), so where both ends
-// convert to the same code (all but about 2^-20 of the values) the code is
+// exponent.  With nvfp4 the quotient is bracketed: x r_lo < x / (s t) < x r_hi
+// with r_lo and r_hi 2^-20 of it below and above 1 / (s t), so where both ends
+// convert to the same code (all but about 2^-19 of the values) the code is
 // certain, and where they do not the exact products b s t of the rounding
-// borders b (at most 31 bits) are compared in 64 bits.
+// borders b (at most 31 bits) are compared in 64 bits.  The scale is decided
+// in the same way.
 //
 // Bound by HBM: per value 2 (bf16) or 4 (fp32) bytes in, 1/2 + 1/B out, and 4
 // with the dequantised values.  A CTA takes a band of 128 rows x 256 columns,
-// a thread a block at a time (its maximum needs no other thread), and the
-// band's scale tiles go out whole from shared memory.
+// a thread a block at a time (its maximum needs no other thread) with the
+// loads of several rows in flight, and the band's scale tiles go out whole
+// from shared memory.
 #include <algorithm>
 #include <cfloat>
+
+#include <cuda_fp16.h>
 
 #include "fp4.cuh"
 
@@ -54,7 +58,7 @@ struct Shape {
   static constexpr int kWords = kBlock * (BF16 ? 2 : 4) / 4;
   static constexpr int kCols = kChunk / kBlock;      // blocks across the tile
   static constexpr int kRowsAtOnce = kThreads / kCols;
-  static constexpr int kIters = kFp4Band / kRowsAtOnce;
+  static constexpr int kBatch = kWords <= 8 ? 4 : 2;  // blocks whose loads are in flight together
 };
 
 __device__ __forceinline__ void load32(const void* p, uint32_t* w) {
@@ -150,21 +154,34 @@ __device__ __forceinline__ int64_t source_row(const QuantArgs& a, int64_t r) {
   return -1;
 }
 
-// Largest finite magnitude of rows [r0, r1), columns [c0, c1), over the CTA.
-template <bool BF16, bool NV>
-__device__ __forceinline__ uint32_t region_max(const QuantArgs& a, int64_t r0, int64_t r1, int c0, int c1, uint32_t* s) {
+// Largest finite magnitude of `count` blocks, block i at the row and column
+// that at(i) gives, over the CTA.
+template <bool BF16, bool NV, typename At>
+__device__ __forceinline__ uint32_t blocks_max(const QuantArgs& a, int count, uint32_t* s, At at) {
   using S = Shape<BF16, NV>;
-  const int across = (c1 - c0 + S::kBlock - 1) / S::kBlock;
+  constexpr int kBatch = 32 / S::kWords * 2;
   uint32_t m = 0;
-  for (int64_t r = r0 + threadIdx.x / S::kCols; r < r1; r += S::kRowsAtOnce) {
-    const int64_t src = source_row(a, r);
-    if (src < 0) continue;
-#pragma unroll 4
-    for (int b = threadIdx.x % S::kCols; b < across; b += S::kCols) {
-      uint32_t w[S::kWords];
-      load_block<BF16, NV>(a, src, c0 + b * S::kBlock, w);
-      m = max(m, finite_max<BF16>(w));
+  for (int i0 = threadIdx.x; i0 < count; i0 += kBatch * kThreads) {
+    uint32_t w[kBatch][S::kWords];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      int64_t src = -1;
+      int col = 0;
+      const int i = i0 + u * kThreads;
+      if (i < count) {
+        int64_t row;
+        at(i, row, col);
+        src = source_row(a, row);
+      }
+      if (src >= 0) {
+        load_block<BF16, NV>(a, src, col, w[u]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < S::kWords; ++k) w[u][k] = 0;
+      }
     }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) m = max(m, finite_max<BF16>(w[u]));
   }
   return cta_max(m, s);
 }
@@ -200,6 +217,25 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
   return c & 8 ? -v : v;
 }
 
+// What eight codes stand for.
+__device__ __forceinline__ void from_e2m1(uint32_t codes, float (&v)[8]) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
 // E4M3 byte nearest to amax / (6 t), decided on amax against the exact product
 // of the border between two neighbours (5 bits) and 6 t (26 bits).
 __device__ __noinline__ uint32_t exact_scale(float amax, float t, uint32_t lo, uint32_t hi) {
@@ -222,10 +258,35 @@ __device__ __noinline__ uint32_t exact_code(float x, float s, float t) {
   return k | (__float_as_uint(x) >> 31) << 3;
 }
 
-struct Unit {  // what a CTA keeps of its group's tensor scale
-  float t, c_lo, c_hi;      // c_lo <= 1 / (6 t) <= c_hi
-  const float2* recip;      // shared: [scale byte] -> (r_lo, r_hi) around 1 / (s t)
+constexpr float kBelow = 1.0f - 0x1p-20f, kAbove = 1.0f + 0x1p-20f;
+
+// What a CTA keeps of its group's tensor scale: about 1 / t and 1 / (6 t), a
+// rounding each.  Outside [2^-100, 2^100] they, or their products with 1 / s,
+// may leave the normal numbers: every decision is then taken in 64 bits.
+struct Unit {
+  float t, rt, c;
+  bool plain;
 };
+__device__ __forceinline__ Unit unit_of(float t) {
+  return {t, __frcp_rn(t), __frcp_rn(__fmul_rn(6.0f, t)), t >= 0x1p-100f && t <= 0x1p100f};
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {  // within an ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// (a, b) * (k, k), as one instruction.
+__device__ __forceinline__ void mul2(float& a, float& b, float x, float y, float k) {
+  asm("{\n\t.reg .b64 p, q;\n\t"
+      "mov.b64 p, {%2, %3};\n\t"
+      "mov.b64 q, {%4, %4};\n\t"
+      "mul.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(a), "=f"(b)
+      : "f"(x), "f"(y), "f"(k));
+}
 
 // One block: codes, scale byte and s (NaN for a block with a value that is not
 // finite: it must not pass for a number, and its codes are zero).
@@ -251,17 +312,21 @@ __device__ __forceinline__ void quantize_block(const uint32_t (&w)[Shape<BF16, N
     for (int i = 0; i < S::kBlock / 8; ++i) {
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = value<BF16>(w, 8 * i + j) * inv;
+      for (int j = 0; j < 8; j += 2) mul2(v[j], v[j + 1], value<BF16>(w, 8 * i + j), value<BF16>(w, 8 * i + j + 1), inv);
       codes[i] = to_e2m1(v);
     }
     return;
   }
   const float amax = __uint_as_float(m);
-  const uint32_t two = to_e4m3x2(__fmul_rd(amax, u.c_lo), __fmul_ru(amax, u.c_hi));
+  // c, two products and a quotient of 24 bits are within 2^-22 of the exact ones
+  const uint32_t two = to_e4m3x2(amax * u.c * kBelow, amax * u.c * kAbove);
   byte = two & 0xff;
-  if (byte != two >> 8) byte = exact_scale(amax, u.t, byte, two >> 8);
+  if (!u.plain)
+    byte = exact_scale(amax, u.t, 0, 126);
+  else if (byte != two >> 8)
+    byte = exact_scale(amax, u.t, byte, two >> 8);
   s = e4m3_value(byte);
-  const float2 r = u.recip[byte];
+  const float r = rcp_approx(s) * u.rt, r_lo = r * kBelow, r_hi = r * kAbove;
   if (byte == 0) {
 #pragma unroll
     for (int i = 0; i < S::kBlock / 8; ++i) codes[i] = 0;
@@ -272,13 +337,13 @@ __device__ __forceinline__ void quantize_block(const uint32_t (&w)[Shape<BF16, N
   for (int i = 0; i < S::kBlock / 8; ++i) {
     float lo[8], hi[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      lo[j] = value<BF16>(w, 8 * i + j) * r.x;
-      hi[j] = value<BF16>(w, 8 * i + j) * r.y;
+    for (int j = 0; j < 8; j += 2) {
+      const float x = value<BF16>(w, 8 * i + j), y = value<BF16>(w, 8 * i + j + 1);
+      mul2(lo[j], lo[j + 1], x, y, r_lo);
+      mul2(hi[j], hi[j + 1], x, y, r_hi);
     }
     codes[i] = to_e2m1(lo);
-    differ[i] = codes[i] ^ to_e2m1(hi);
-    if (!(r.y < FLT_MAX)) differ[i] = 0xffffffffu;  // 1 / (s t) is beyond a float
+    differ[i] = u.plain ? codes[i] ^ to_e2m1(hi) : 0xffffffffu;
     any |= differ[i];
   }
   if (any != 0) {
@@ -335,9 +400,18 @@ __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(QuantArgs a) {
   Band b;
   if (!find_band(a, t, band, b)) return;
   const int chunks = (a.n + kChunk - 1) / kChunk;
-  const int c0 = static_cast<int>(int64_t(chunks) * part / a.splits) * kChunk;
-  const int c1 = min(a.n, static_cast<int>(int64_t(chunks) * (part + 1) / a.splits) * kChunk);
-  const uint32_t m = region_max<BF16, NV>(a, b.r0, b.r0 + b.rows, c0, c1, red);
+  // this part's columns, block by block down the band's rows
+  using S = Shape<BF16, NV>;
+  const int c0 = static_cast<int>(int64_t(chunks) * part / a.splits) * S::kCols;
+  const int c1 = min((a.n + S::kBlock - 1) / S::kBlock, static_cast<int>(int64_t(chunks) * (part + 1) / a.splits) * S::kCols);
+  const int tall = (b.rows + S::kRowsAtOnce - 1) / S::kRowsAtOnce * S::kRowsAtOnce;  // whole strips of rows
+  const int wide = (c1 - c0 + S::kCols - 1) / S::kCols;
+  const uint32_t m = blocks_max<BF16, NV>(a, tall * wide * S::kCols, red, [&](int i, int64_t& row, int& col) {
+    const int strip = i / kThreads, r = strip / wide * S::kRowsAtOnce + i % kThreads / S::kCols;
+    const int c = c0 + strip % wide * S::kCols + i % S::kCols;
+    row = b.r0 + min(r, b.rows - 1);  // (past the ends: the last row or block once more)
+    col = min(c, c1 - 1) * S::kBlock;
+  });
   if (threadIdx.x == 0) a.partial[blockIdx.x] = __uint_as_float(m);
 }
 
@@ -346,7 +420,6 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(QuantArgs a) {
   using S = Shape<BF16, NV>;
   __shared__ int tab[3][kFp4MaxGroups + 1];
   __shared__ uint32_t red[32];
-  __shared__ float2 recip[NV ? 128 : 1];
   __shared__ __align__(16) uint8_t sc[kFp4Band * (kChunk / S::kBlock)];
   const GroupTable t{tab[0], tab[1], tab[2]};
   pdl_trigger();
@@ -365,10 +438,11 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(QuantArgs a) {
   Band b;
   if (!find_band(a, t, band, b)) return;
 
-  Unit u{1.0f, 0.0f, 0.0f, recip};
+  Unit u{1.0f, 1.0f, 1.0f, true};
   if (NV) {
+    float tensor;
     if (a.given) {
-      u.t = a.tensor_scale[b.g];
+      tensor = a.tensor_scale[b.g];
     } else {
       uint32_t m = 0;
       if (a.partial != nullptr) {
@@ -376,20 +450,16 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(QuantArgs a) {
         for (int64_t i = threadIdx.x; i < b.bands * a.splits; i += kThreads) m = max(m, __float_as_uint(p[i]));
         m = cta_max(m, red);
       } else {
-        m = region_max<BF16, NV>(a, b.g0, b.g1, 0, a.n, red);
+        const int across = (a.n + S::kBlock - 1) / S::kBlock;
+        m = blocks_max<BF16, NV>(a, static_cast<int>(b.g1 - b.g0) * across, red, [&](int i, int64_t& row, int& col) {
+          row = b.g0 + i / across;
+          col = i % across * S::kBlock;
+        });
       }
-      u.t = fmaxf(__fdiv_rn(__uint_as_float(m), 2688.0f), FLT_MIN);
-      if (band == b.first && chunk == 0 && threadIdx.x == 0) a.tensor_scale[b.g] = u.t;
+      tensor = fmaxf(__fdiv_rn(__uint_as_float(m), 2688.0f), FLT_MIN);
+      if (band == b.first && chunk == 0 && threadIdx.x == 0) a.tensor_scale[b.g] = tensor;
     }
-    const double c = 1.0 / (6.0 * double(u.t));
-    u.c_lo = __double2float_rd(c * (1.0 - 0x1p-50));
-    u.c_hi = __double2float_ru(c * (1.0 + 0x1p-50));
-    if (threadIdx.x < 127) {
-      // one float further out than the nearest ones: the products x r_lo and
-      // x r_hi are rounded themselves
-      const double r = threadIdx.x > 0 ? 1.0 / (double(e4m3_value(threadIdx.x)) * double(u.t)) : 0.0;
-      recip[threadIdx.x] = make_float2(nextafterf(__double2float_rd(r), 0.0f), nextafterf(__double2float_ru(r), INFINITY));
-    }
+    u = unit_of(tensor);
   }
   for (int i = threadIdx.x; i < int(sizeof(sc)) / 4; i += kThreads) reinterpret_cast<uint32_t*>(sc)[i] = 0;
   __syncthreads();
@@ -397,42 +467,53 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(QuantArgs a) {
   const int cb = threadIdx.x % S::kCols;
   const int col = chunk * kChunk + cb * S::kBlock;
   const int64_t pitch = fp4_pitch(a.n);
+  const bool vec = a.n % 8 == 0 && col + S::kBlock <= a.n && reinterpret_cast<uintptr_t>(a.deq) % 32 == 0;
   if (col / 2 < pitch) {
-    for (int it = 0; it < S::kIters; ++it) {
-      const int r = it * S::kRowsAtOnce + threadIdx.x / S::kCols;
-      if (r >= b.rows) break;
-      const int64_t row = b.r0 + r;
-      const int64_t src = source_row(a, row);
-      uint32_t w[S::kWords];
-      if (src >= 0 && col < a.n) {
-        load_block<BF16, NV>(a, src, col, w);
-      } else {
+    for (int r0 = threadIdx.x / S::kCols; r0 < b.rows; r0 += S::kBatch * S::kRowsAtOnce) {
+      uint32_t w[S::kBatch][S::kWords];
 #pragma unroll
-        for (int i = 0; i < S::kWords; ++i) w[i] = 0;
+      for (int v = 0; v < S::kBatch; ++v) {
+        const int r = r0 + v * S::kRowsAtOnce;
+        const int64_t src = r < b.rows ? source_row(a, b.r0 + r) : -1;
+        if (src >= 0 && col < a.n) {
+          load_block<BF16, NV>(a, src, col, w[v]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < S::kWords; ++i) w[v][i] = 0;
+        }
       }
-      uint32_t codes[S::kBlock / 8], byte;
-      float s;
-      quantize_block<BF16, NV>(w, u, codes, byte, s);
-      uint8_t* dst = a.packed + row * pitch + col / 2;
-      if (NV)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(codes[0], codes[1]);
-      else
-        *reinterpret_cast<uint4*>(dst) = make_uint4(codes[0], codes[1], codes[S::kBlock / 8 - 2], codes[S::kBlock / 8 - 1]);
-      if (col < a.n) sc[cb / 4 * kFp4TileBytes + r % 32 * 16 + r / 32 * 4 + cb % 4] = static_cast<uint8_t>(byte);
-      if (a.deq != nullptr && col < a.n) {
-        float* d = a.deq + row * a.n + col;
-        const bool vec = a.n % 8 == 0 && col + S::kBlock <= a.n && reinterpret_cast<uintptr_t>(a.deq) % 32 == 0;
 #pragma unroll
-        for (int i = 0; i < S::kBlock / 8; ++i) {
-          float v[8];
+      for (int v = 0; v < S::kBatch; ++v) {
+        const int r = r0 + v * S::kRowsAtOnce;
+        if (r >= b.rows) break;
+        const int64_t row = b.r0 + r;
+        uint32_t codes[S::kBlock / 8], byte;
+        float s;
+        quantize_block<BF16, NV>(w[v], u, codes, byte, s);
+        uint8_t* dst = a.packed + row * pitch + col / 2;
+        if (NV)
+          *reinterpret_cast<uint2*>(dst) = make_uint2(codes[0], codes[1]);
+        else
+          *reinterpret_cast<uint4*>(dst) = make_uint4(codes[0], codes[1], codes[S::kBlock / 8 - 2], codes[S::kBlock / 8 - 1]);
+        if (col < a.n) sc[cb / 4 * kFp4TileBytes + r % 32 * 16 + r / 32 * 4 + cb % 4] = static_cast<uint8_t>(byte);
+        if (a.deq != nullptr && col < a.n) {
+          float* d = a.deq + row * a.n + col;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(e2m1_value(codes[i] >> 4 * j & 15) * s, u.t);
-          if (vec) {
-            store32(d + 8 * i, v);
-          } else {
+          for (int i = 0; i < S::kBlock / 8; ++i) {
+            float f[8];
+            from_e2m1(codes[i], f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (col + 8 * i + j < a.n) d[8 * i + j] = v[j];
+            for (int j = 0; j < 8; j += 2) {
+              mul2(f[j], f[j + 1], f[j], f[j + 1], s);
+              if (NV) mul2(f[j], f[j + 1], f[j], f[j + 1], u.t);
+            }
+            if (vec) {
+              store32(d + 8 * i, f);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (col + 8 * i + j < a.n) d[8 * i + j] = f[j];
+            }
           }
         }
       }
