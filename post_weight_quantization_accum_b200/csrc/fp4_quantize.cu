@@ -29,6 +29,9 @@
 namespace gptq {
 namespace {
 
+#ifndef AHEAD
+#define AHEAD 1
+#endif
 constexpr int kThreads = 256;
 constexpr int kChunk = 256;  // columns of a CTA's tile
 
@@ -58,7 +61,7 @@ struct Shape {
   static constexpr int kWords = kBlock * (BF16 ? 2 : 4) / 4;
   static constexpr int kCols = kChunk / kBlock;      // blocks across the tile
   static constexpr int kRowsAtOnce = kThreads / kCols;
-  static constexpr int kBatch = kWords <= 8 ? 4 : 2;  // blocks whose loads are in flight together
+  static constexpr int kAhead = AHEAD;  // blocks a thread loads before it needs them
 };
 
 __device__ __forceinline__ void load32(const void* p, uint32_t* w) {
@@ -73,16 +76,15 @@ __device__ __forceinline__ void store32(void* p, const float* v) {
                : "memory");
 }
 
-// The block's values as raw words, zeros past the row's end.
-template <bool BF16, bool NV>
-__device__ __forceinline__ void load_block(const QuantArgs& a, int64_t row, int col, uint32_t (&w)[Shape<BF16, NV>::kWords]) {
+// The block's values as raw words, zeros past the row's end: `left` columns are
+// there.  VEC: a whole block, in 32-byte loads.
+template <bool BF16, bool NV, bool VEC>
+__device__ __forceinline__ void load_block(const char* p, int left, int align, uint32_t (&w)[Shape<BF16, NV>::kWords]) {
   using S = Shape<BF16, NV>;
-  const int left = a.n - col;
-  const char* p = static_cast<const char*>(a.X) + (row * a.ldx + col) * (BF16 ? 2 : 4);
-  if (left >= S::kBlock && a.align == 32) {
+  if (VEC) {
 #pragma unroll
     for (int i = 0; i < S::kWords; i += 8) load32(p + 4 * i, w + i);
-  } else if (left >= S::kBlock && a.align == 16) {
+  } else if (left >= S::kBlock && align >= 16) {
 #pragma unroll
     for (int i = 0; i < S::kWords; i += 4) {
       const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
@@ -111,14 +113,28 @@ __device__ __forceinline__ float value(const uint32_t* w, int i) {
   return __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
 }
 
-// Largest magnitude of the block as float bits (an infinity or NaN shows as
-// bits >= 0x7f800000, as magnitudes order like their bits).
+// Value i of a block in memory.
+template <bool BF16>
+__device__ __forceinline__ float memory_value(const char* p, int i) {
+  if (!BF16) return reinterpret_cast<const float*>(p)[i];
+  return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << 16);
+}
+
+// Largest magnitude of the block as float bits (from 0x7f800000 on where a
+// value is not finite).
 template <bool BF16, int WORDS>
 __device__ __forceinline__ uint32_t block_max(const uint32_t (&w)[WORDS]) {
-  uint32_t m = 0;
+  if (BF16) {  // two at a time, by magnitude (the sign of the result means nothing)
+    uint32_t m = w[0];
 #pragma unroll
-  for (int i = 0; i < WORDS; ++i) m = BF16 ? __vmaxu2(m, w[i] & 0x7fff7fffu) : max(m, w[i] & 0x7fffffffu);
-  return BF16 ? max(m << 16, m & 0xffff0000u) : m;
+    for (int i = 1; i < WORDS; ++i) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+    return max(m << 16 & 0x7fff0000u, m & 0x7fff0000u);
+  }
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < WORDS; i += 2)
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(__uint_as_float(w[i])), "f"(__uint_as_float(w[i + 1])));
+  return __float_as_uint(m) & 0x7fffffffu;
 }
 
 // Largest finite magnitude.
@@ -146,44 +162,52 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t m, uint32_t* s) {
 
 // Source row of output row r, or -1 (and an error in the status word) where
 // the index leaves X.
-__device__ __forceinline__ int64_t source_row(const QuantArgs& a, int64_t r) {
-  if (a.row_index == nullptr) return r;
-  const int64_t s = a.row_index[r];
+__device__ __forceinline__ int source_row(const QuantArgs& a, int64_t r) {
+  if (a.row_index == nullptr) return static_cast<int>(r);
+  const int s = a.row_index[r];
   if (s >= 0 && s < a.x_rows) return s;
   set_status(a.status, GPTQ_ERR_INVALID_ARG);
   return -1;
 }
 
-// Largest finite magnitude of `count` blocks, block i at the row and column
-// that at(i) gives, over the CTA.
-template <bool BF16, bool NV, typename At>
-__device__ __forceinline__ uint32_t blocks_max(const QuantArgs& a, int count, uint32_t* s, At at) {
+// The source rows of a band, once for the whole CTA (a gather's indices are
+// then not waited for row by row).
+__device__ __forceinline__ void band_rows(const QuantArgs& a, int64_t r0, int rows, int* src) {
+  if (threadIdx.x < rows) src[threadIdx.x] = source_row(a, r0 + threadIdx.x);
+  __syncthreads();
+}
+
+// Largest finite magnitude of a thread's blocks: kRows of them in flight, given
+// by at(i) as pointer (nullptr: none) and columns left.
+template <bool BF16, bool NV, bool VEC, int kRows, typename At>
+__device__ __forceinline__ uint32_t thread_max(const QuantArgs& a, int first, int step, int count, At at) {
   using S = Shape<BF16, NV>;
-  constexpr int kBatch = 32 / S::kWords * 2;
   uint32_t m = 0;
-  for (int i0 = threadIdx.x; i0 < count; i0 += kBatch * kThreads) {
-    uint32_t w[kBatch][S::kWords];
+  for (int i0 = first; i0 < count; i0 += kRows * step) {
+    uint32_t w[kRows][S::kWords];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      int64_t src = -1;
-      int col = 0;
-      const int i = i0 + u * kThreads;
-      if (i < count) {
-        int64_t row;
-        at(i, row, col);
-        src = source_row(a, row);
-      }
-      if (src >= 0) {
-        load_block<BF16, NV>(a, src, col, w[u]);
+    for (int u = 0; u < kRows; ++u) {
+      const int i = i0 + u * step;
+      int left = 0;
+      const char* p = i < count ? at(i, left) : nullptr;
+      if (p != nullptr) {
+        load_block<BF16, NV, VEC>(p, left, a.align, w[u]);
       } else {
 #pragma unroll
         for (int k = 0; k < S::kWords; ++k) w[u][k] = 0;
       }
     }
+    uint32_t b = 0;
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) m = max(m, finite_max<BF16>(w[u]));
+    for (int u = 0; u < kRows; ++u) b = max(b, block_max<BF16>(w[u]));
+    if (b >= 0x7f800000u) {  // something not finite: leave it out
+      b = 0;
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) b = max(b, finite_max<BF16>(w[u]));
+    }
+    m = max(m, b);
   }
-  return cta_max(m, s);
+  return m;
 }
 
 // Eight values to E2M1, the first in the low bits.
@@ -258,6 +282,16 @@ __device__ __noinline__ uint32_t exact_code(float x, float s, float t) {
   return k | (__float_as_uint(x) >> 31) << 3;
 }
 
+// Whether a > border * t, or equal with an odd `below`, on the exact product:
+// border has at most 8 bits, so the product is a float and its exact rest, and
+// a minus that float is exact where the comparison is near.
+__device__ __forceinline__ uint32_t past(float a, float border, float t, uint32_t below) {
+  const float near = __fmul_rn(border, t), rest = __fmaf_rn(border, t, -near), d = __fsub_rn(a, near);
+  return d > rest || (d == rest && (below & 1));
+}
+// The border above magnitude code k < 7.
+__constant__ float kE2m1Border[8] = {0.25f, 0.75f, 1.25f, 1.75f, 2.5f, 3.5f, 5.0f, 0.0f};
+
 constexpr float kBelow = 1.0f - 0x1p-20f, kAbove = 1.0f + 0x1p-20f;
 
 // What a CTA keeps of its group's tensor scale: about 1 / t and 1 / (6 t), a
@@ -289,9 +323,10 @@ __device__ __forceinline__ void mul2(float& a, float& b, float x, float y, float
 }
 
 // One block: codes, scale byte and s (NaN for a block with a value that is not
-// finite: it must not pass for a number, and its codes are zero).
+// finite: it must not pass for a number, and its codes are zero).  p: where the
+// block's values are in memory.
 template <bool BF16, bool NV>
-__device__ __forceinline__ void quantize_block(const uint32_t (&w)[Shape<BF16, NV>::kWords], const Unit& u,
+__device__ __forceinline__ void quantize_block(const uint32_t (&w)[Shape<BF16, NV>::kWords], const char* p, const Unit& u,
                                                uint32_t (&codes)[Shape<BF16, NV>::kBlock / 8], uint32_t& byte, float& s) {
   using S = Shape<BF16, NV>;
   const uint32_t m = block_max<BF16>(w);
@@ -324,7 +359,7 @@ __device__ __forceinline__ void quantize_block(const uint32_t (&w)[Shape<BF16, N
   if (!u.plain)
     byte = exact_scale(amax, u.t, 0, 126);
   else if (byte != two >> 8)
-    byte = exact_scale(amax, u.t, byte, two >> 8);
+    byte += past(amax, (e4m3_value(byte) + e4m3_value(byte + 1)) * 3.0f, u.t, byte);  // (neighbours)
   s = e4m3_value(byte);
   const float r = rcp_approx(s) * u.rt, r_lo = r * kBelow, r_hi = r * kAbove;
   if (byte == 0) {
@@ -332,7 +367,7 @@ __device__ __forceinline__ void quantize_block(const uint32_t (&w)[Shape<BF16, N
     for (int i = 0; i < S::kBlock / 8; ++i) codes[i] = 0;
     return;
   }
-  uint32_t differ[S::kBlock / 8], any = 0;
+  uint32_t differ[S::kBlock / 8];
 #pragma unroll
   for (int i = 0; i < S::kBlock / 8; ++i) {
     float lo[8], hi[8];
@@ -343,14 +378,30 @@ __device__ __forceinline__ void quantize_block(const uint32_t (&w)[Shape<BF16, N
       mul2(hi[j], hi[j + 1], x, y, r_hi);
     }
     codes[i] = to_e2m1(lo);
-    differ[i] = u.plain ? codes[i] ^ to_e2m1(hi) : 0xffffffffu;
-    any |= differ[i];
+    differ[i] = codes[i] ^ to_e2m1(hi);
   }
-  if (any != 0) {
-#pragma unroll
+  if (!u.plain) {
+#pragma unroll 1
     for (int i = 0; i < S::kBlock; ++i) {
-      const int at = 4 * (i % 8);
-      if (differ[i / 8] >> at & 15) codes[i / 8] = (codes[i / 8] & ~(15u << at)) | exact_code(value<BF16>(w, i), s, u.t) << at;
+      const uint32_t at = 4 * (i % 8), c = exact_code(memory_value<BF16>(p, i), s, u.t) << at;
+      if (i < 8)
+        codes[0] = (codes[0] & ~(15u << at)) | c;
+      else
+        codes[1] = (codes[1] & ~(15u << at)) | c;
+    }
+  } else {
+    // a border in between (often a tie: bf16 values over a scale made from a
+    // bf16 maximum): the code or the next one.  Rolled, with the value read
+    // again, as a few lanes of a warp come here.
+#pragma unroll
+    for (int i = 0; i < S::kBlock / 8; ++i) {
+#pragma unroll 1
+      while (differ[i] != 0) {
+        const int at = (__ffs(differ[i]) - 1) & ~3;
+        differ[i] &= ~(15u << at);
+        const uint32_t k = codes[i] >> at & 7;
+        codes[i] += past(fabsf(memory_value<BF16>(p, 8 * i + at / 4)), kE2m1Border[k] * s, u.t, k) << at;
+      }
     }
   }
 }
@@ -391,6 +442,7 @@ template <bool BF16, bool NV>
 __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(QuantArgs a) {
   __shared__ int tab[3][kFp4MaxGroups + 1];
   __shared__ uint32_t red[32];
+  __shared__ int src[kFp4Band];
   const GroupTable t{tab[0], tab[1], tab[2]};
   pdl_trigger();
   pdl_wait();
@@ -400,19 +452,99 @@ __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(QuantArgs a) {
   Band b;
   if (!find_band(a, t, band, b)) return;
   const int chunks = (a.n + kChunk - 1) / kChunk;
-  // this part's columns, block by block down the band's rows
+  // this part's columns, a chunk after the other, each down the band's rows
   using S = Shape<BF16, NV>;
-  const int c0 = static_cast<int>(int64_t(chunks) * part / a.splits) * S::kCols;
-  const int c1 = min((a.n + S::kBlock - 1) / S::kBlock, static_cast<int>(int64_t(chunks) * (part + 1) / a.splits) * S::kCols);
-  const int tall = (b.rows + S::kRowsAtOnce - 1) / S::kRowsAtOnce * S::kRowsAtOnce;  // whole strips of rows
-  const int wide = (c1 - c0 + S::kCols - 1) / S::kCols;
-  const uint32_t m = blocks_max<BF16, NV>(a, tall * wide * S::kCols, red, [&](int i, int64_t& row, int& col) {
-    const int strip = i / kThreads, r = strip / wide * S::kRowsAtOnce + i % kThreads / S::kCols;
-    const int c = c0 + strip % wide * S::kCols + i % S::kCols;
-    row = b.r0 + min(r, b.rows - 1);  // (past the ends: the last row or block once more)
-    col = min(c, c1 - 1) * S::kBlock;
-  });
+  band_rows(a, b.r0, b.rows, src);
+  const int c0 = static_cast<int>(int64_t(chunks) * part / a.splits), c1 = static_cast<int>(int64_t(chunks) * (part + 1) / a.splits);
+  const char* X = static_cast<const char*>(a.X);
+  constexpr int kSize = BF16 ? 2 : 4;
+  uint32_t m = 0;
+  for (int c = c0; c < c1; ++c) {
+    const int col = c * kChunk + threadIdx.x % S::kCols * S::kBlock;
+    auto at = [&](int r, int& left) -> const char* {
+      const int row = src[r];
+      left = a.n - col;
+      return row < 0 || left <= 0 ? nullptr : X + (row * a.ldx + col) * kSize;
+    };
+    const uint32_t t = a.align == 32 && (c + 1) * kChunk <= a.n
+                           ? thread_max<BF16, NV, true, S::kWords <= 16 ? 4 : 2>(a, threadIdx.x / S::kCols, S::kRowsAtOnce, b.rows, at)
+                           : thread_max<BF16, NV, false, 2>(a, threadIdx.x / S::kCols, S::kRowsAtOnce, b.rows, at);
+    m = max(m, t);
+  }
+  m = cta_max(m, red);
   if (threadIdx.x == 0) a.partial[blockIdx.x] = __uint_as_float(m);
+}
+
+// A thread's blocks down the band's rows.
+template <bool BF16, bool NV, bool VEC>
+__device__ __forceinline__ void quantize_rows(const QuantArgs& a, const Band& b, const Unit& u, const int* src, int col,
+                                              int cb, int64_t pitch, uint8_t* sc) {
+  using S = Shape<BF16, NV>;
+  constexpr int kSize = BF16 ? 2 : 4;
+  const char* X = static_cast<const char*>(a.X);
+  const int left = a.n - col;
+  const bool wide = left >= S::kBlock && a.n % 8 == 0 && reinterpret_cast<uintptr_t>(a.deq) % 32 == 0;
+  auto at = [&](int r) -> const char* {
+    const int row = r < b.rows ? src[r] : -1;
+    return row < 0 || left <= 0 ? nullptr : X + (row * a.ldx + col) * kSize;
+  };
+  auto fetch = [&](const char* p, uint32_t (&w)[S::kWords]) {
+    if (p != nullptr) {
+      load_block<BF16, NV, VEC>(p, left, a.align, w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::kWords; ++i) w[i] = 0;
+    }
+  };
+  uint32_t w[S::kAhead + 1][S::kWords];
+  const char* p[S::kAhead + 1];
+  int r = threadIdx.x / S::kCols;
+#pragma unroll
+  for (int v = 0; v < S::kAhead; ++v) {
+    p[v] = at(r + v * S::kRowsAtOnce);
+    fetch(p[v], w[v]);
+  }
+#pragma unroll 1
+  for (; r < b.rows; r += S::kRowsAtOnce) {
+    p[S::kAhead] = at(r + S::kAhead * S::kRowsAtOnce);
+    fetch(p[S::kAhead], w[S::kAhead]);
+    const int64_t row = b.r0 + r;
+    uint32_t codes[S::kBlock / 8], byte;
+    float s;
+    quantize_block<BF16, NV>(w[0], p[0], u, codes, byte, s);
+    uint8_t* dst = a.packed + row * pitch + col / 2;
+    if (NV)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(codes[0], codes[1]);
+    else
+      *reinterpret_cast<uint4*>(dst) = make_uint4(codes[0], codes[1], codes[S::kBlock / 8 - 2], codes[S::kBlock / 8 - 1]);
+    if (left > 0) sc[cb / 4 * kFp4TileBytes + r % 32 * 16 + r / 32 * 4 + cb % 4] = static_cast<uint8_t>(byte);
+    if (a.deq != nullptr && left > 0) {
+      float* d = a.deq + row * a.n + col;
+#pragma unroll
+      for (int i = 0; i < S::kBlock / 8; ++i) {
+        float f[8];
+        from_e2m1(codes[i], f);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          mul2(f[j], f[j + 1], f[j], f[j + 1], s);
+          if (NV) mul2(f[j], f[j + 1], f[j], f[j + 1], u.t);
+        }
+        if (wide) {
+          store32(d + 8 * i, f);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (8 * i + j < left) d[8 * i + j] = f[j];
+        }
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < S::kAhead; ++v) {
+      p[v] = p[v + 1];
+#pragma unroll
+      for (int i = 0; i < S::kWords; ++i) w[v][i] = w[v + 1][i];
+    }
+  }
 }
 
 template <bool BF16, bool NV>
@@ -420,6 +552,7 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(QuantArgs a) {
   using S = Shape<BF16, NV>;
   __shared__ int tab[3][kFp4MaxGroups + 1];
   __shared__ uint32_t red[32];
+  __shared__ int src[kFp4Band];
   __shared__ __align__(16) uint8_t sc[kFp4Band * (kChunk / S::kBlock)];
   const GroupTable t{tab[0], tab[1], tab[2]};
   pdl_trigger();
@@ -451,73 +584,34 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(QuantArgs a) {
         m = cta_max(m, red);
       } else {
         const int across = (a.n + S::kBlock - 1) / S::kBlock;
-        m = blocks_max<BF16, NV>(a, static_cast<int>(b.g1 - b.g0) * across, red, [&](int i, int64_t& row, int& col) {
-          row = b.g0 + i / across;
-          col = i % across * S::kBlock;
-        });
+        m = thread_max<BF16, NV, false, 4>(a, threadIdx.x, kThreads, static_cast<int>(b.g1 - b.g0) * across,
+                                           [&](int i, int& left) -> const char* {
+                                             const int row = source_row(a, b.g0 + i / across);
+                                             left = a.n - i % across * S::kBlock;
+                                             return row < 0 ? nullptr
+                                                            : static_cast<const char*>(a.X) +
+                                                                  (row * a.ldx + a.n - left) * (BF16 ? 2 : 4);
+                                           });
+        m = cta_max(m, red);
       }
       tensor = fmaxf(__fdiv_rn(__uint_as_float(m), 2688.0f), FLT_MIN);
       if (band == b.first && chunk == 0 && threadIdx.x == 0) a.tensor_scale[b.g] = tensor;
     }
     u = unit_of(tensor);
   }
-  for (int i = threadIdx.x; i < int(sizeof(sc)) / 4; i += kThreads) reinterpret_cast<uint32_t*>(sc)[i] = 0;
-  __syncthreads();
+  if (b.rows < kFp4Band || (chunk + 1) * kChunk > a.n) {  // bytes that have no row or block are zero
+    for (int i = threadIdx.x; i < int(sizeof(sc)) / 4; i += kThreads) reinterpret_cast<uint32_t*>(sc)[i] = 0;
+  }
+  band_rows(a, b.r0, b.rows, src);
 
   const int cb = threadIdx.x % S::kCols;
   const int col = chunk * kChunk + cb * S::kBlock;
   const int64_t pitch = fp4_pitch(a.n);
-  const bool vec = a.n % 8 == 0 && col + S::kBlock <= a.n && reinterpret_cast<uintptr_t>(a.deq) % 32 == 0;
   if (col / 2 < pitch) {
-    for (int r0 = threadIdx.x / S::kCols; r0 < b.rows; r0 += S::kBatch * S::kRowsAtOnce) {
-      uint32_t w[S::kBatch][S::kWords];
-#pragma unroll
-      for (int v = 0; v < S::kBatch; ++v) {
-        const int r = r0 + v * S::kRowsAtOnce;
-        const int64_t src = r < b.rows ? source_row(a, b.r0 + r) : -1;
-        if (src >= 0 && col < a.n) {
-          load_block<BF16, NV>(a, src, col, w[v]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < S::kWords; ++i) w[v][i] = 0;
-        }
-      }
-#pragma unroll
-      for (int v = 0; v < S::kBatch; ++v) {
-        const int r = r0 + v * S::kRowsAtOnce;
-        if (r >= b.rows) break;
-        const int64_t row = b.r0 + r;
-        uint32_t codes[S::kBlock / 8], byte;
-        float s;
-        quantize_block<BF16, NV>(w[v], u, codes, byte, s);
-        uint8_t* dst = a.packed + row * pitch + col / 2;
-        if (NV)
-          *reinterpret_cast<uint2*>(dst) = make_uint2(codes[0], codes[1]);
-        else
-          *reinterpret_cast<uint4*>(dst) = make_uint4(codes[0], codes[1], codes[S::kBlock / 8 - 2], codes[S::kBlock / 8 - 1]);
-        if (col < a.n) sc[cb / 4 * kFp4TileBytes + r % 32 * 16 + r / 32 * 4 + cb % 4] = static_cast<uint8_t>(byte);
-        if (a.deq != nullptr && col < a.n) {
-          float* d = a.deq + row * a.n + col;
-#pragma unroll
-          for (int i = 0; i < S::kBlock / 8; ++i) {
-            float f[8];
-            from_e2m1(codes[i], f);
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              mul2(f[j], f[j + 1], f[j], f[j + 1], s);
-              if (NV) mul2(f[j], f[j + 1], f[j], f[j + 1], u.t);
-            }
-            if (vec) {
-              store32(d + 8 * i, f);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (col + 8 * i + j < a.n) d[8 * i + j] = f[j];
-            }
-          }
-        }
-      }
-    }
+    if (a.align == 32 && (chunk + 1) * kChunk <= a.n)
+      quantize_rows<BF16, NV, true>(a, b, u, src, col, cb, pitch, sc);
+    else
+      quantize_rows<BF16, NV, false>(a, b, u, src, col, cb, pitch, sc);
   }
   __syncthreads();
   const int quads = fp4_quads(a.n, NV);
