@@ -16,8 +16,8 @@
 //
 // Bound by HBM: per value 2 (bf16) or 4 (fp32) bytes in, 1/2 + 1/B out, and 4
 // with the dequantised values.  A CTA takes a band of 128 rows x 256 columns,
-// a thread a block at a time (its maximum needs no other thread) with the
-// loads of several rows in flight, and the band's scale tiles go out whole
+// a lane 32 bytes of a row at a time, with the loads of the next
+// rows in flight, and the band's scale tiles go out whole
 // from shared memory.
 #include <algorithm>
 #include <cfloat>
@@ -29,9 +29,6 @@
 namespace gptq {
 namespace {
 
-#ifndef AHEAD
-#define AHEAD 1
-#endif
 constexpr int kThreads = 256;
 constexpr int kChunk = 256;  // columns of a CTA's tile
 
@@ -55,13 +52,18 @@ struct QuantArgs {
   int* status;
 };
 
+// A lane takes 32 bytes of a row, so that a warp's loads are whole lines; a
+// block is 1 (nvfp4 of bf16), 2 or 4 (mxfp4 of fp32) neighbouring lanes.
 template <bool BF16, bool NV>
 struct Shape {
   static constexpr int kBlock = NV ? 16 : 32;
-  static constexpr int kWords = kBlock * (BF16 ? 2 : 4) / 4;
-  static constexpr int kCols = kChunk / kBlock;      // blocks across the tile
-  static constexpr int kRowsAtOnce = kThreads / kCols;
-  static constexpr int kAhead = AHEAD;  // blocks a thread loads before it needs them
+  static constexpr int kLane = BF16 ? 16 : 8;        // values of a lane
+  static constexpr int kLanes = kBlock / kLane;      // lanes of a block
+  static constexpr int kAcross = kChunk / kLane;     // lanes across the tile
+  static constexpr int kRowsAtOnce = kThreads / kAcross;
+  // rows loaded ahead of the one in work (nvfp4 of bf16 is bound by issuing:
+  // more registers would cost it warps)
+  static constexpr int kAhead = BF16 && NV ? 1 : 2;
 };
 
 __device__ __forceinline__ void load32(const void* p, uint32_t* w) {
@@ -76,17 +78,16 @@ __device__ __forceinline__ void store32(void* p, const float* v) {
                : "memory");
 }
 
-// The block's values as raw words, zeros past the row's end: `left` columns are
-// there.  VEC: a whole block, in 32-byte loads.
-template <bool BF16, bool NV, bool VEC>
-__device__ __forceinline__ void load_block(const char* p, int left, int align, uint32_t (&w)[Shape<BF16, NV>::kWords]) {
-  using S = Shape<BF16, NV>;
+// A lane's values as raw words, zeros past the row's end: `left` columns are
+// there.  VEC: all of them, in a 32-byte load.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load_lane(const char* p, int left, int align, uint32_t (&w)[8]) {
+  constexpr int kLane = BF16 ? 16 : 8;
   if (VEC) {
+    load32(p, w);
+  } else if (left >= kLane && align >= 16) {
 #pragma unroll
-    for (int i = 0; i < S::kWords; i += 8) load32(p + 4 * i, w + i);
-  } else if (left >= S::kBlock && align >= 16) {
-#pragma unroll
-    for (int i = 0; i < S::kWords; i += 4) {
+    for (int i = 0; i < 8; i += 4) {
       const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
       w[i] = v.x;
       w[i + 1] = v.y;
@@ -96,14 +97,14 @@ __device__ __forceinline__ void load_block(const char* p, int left, int align, u
   } else if (BF16) {
     const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-    for (int i = 0; i < S::kWords; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const uint32_t lo = 2 * i < left ? h[2 * i] : 0, hi = 2 * i + 1 < left ? h[2 * i + 1] : 0;
       w[i] = lo | hi << 16;
     }
   } else {
     const uint32_t* f = reinterpret_cast<const uint32_t*>(p);
 #pragma unroll
-    for (int i = 0; i < S::kWords; ++i) w[i] = i < left ? f[i] : 0;
+    for (int i = 0; i < 8; ++i) w[i] = i < left ? f[i] : 0;
   }
 }
 
@@ -113,17 +114,17 @@ __device__ __forceinline__ float value(const uint32_t* w, int i) {
   return __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
 }
 
-// Value i of a block in memory.
+// Value i of a lane's, in memory.
 template <bool BF16>
 __device__ __forceinline__ float memory_value(const char* p, int i) {
   if (!BF16) return reinterpret_cast<const float*>(p)[i];
   return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << 16);
 }
 
-// Largest magnitude of the block as float bits (from 0x7f800000 on where a
+// Largest magnitude of a lane's values as float bits (from 0x7f800000 on where a
 // value is not finite).
 template <bool BF16, int WORDS>
-__device__ __forceinline__ uint32_t block_max(const uint32_t (&w)[WORDS]) {
+__device__ __forceinline__ uint32_t lane_max(const uint32_t (&w)[WORDS]) {
   if (BF16) {  // two at a time, by magnitude (the sign of the result means nothing)
     uint32_t m = w[0];
 #pragma unroll
@@ -140,7 +141,7 @@ __device__ __forceinline__ uint32_t block_max(const uint32_t (&w)[WORDS]) {
 // Largest finite magnitude.
 template <bool BF16, int WORDS>
 __device__ __forceinline__ uint32_t finite_max(const uint32_t (&w)[WORDS]) {
-  uint32_t m = block_max<BF16>(w);
+  uint32_t m = lane_max<BF16>(w);
   if (m >= 0x7f800000u) {
     m = 0;
     for (int i = 0; i < (BF16 ? 2 * WORDS : WORDS); ++i) {
@@ -177,29 +178,28 @@ __device__ __forceinline__ void band_rows(const QuantArgs& a, int64_t r0, int ro
   __syncthreads();
 }
 
-// Largest finite magnitude of a thread's blocks: kRows of them in flight, given
+// Largest finite magnitude of a thread's runs of values: kRows of them in flight, given
 // by at(i) as pointer (nullptr: none) and columns left.
-template <bool BF16, bool NV, bool VEC, int kRows, typename At>
+template <bool BF16, bool VEC, int kRows, typename At>
 __device__ __forceinline__ uint32_t thread_max(const QuantArgs& a, int first, int step, int count, At at) {
-  using S = Shape<BF16, NV>;
   uint32_t m = 0;
   for (int i0 = first; i0 < count; i0 += kRows * step) {
-    uint32_t w[kRows][S::kWords];
+    uint32_t w[kRows][8];
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
       const int i = i0 + u * step;
       int left = 0;
       const char* p = i < count ? at(i, left) : nullptr;
       if (p != nullptr) {
-        load_block<BF16, NV, VEC>(p, left, a.align, w[u]);
+        load_lane<BF16, VEC>(p, left, a.align, w[u]);
       } else {
 #pragma unroll
-        for (int k = 0; k < S::kWords; ++k) w[u][k] = 0;
+        for (int k = 0; k < 8; ++k) w[u][k] = 0;
       }
     }
     uint32_t b = 0;
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) b = max(b, block_max<BF16>(w[u]));
+    for (int u = 0; u < kRows; ++u) b = max(b, lane_max<BF16>(w[u]));
     if (b >= 0x7f800000u) {  // something not finite: leave it out
       b = 0;
 #pragma unroll
@@ -233,6 +233,12 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
 
 __device__ __forceinline__ float e4m3_value(uint32_t b) {
   return b < 8 ? b * 0.001953125f : __uint_as_float(((b >> 3) + 120) << 23 | (b & 7) << 20);
+}
+
+__device__ __forceinline__ float e4m3_to_float(uint32_t b) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(b)));
+  return __half2float(*reinterpret_cast<const __half*>(&h));
 }
 
 __device__ __forceinline__ float e2m1_value(uint32_t c) {
@@ -322,19 +328,22 @@ __device__ __forceinline__ void mul2(float& a, float& b, float x, float y, float
       : "f"(x), "f"(y), "f"(k));
 }
 
-// One block: codes, scale byte and s (NaN for a block with a value that is not
-// finite: it must not pass for a number, and its codes are zero).  p: where the
-// block's values are in memory.
+// A lane's part of a block: its codes, and the block's scale byte and s (NaN
+// for a block with a value that is not finite: it must not pass for a number,
+// and its codes are zero).  p: where the lane's values are in memory.  Called
+// by whole warps.
 template <bool BF16, bool NV>
-__device__ __forceinline__ void quantize_block(const uint32_t (&w)[Shape<BF16, NV>::kWords], const char* p, const Unit& u,
-                                               uint32_t (&codes)[Shape<BF16, NV>::kBlock / 8], uint32_t& byte, float& s) {
+__device__ __forceinline__ void quantize_lane(const uint32_t (&w)[8], const char* p, const Unit& u,
+                                              uint32_t (&codes)[Shape<BF16, NV>::kLane / 8], uint32_t& byte, float& s) {
   using S = Shape<BF16, NV>;
-  const uint32_t m = block_max<BF16>(w);
+  uint32_t m = lane_max<BF16>(w);
+#pragma unroll
+  for (int d = 1; d < S::kLanes; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
   if (m >= 0x7f800000u) {
     byte = NV ? 0x7f : 0xff;
     s = __uint_as_float(0x7fc00000u);
 #pragma unroll
-    for (int i = 0; i < S::kBlock / 8; ++i) codes[i] = 0;
+    for (int i = 0; i < S::kLane / 8; ++i) codes[i] = 0;
     return;
   }
   if (!NV) {
@@ -344,7 +353,7 @@ __device__ __forceinline__ void quantize_block(const uint32_t (&w)[Shape<BF16, N
     s = e > -127 ? __uint_as_float(uint32_t(e + 127) << 23) : __uint_as_float(0x00400000u);
     const float inv = __uint_as_float(uint32_t(127 - e) << 23);
 #pragma unroll
-    for (int i = 0; i < S::kBlock / 8; ++i) {
+    for (int i = 0; i < S::kLane / 8; ++i) {
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; j += 2) mul2(v[j], v[j + 1], value<BF16>(w, 8 * i + j), value<BF16>(w, 8 * i + j + 1), inv);
@@ -360,16 +369,16 @@ __device__ __forceinline__ void quantize_block(const uint32_t (&w)[Shape<BF16, N
     byte = exact_scale(amax, u.t, 0, 126);
   else if (byte != two >> 8)
     byte += past(amax, (e4m3_value(byte) + e4m3_value(byte + 1)) * 3.0f, u.t, byte);  // (neighbours)
-  s = e4m3_value(byte);
+  s = e4m3_to_float(byte);
   const float r = rcp_approx(s) * u.rt, r_lo = r * kBelow, r_hi = r * kAbove;
   if (byte == 0) {
 #pragma unroll
-    for (int i = 0; i < S::kBlock / 8; ++i) codes[i] = 0;
+    for (int i = 0; i < S::kLane / 8; ++i) codes[i] = 0;
     return;
   }
-  uint32_t differ[S::kBlock / 8];
+  uint32_t differ[S::kLane / 8];
 #pragma unroll
-  for (int i = 0; i < S::kBlock / 8; ++i) {
+  for (int i = 0; i < S::kLane / 8; ++i) {
     float lo[8], hi[8];
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
@@ -382,19 +391,19 @@ __device__ __forceinline__ void quantize_block(const uint32_t (&w)[Shape<BF16, N
   }
   if (!u.plain) {
 #pragma unroll 1
-    for (int i = 0; i < S::kBlock; ++i) {
-      const uint32_t at = 4 * (i % 8), c = exact_code(memory_value<BF16>(p, i), s, u.t) << at;
+    for (int i = 0; i < S::kLane; ++i) {
+      const uint32_t at = 4 * (i % 8), c = exact_code(p == nullptr ? 0.0f : memory_value<BF16>(p, i), s, u.t) << at;
       if (i < 8)
         codes[0] = (codes[0] & ~(15u << at)) | c;
       else
-        codes[1] = (codes[1] & ~(15u << at)) | c;
+        codes[S::kLane / 8 - 1] = (codes[S::kLane / 8 - 1] & ~(15u << at)) | c;
     }
   } else {
     // a border in between (often a tie: bf16 values over a scale made from a
     // bf16 maximum): the code or the next one.  Rolled, with the value read
     // again, as a few lanes of a warp come here.
 #pragma unroll
-    for (int i = 0; i < S::kBlock / 8; ++i) {
+    for (int i = 0; i < S::kLane / 8; ++i) {
 #pragma unroll 1
       while (differ[i] != 0) {
         const int at = (__ffs(differ[i]) - 1) & ~3;
@@ -460,95 +469,103 @@ __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(QuantArgs a) {
   constexpr int kSize = BF16 ? 2 : 4;
   uint32_t m = 0;
   for (int c = c0; c < c1; ++c) {
-    const int col = c * kChunk + threadIdx.x % S::kCols * S::kBlock;
+    const int col = c * kChunk + threadIdx.x % S::kAcross * S::kLane;
     auto at = [&](int r, int& left) -> const char* {
       const int row = src[r];
       left = a.n - col;
       return row < 0 || left <= 0 ? nullptr : X + (row * a.ldx + col) * kSize;
     };
     const uint32_t t = a.align == 32 && (c + 1) * kChunk <= a.n
-                           ? thread_max<BF16, NV, true, S::kWords <= 16 ? 4 : 2>(a, threadIdx.x / S::kCols, S::kRowsAtOnce, b.rows, at)
-                           : thread_max<BF16, NV, false, 2>(a, threadIdx.x / S::kCols, S::kRowsAtOnce, b.rows, at);
+                           ? thread_max<BF16, true, 4>(a, threadIdx.x / S::kAcross, S::kRowsAtOnce, b.rows, at)
+                           : thread_max<BF16, false, 4>(a, threadIdx.x / S::kAcross, S::kRowsAtOnce, b.rows, at);
     m = max(m, t);
   }
   m = cta_max(m, red);
   if (threadIdx.x == 0) a.partial[blockIdx.x] = __uint_as_float(m);
 }
 
-// A thread's blocks down the band's rows.
+// A lane's values down the band's rows.
 template <bool BF16, bool NV, bool VEC>
 __device__ __forceinline__ void quantize_rows(const QuantArgs& a, const Band& b, const Unit& u, const int* src, int col,
-                                              int cb, int64_t pitch, uint8_t* sc) {
+                                              int64_t pitch, uint8_t* sc) {
   using S = Shape<BF16, NV>;
   constexpr int kSize = BF16 ? 2 : 4;
   const char* X = static_cast<const char*>(a.X);
   const int left = a.n - col;
-  const bool wide = left >= S::kBlock && a.n % 8 == 0 && reinterpret_cast<uintptr_t>(a.deq) % 32 == 0;
+  const bool wide = left >= S::kLane && a.n % 8 == 0 && reinterpret_cast<uintptr_t>(a.deq) % 32 == 0;
+  const int cb = threadIdx.x % S::kAcross / S::kLanes;  // block of the chunk
+  const bool first = threadIdx.x % S::kLanes == 0 && left > 0;  // the lane that writes the block's scale
+  uint8_t* sc_col = sc + cb / 4 * kFp4TileBytes + cb % 4;
   auto at = [&](int r) -> const char* {
     const int row = r < b.rows ? src[r] : -1;
     return row < 0 || left <= 0 ? nullptr : X + (row * a.ldx + col) * kSize;
   };
-  auto fetch = [&](const char* p, uint32_t (&w)[S::kWords]) {
+  auto fetch = [&](const char* p, uint32_t (&w)[8]) {
     if (p != nullptr) {
-      load_block<BF16, NV, VEC>(p, left, a.align, w);
+      load_lane<BF16, VEC>(p, left, a.align, w);
     } else {
 #pragma unroll
-      for (int i = 0; i < S::kWords; ++i) w[i] = 0;
+      for (int i = 0; i < 8; ++i) w[i] = 0;
     }
   };
-  uint32_t w[S::kAhead + 1][S::kWords];
+  uint32_t w[S::kAhead + 1][8];
   const char* p[S::kAhead + 1];
-  int r = threadIdx.x / S::kCols;
+  int r = threadIdx.x / S::kAcross;
 #pragma unroll
   for (int v = 0; v < S::kAhead; ++v) {
     p[v] = at(r + v * S::kRowsAtOnce);
     fetch(p[v], w[v]);
   }
-#pragma unroll 1
-  for (; r < b.rows; r += S::kRowsAtOnce) {
+  uint8_t* dst = a.packed + (b.r0 + r) * pitch + col / 2;
+  float* deq = a.deq + (b.r0 + r) * a.n + col;
+#pragma unroll 2
+  for (int r0 = 0; r0 < b.rows; r0 += S::kRowsAtOnce, r += S::kRowsAtOnce) {  // (as often in every lane)
     p[S::kAhead] = at(r + S::kAhead * S::kRowsAtOnce);
     fetch(p[S::kAhead], w[S::kAhead]);
-    const int64_t row = b.r0 + r;
-    uint32_t codes[S::kBlock / 8], byte;
+    uint32_t codes[S::kLane / 8], byte;
     float s;
-    quantize_block<BF16, NV>(w[0], p[0], u, codes, byte, s);
-    uint8_t* dst = a.packed + row * pitch + col / 2;
-    if (NV)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(codes[0], codes[1]);
-    else
-      *reinterpret_cast<uint4*>(dst) = make_uint4(codes[0], codes[1], codes[S::kBlock / 8 - 2], codes[S::kBlock / 8 - 1]);
-    if (left > 0) sc[cb / 4 * kFp4TileBytes + r % 32 * 16 + r / 32 * 4 + cb % 4] = static_cast<uint8_t>(byte);
-    if (a.deq != nullptr && left > 0) {
-      float* d = a.deq + row * a.n + col;
+    quantize_lane<BF16, NV>(w[0], p[0], u, codes, byte, s);
+    if (r < b.rows) {
+      if (col / 2 < pitch) {
+        if (BF16)
+          *reinterpret_cast<uint2*>(dst) = make_uint2(codes[0], codes[S::kLane / 8 - 1]);
+        else
+          *reinterpret_cast<uint32_t*>(dst) = codes[0];
+      }
+      if (first) sc_col[r % 32 * 16 + r / 32 * 4] = static_cast<uint8_t>(byte);
+      if (a.deq != nullptr && left > 0) {
 #pragma unroll
-      for (int i = 0; i < S::kBlock / 8; ++i) {
-        float f[8];
-        from_e2m1(codes[i], f);
+        for (int i = 0; i < S::kLane / 8; ++i) {
+          float f[8];
+          from_e2m1(codes[i], f);
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          mul2(f[j], f[j + 1], f[j], f[j + 1], s);
-          if (NV) mul2(f[j], f[j + 1], f[j], f[j + 1], u.t);
-        }
-        if (wide) {
-          store32(d + 8 * i, f);
-        } else {
+          for (int j = 0; j < 8; j += 2) {
+            mul2(f[j], f[j + 1], f[j], f[j + 1], s);
+            if (NV) mul2(f[j], f[j + 1], f[j], f[j + 1], u.t);
+          }
+          if (wide) {
+            store32(deq + 8 * i, f);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (8 * i + j < left) d[8 * i + j] = f[j];
+            for (int j = 0; j < 8; ++j)
+              if (8 * i + j < left) deq[8 * i + j] = f[j];
+          }
         }
       }
     }
+    dst += S::kRowsAtOnce * pitch;
+    deq += static_cast<int64_t>(S::kRowsAtOnce) * a.n;
 #pragma unroll
     for (int v = 0; v < S::kAhead; ++v) {
       p[v] = p[v + 1];
 #pragma unroll
-      for (int i = 0; i < S::kWords; ++i) w[v][i] = w[v + 1][i];
+      for (int i = 0; i < 8; ++i) w[v][i] = w[v + 1][i];
     }
   }
 }
 
 template <bool BF16, bool NV>
-__global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(QuantArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) {
   using S = Shape<BF16, NV>;
   __shared__ int tab[3][kFp4MaxGroups + 1];
   __shared__ uint32_t red[32];
@@ -583,15 +600,14 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(QuantArgs a) {
         for (int64_t i = threadIdx.x; i < b.bands * a.splits; i += kThreads) m = max(m, __float_as_uint(p[i]));
         m = cta_max(m, red);
       } else {
-        const int across = (a.n + S::kBlock - 1) / S::kBlock;
-        m = thread_max<BF16, NV, false, 4>(a, threadIdx.x, kThreads, static_cast<int>(b.g1 - b.g0) * across,
-                                           [&](int i, int& left) -> const char* {
-                                             const int row = source_row(a, b.g0 + i / across);
-                                             left = a.n - i % across * S::kBlock;
-                                             return row < 0 ? nullptr
-                                                            : static_cast<const char*>(a.X) +
-                                                                  (row * a.ldx + a.n - left) * (BF16 ? 2 : 4);
-                                           });
+        const int across = (a.n + S::kLane - 1) / S::kLane;
+        m = thread_max<BF16, false, 4>(a, threadIdx.x, kThreads, static_cast<int>(b.g1 - b.g0) * across,
+                                       [&](int i, int& left) -> const char* {
+                                         const int row = source_row(a, b.g0 + i / across), col = i % across * S::kLane;
+                                         left = a.n - col;
+                                         return row < 0 ? nullptr
+                                                        : static_cast<const char*>(a.X) + (row * a.ldx + col) * (BF16 ? 2 : 4);
+                                       });
         m = cta_max(m, red);
       }
       tensor = fmaxf(__fdiv_rn(__uint_as_float(m), 2688.0f), FLT_MIN);
@@ -604,19 +620,17 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(QuantArgs a) {
   }
   band_rows(a, b.r0, b.rows, src);
 
-  const int cb = threadIdx.x % S::kCols;
-  const int col = chunk * kChunk + cb * S::kBlock;
+  const int col = chunk * kChunk + threadIdx.x % S::kAcross * S::kLane;
   const int64_t pitch = fp4_pitch(a.n);
-  if (col / 2 < pitch) {
-    if (a.align == 32 && (chunk + 1) * kChunk <= a.n)
-      quantize_rows<BF16, NV, true>(a, b, u, src, col, cb, pitch, sc);
-    else
-      quantize_rows<BF16, NV, false>(a, b, u, src, col, cb, pitch, sc);
-  }
+  if (a.align == 32 && (chunk + 1) * kChunk <= a.n)
+    quantize_rows<BF16, NV, true>(a, b, u, src, col, pitch, sc);
+  else
+    quantize_rows<BF16, NV, false>(a, b, u, src, col, pitch, sc);
   __syncthreads();
   const int quads = fp4_quads(a.n, NV);
-  const int q0 = chunk * (S::kCols / 4);
-  const int bytes = min(S::kCols / 4, quads - q0) * kFp4TileBytes;
+  constexpr int kQuads = kChunk / (4 * S::kBlock);  // scale tiles across the chunk
+  const int q0 = chunk * kQuads;
+  const int bytes = min(kQuads, quads - q0) * kFp4TileBytes;
   uint8_t* out = a.scales + (band * quads + q0) * kFp4TileBytes;
   for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16)
     *reinterpret_cast<uint4*>(out + i) = *reinterpret_cast<const uint4*>(sc + i);
