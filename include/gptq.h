@@ -511,19 +511,22 @@ gptq_status gptq_fp4_grouped_matmul(gptq_fp4_format format, const uint8_t* w_pac
                                     const float* x_tensor, int64_t tokens, const int32_t* offsets, void* y, gptq_dtype ydt,
                                     int64_t ldy, void* stream);
 
-/* Bytes of workspace gptq_fp4_linear needs; 0 for sizes that are refused. */
-size_t gptq_fp4_linear_workspace_size(int64_t tokens, int32_t n, gptq_fp4_format format, int32_t groups,
-                                      int32_t ragged);
+/* Bytes of workspace gptq_fp4_linear needs: 0 for a few tokens, which the
+ * product quantises itself, and for sizes that are refused. */
+size_t gptq_fp4_linear_workspace_size(int64_t tokens, int64_t rows, int32_t n, gptq_fp4_format format,
+                                      int32_t groups, int32_t ragged);
 
 /* gptq_fp4_quantize of X followed by the product with W, in one call: what a
- * 4-bit layer does at inference.  The quantised X lives in the workspace.
+ * 4-bit layer does at inference.  The quantised X lives in the workspace (of a
+ * few tokens: on the chip, and the whole call is one launch).
  *   w_packed, w_scales, w_tensor, groups, rows, n  W, as for the products
  *   X, xdt, x_rows, ldx, row_index  as in gptq_fp4_quantize, `tokens` rows
  *   offsets      NULL: groups == 1, every token with the one W; else the
  *                tokens' groups, as in gptq_fp4_grouped_matmul
  *   x_tensor     fp32 [groups] tensor scales of X to use, or NULL to make them
  *   y, ydt, ldy  as for the products
- *   ws           gptq_fp4_linear_workspace_size bytes, 256-byte aligned
+ *   ws           gptq_fp4_linear_workspace_size bytes, 256-byte aligned (may be
+ *                NULL when that is 0)
  * The result is that of the two calls, bit for bit.  Errors as theirs. */
 gptq_status gptq_fp4_linear(gptq_fp4_format format, const uint8_t* w_packed, const uint8_t* w_scales,
                             const float* w_tensor, int32_t groups, int64_t rows, int32_t n, const void* X,

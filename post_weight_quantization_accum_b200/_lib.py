@@ -72,8 +72,8 @@ _SIGS = {
     "gptq_fp4_grouped_matmul": (ctypes.c_int, [ctypes.c_int, _P, _P, _P, ctypes.c_int32, ctypes.c_int64,
                                                ctypes.c_int32, _P, _P, _P, ctypes.c_int64, _P, _P, ctypes.c_int,
                                                ctypes.c_int64, _P]),
-    "gptq_fp4_linear_workspace_size": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_int32,
-                                                         ctypes.c_int32]),
+    "gptq_fp4_linear_workspace_size": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int,
+                                                         ctypes.c_int32, ctypes.c_int32]),
     "gptq_fp4_linear": (ctypes.c_int, [ctypes.c_int, _P, _P, _P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, _P,
                                        ctypes.c_int, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P,
                                        ctypes.c_int, ctypes.c_int64, _P, ctypes.c_size_t, _P]),

@@ -45,6 +45,11 @@ gptq_status fp4_quantize(const void* X, int x_bf16, int64_t x_rows, int n, int64
 gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const float* wt, int groups, int64_t rows,
                        int n, const uint8_t* xq, const uint8_t* xscales, const float* xt, int64_t tokens,
                        const int32_t* offsets, void* y, int y_bf16, int64_t ldy, cudaStream_t st);
+bool fp4_linear_raw(int64_t tokens, int groups, bool ragged, int64_t rows, int n);
+gptq_status fp4_raw_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const float* wt, int groups, int64_t rows,
+                           int n, const void* X, int x_bf16, int64_t x_rows, int64_t ldx, const int32_t* row_index,
+                           const float* x_tensor, int64_t tokens, const int32_t* offsets, void* y, int y_bf16, int64_t ldy,
+                           cudaStream_t st);
 
 // Status words of each device: [0] failures of asynchronous kernels (bounded
 // waits), [1] the factorization status of gptq_prepare_hinv.
@@ -465,14 +470,34 @@ gptq_status check_product(gptq_fp4_format format, const uint8_t* w_packed, const
   return GPTQ_OK;
 }
 
+gptq_status check_quantize(const void* X, gptq_dtype xdt, int64_t x_rows, int32_t n, int64_t ldx,
+                           const int32_t* row_index, int64_t rows, const int32_t* offsets, int32_t groups,
+                           gptq_fp4_format format, int32_t given, const float* tensor_scale, const uint8_t* packed,
+                           const uint8_t* scales, const float* deq) {
+  if ((xdt != GPTQ_F32 && xdt != GPTQ_BF16) || !valid_format(format) || rows < 0 || rows > kMaxFp4Rows || x_rows < 0 ||
+      x_rows > kMaxFp4Rows || n < 1 || n > kMaxN || ldx < n || (given != 0 && given != 1) ||
+      !valid_groups(rows, groups, offsets != nullptr) || (row_index == nullptr && x_rows < rows))
+    return GPTQ_ERR_INVALID_ARG;
+  const bool nv = format == GPTQ_NVFP4;
+  if (nv != (tensor_scale != nullptr) || (!nv && given) || !aligned(tensor_scale, 4)) return GPTQ_ERR_INVALID_ARG;
+  if (rows > 0 && (X == nullptr || packed == nullptr || scales == nullptr)) return GPTQ_ERR_INVALID_ARG;
+  if (!aligned(X, xdt == GPTQ_BF16 ? 2 : 4) || !aligned(packed, 16) || !aligned(scales, 16) || !aligned(deq, 4) ||
+      !aligned(row_index, 4) || !aligned(offsets, 4))
+    return GPTQ_ERR_INVALID_ARG;
+  if ((fp4_bands(rows, groups, offsets != nullptr) + 1) * ((n + 255) / 256) > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  return GPTQ_OK;
+}
+
 // The workspace of gptq_fp4_linear: codes, then (each on 256 bytes) scales,
-// tensor scales and the quantiser's own.
+// tensor scales and the quantiser's own; nothing where the product quantises
+// X itself.
 struct LinearLayout {
   size_t scales, tensor, partial, total;
 };
-LinearLayout linear_layout(int64_t tokens, int n, bool nv, int groups, bool ragged) {
+LinearLayout linear_layout(int64_t tokens, int64_t rows, int n, bool nv, int groups, bool ragged) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  LinearLayout l;
+  LinearLayout l = {};
+  if (tokens == 0 || rows == 0 || fp4_linear_raw(tokens, groups, ragged, rows, n)) return l;
   l.scales = up(static_cast<size_t>(tokens) * fp4_pitch(n));
   l.tensor = l.scales + up(static_cast<size_t>(fp4_bands(tokens, groups, ragged)) * fp4_quads(n, nv) * kFp4TileBytes);
   l.partial = l.tensor + up(static_cast<size_t>(groups) * 4);
@@ -504,18 +529,10 @@ gptq_status gptq_fp4_quantize(const void* X, gptq_dtype xdt, int64_t x_rows, int
                               const int32_t* row_index, int64_t rows, const int32_t* offsets, int32_t groups,
                               gptq_fp4_format format, int32_t given, float* tensor_scale, uint8_t* packed,
                               uint8_t* scales, float* deq, void* ws, size_t ws_bytes, void* stream) {
-  if ((xdt != GPTQ_F32 && xdt != GPTQ_BF16) || !valid_format(format) || rows < 0 || rows > kMaxFp4Rows || x_rows < 0 ||
-      x_rows > kMaxFp4Rows || n < 1 || n > kMaxN || ldx < n || (given != 0 && given != 1) ||
-      !valid_groups(rows, groups, offsets != nullptr) || (row_index == nullptr && x_rows < rows))
-    return GPTQ_ERR_INVALID_ARG;
+  const gptq_status s = check_quantize(X, xdt, x_rows, n, ldx, row_index, rows, offsets, groups, format, given,
+                                       tensor_scale, packed, scales, deq);
   const bool nv = format == GPTQ_NVFP4;
-  if (nv != (tensor_scale != nullptr) || (!nv && given) || !aligned(tensor_scale, 4)) return GPTQ_ERR_INVALID_ARG;
-  if (rows > 0 && (X == nullptr || packed == nullptr || scales == nullptr)) return GPTQ_ERR_INVALID_ARG;
-  if (rows == 0 && !(nv && !given)) return GPTQ_OK;
-  if (!aligned(X, xdt == GPTQ_BF16 ? 2 : 4) || !aligned(packed, 16) || !aligned(scales, 16) || !aligned(deq, 4) ||
-      !aligned(row_index, 4) || !aligned(offsets, 4))
-    return GPTQ_ERR_INVALID_ARG;
-  if ((fp4_bands(rows, groups, offsets != nullptr) + 1) * ((n + 255) / 256) > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  if (s != GPTQ_OK || (rows == 0 && (!nv || given))) return s;  // (groups without rows have a tensor scale too)
   const size_t need = given ? 0 : fp4_quantize_workspace_size(rows, n, nv, groups, offsets != nullptr);
   if (need > 0 && (ws == nullptr || !aligned(ws, 256) || ws_bytes < need)) return GPTQ_ERR_INVALID_ARG;
   return fp4_quantize(X, xdt == GPTQ_BF16 ? 1 : 0, x_rows, n, ldx, row_index, rows, offsets, groups, nv, given,
@@ -542,12 +559,12 @@ gptq_status gptq_fp4_grouped_matmul(gptq_fp4_format format, const uint8_t* w_pac
                     ydt == GPTQ_BF16 ? 1 : 0, ldy, as_stream(stream));
 }
 
-size_t gptq_fp4_linear_workspace_size(int64_t tokens, int32_t n, gptq_fp4_format format, int32_t groups,
+size_t gptq_fp4_linear_workspace_size(int64_t tokens, int64_t rows, int32_t n, gptq_fp4_format format, int32_t groups,
                                       int32_t ragged) {
-  if (tokens < 0 || tokens > kMaxFp4Rows || n < 1 || n > kMaxN || !valid_format(format) ||
+  if (tokens < 0 || tokens > kMaxFp4Rows || rows < 0 || n < 1 || n > kMaxN || !valid_format(format) ||
       !valid_groups(tokens, groups, ragged != 0) || (ragged == 0 && groups != 1))
     return 0;
-  return linear_layout(tokens, n, format == GPTQ_NVFP4, groups, ragged != 0).total;
+  return linear_layout(tokens, rows, n, format == GPTQ_NVFP4, groups, ragged != 0).total;
 }
 
 gptq_status gptq_fp4_linear(gptq_fp4_format format, const uint8_t* w_packed, const uint8_t* w_scales,
@@ -555,24 +572,29 @@ gptq_status gptq_fp4_linear(gptq_fp4_format format, const uint8_t* w_packed, con
                             gptq_dtype xdt, int64_t x_rows, int64_t ldx, const int32_t* row_index, int64_t tokens,
                             const int32_t* offsets, const float* x_tensor, void* y, gptq_dtype ydt, int64_t ldy,
                             void* ws, size_t ws_bytes, void* stream) {
-  if (!valid_format(format) || tokens < 0 || tokens > kMaxFp4Rows || n < 1 || n > kMaxN ||
-      !valid_groups(tokens, groups, offsets != nullptr) || (offsets == nullptr && groups != 1) ||
-      (format == GPTQ_MXFP4 && x_tensor != nullptr))
+  const bool nv = format == GPTQ_NVFP4, ragged = offsets != nullptr;
+  // (stands for the quantised X where the arguments are only looked at)
+  alignas(16) static const uint8_t some[16] = {};
+  const float* some_t = nv ? reinterpret_cast<const float*>(some) : nullptr;
+  gptq_status s = check_product(format, w_packed, w_scales, w_tensor, groups, rows, n, some, some, some_t, tokens, y, ydt, ldy);
+  if (s != GPTQ_OK) return s;
+  if (!valid_groups(tokens, groups, ragged) || (!ragged && groups != 1) || (!nv && x_tensor != nullptr))
     return GPTQ_ERR_INVALID_ARG;
-  const bool nv = format == GPTQ_NVFP4;
-  const LinearLayout l = linear_layout(tokens, n, nv, groups, offsets != nullptr);
-  if (tokens > 0 && rows > 0 && (ws == nullptr || !aligned(ws, 256) || ws_bytes < l.total)) return GPTQ_ERR_INVALID_ARG;
+  s = check_quantize(X, xdt, x_rows, n, ldx, row_index, tokens, offsets, groups, format, x_tensor != nullptr ? 1 : 0,
+                     nv ? (x_tensor != nullptr ? x_tensor : some_t) : nullptr, some, some, nullptr);
+  if (s != GPTQ_OK || rows == 0 || tokens == 0) return s;
+  const LinearLayout l = linear_layout(tokens, rows, n, nv, groups, ragged);
+  if (l.total == 0)
+    return fp4_raw_matmul(nv, w_packed, w_scales, w_tensor, groups, rows, n, X, xdt == GPTQ_BF16 ? 1 : 0, x_rows, ldx,
+                          row_index, x_tensor, tokens, offsets, y, ydt == GPTQ_BF16 ? 1 : 0, ldy, as_stream(stream));
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < l.total) return GPTQ_ERR_INVALID_ARG;
   uint8_t* base = static_cast<uint8_t*>(ws);
   uint8_t* xq = base;
   uint8_t* xs = base + l.scales;
   float* xt = !nv ? nullptr : x_tensor != nullptr ? const_cast<float*>(x_tensor) : reinterpret_cast<float*>(base + l.tensor);
-  // every argument is checked before the first launch
-  const gptq_status s = check_product(format, w_packed, w_scales, w_tensor, groups, rows, n, xq, xs, xt, tokens, y, ydt, ldy);
-  if (s != GPTQ_OK || rows == 0 || tokens == 0) return s;
-  const gptq_status q = gptq_fp4_quantize(X, xdt, x_rows, n, ldx, row_index, tokens, offsets, groups, format,
-                                          x_tensor != nullptr ? 1 : 0, xt, xq, xs, nullptr, base + l.partial,
-                                          l.total - l.partial, stream);
-  if (q != GPTQ_OK) return q;
+  s = fp4_quantize(X, xdt == GPTQ_BF16 ? 1 : 0, x_rows, n, ldx, row_index, tokens, offsets, groups, nv,
+                   x_tensor != nullptr ? 1 : 0, xt, xq, xs, nullptr, base + l.partial, as_stream(stream));
+  if (s != GPTQ_OK) return s;
   return fp4_matmul(nv, w_packed, w_scales, w_tensor, groups, rows, n, xq, xs, xt, tokens, offsets, y,
                     ydt == GPTQ_BF16 ? 1 : 0, ldy, as_stream(stream));
 }

@@ -19,7 +19,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "fp4.cuh"
+#include "fp4_quant.cuh"
 
 namespace gptq {
 namespace {
@@ -114,7 +114,7 @@ struct Tile {
   int token;      // first token (row of X)
   int count;      // tokens of the tile
   int cols;       // MMA columns: count rounded up to 16
-  int64_t xband;  // first band of X's scales
+  int xband;      // first band of X's scales
   int xcol;       // tensor-memory column (32 tokens each) of the first token in that band
   int wtile;      // tile of W's rows in the group
 };
@@ -125,11 +125,20 @@ struct Scale {
   float k;
   float before;  // 1 where k is the product
 };
-__device__ __forceinline__ Scale tile_scale(const MatmulArgs& a, int g) {
-  if (a.wt == nullptr) return {1.0f, 1.0f};
-  const float tw = a.wt[g], tx = a.xt[g], k = tw * tx;
+__device__ __forceinline__ Scale make_scale(float tw, float tx) {
+  const float k = tw * tx;
   if (k >= 1.17549435e-38f && k <= 3.40282347e38f) return {k, 1.0f};
   return {tx, tw};
+}
+__device__ __forceinline__ Scale tile_scale(const MatmulArgs& a, int g) {
+  return a.wt == nullptr ? Scale{1.0f, 1.0f} : make_scale(a.wt[g], a.xt[g]);
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
@@ -160,33 +169,39 @@ __device__ __forceinline__ void store_four(__nv_bfloat16* p, float4 v, Scale k, 
   }
 }
 
-// One group of all tokens, or the groups of the offsets, in tiles of `width`.
-__device__ __forceinline__ bool group_table(const GroupTable& t, const MatmulArgs& a, int width) {
-  if (a.offsets != nullptr) {
-    const bool ok = build_groups(t, a.offsets, a.groups, a.tokens, width);
-    if (!ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, GPTQ_ERR_INVALID_ARG);
-    return ok;
-  }
-  if (threadIdx.x == 0) {
-    t.off[0] = t.band[0] = t.tile[0] = 0;
-    t.off[1] = static_cast<int>(a.tokens);
-    t.band[1] = static_cast<int>((a.tokens + kFp4Band - 1) / kFp4Band);
-    t.tile[1] = static_cast<int>((a.tokens + width - 1) / width);
-  }
-  __syncthreads();
-  return true;
+// The groups of the offsets in tiles of `width`; without offsets there is one
+// group of all tokens, and no table.  `tiles`: token tiles of all groups.
+__device__ __forceinline__ bool group_table(const GroupTable& t, const MatmulArgs& a, int width, int& tiles) {
+  tiles = static_cast<int>((a.tokens + width - 1) / width);
+  if (a.offsets == nullptr) return true;
+  const bool ok = build_groups(t, a.offsets, a.groups, a.tokens, width);
+  if (!ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, GPTQ_ERR_INVALID_ARG);
+  tiles = t.tile[a.groups];
+  return ok;
 }
 
-__device__ __forceinline__ Tile tile_at(const GroupTable& t, const MatmulArgs& a, int wtiles, int width, int64_t item) {
+// Items count token tiles first, then row tiles; the host has checked that
+// there are less than 2^31.
+__device__ __forceinline__ Tile tile_at(const GroupTable& t, const MatmulArgs& a, int wtiles, int width, uint32_t item) {
   Tile x;
   const int tt = static_cast<int>(item / wtiles);
-  x.wtile = static_cast<int>(item - static_cast<int64_t>(tt) * wtiles);
-  x.g = find_group(t.tile, a.groups, tt);
-  const int first = (tt - t.tile[x.g]) * width;  // of the group's rows
-  x.token = t.off[x.g] + first;
-  x.count = min(width, t.off[x.g + 1] - x.token);
+  x.wtile = static_cast<int>(item - tt * wtiles);
+  int first, last;
+  if (a.offsets == nullptr) {
+    x.g = 0;
+    first = tt * width;
+    x.token = first;
+    last = static_cast<int>(a.tokens);
+    x.xband = first / kFp4Band;
+  } else {
+    x.g = find_group(t.tile, a.groups, tt);
+    first = (tt - t.tile[x.g]) * width;  // of the group's rows
+    x.token = t.off[x.g] + first;
+    last = t.off[x.g + 1];
+    x.xband = t.band[x.g] + first / kFp4Band;
+  }
+  x.count = min(width, last - x.token);
   x.cols = (x.count + 15) / 16 * 16;
-  x.xband = t.band[x.g] + first / kFp4Band;
   x.xcol = first % kFp4Band / 32;
   return x;
 }
@@ -197,40 +212,134 @@ __device__ __forceinline__ Tile tile_at(const GroupTable& t, const MatmulArgs& a
 // ---------------------------------------------------------------------------
 //
 // Bound by HBM: each weight is read once (128 * 4096 codes and their scales
-// are 288 KB of nvfp4).  Two CTAs share an SM, so that one streams while the
-// other starts or ends, and a layer with too few row tiles for the chip is cut
-// along K; the cluster's CTAs then add up their sums in rank order through
-// each other's shared memory, so the result does not depend on timing.
+// are 288 KB of nvfp4).  Two or three CTAs share an SM, so that one streams
+// while another starts or ends, and a layer with too few row tiles for the
+// chip is cut along K.  The cluster's CTAs then add up their sums in rank
+// order, so the result does not depend on timing: of a few tokens each CTA
+// sends its sums to the one that owns the token, as asynchronous stores that
+// the owner's barrier counts; of many the owner reads them from the others.
+//
+// RAW: X is not quantised yet (gptq_fp4_linear of a few tokens).  The epilogue
+// warps then quantise the CTA's K range of its tokens into shared memory
+// while the first weights arrive, which costs less than a launch in between.
 
 constexpr int kStreamThreads = 192;  // producer, MMA, 4 epilogue warps
 constexpr int kStreamMaxStages = 4;
+constexpr int kPushTokens = 16;      // up to here sums are sent (an MMA's least columns)
+constexpr int kRawTokens = 16;       // of a RAW tile: one MMA's least columns
+constexpr int kRawMaxStages = 8;     // of a RAW CTA's K range
+constexpr int kRawStageBytes = kRawTokens * kStageK / 2 + kSfBytes;
 
 struct StreamShape {
   int width;   // tokens of a tile: 16, 32, 64 or 128
   int stages;
   int splits;  // CTAs of a cluster
+  int raw_stages;  // RAW: most stages of a CTA's K range
 };
-__host__ __device__ inline int stream_stage_bytes(int width) {
-  return kABytes + (width < kBoxRows ? kBoxRows : width) * (kStageK / 2) + 2 * kSfBytes;
+__host__ __device__ inline int stream_stage_bytes(int width, bool raw) {
+  return kABytes + (raw ? 0 : (width < kBoxRows ? kBoxRows : width) * (kStageK / 2) + kSfBytes) + kSfBytes;
 }
 __host__ __device__ inline int table_bytes(int groups) { return 3 * (groups + 1) * 4; }
+// Shared memory in which a CTA of a split collects sums: for each of the
+// `splits` sources the same number of rows of 128 floats (so up to splits - 1
+// rows more than the tokens).  Up to 32 tokens it stands apart; more use the
+// operand ring again, which is larger than 128 rows.
+__host__ __device__ inline int stream_apart_bytes(int width, int splits) {
+  const int bytes = splits * ((width + splits - 1) / splits) * kRows * 4;
+  return splits > 1 && width <= 32 ? (bytes + 1023) / 1024 * 1024 : 0;  // (an operand may follow)
+}
+// Tensor memory of a CTA: the accumulator and 32 scale columns a stage.
+__host__ __device__ inline uint32_t stream_tmem_cols(int width, int stages) { return width + 32 * stages > 128 ? 256 : 128; }
+constexpr size_t kStreamMaxSmem = 1024 + 4 * (2 * kABytes + 2 * kSfBytes) + 256 + 12 * (kFp4MaxGroups + 1);
 
-constexpr size_t kStreamMaxSmem = 1024 + 3 * (2 * kABytes + 2 * kSfBytes) + 128 + 12 * (kFp4MaxGroups + 1);
+// The epilogue warps' part of a RAW tile: x.count tokens, stages [k0, k1) of K,
+// as B operand rows (128-byte swizzle) and scale tiles, stage by stage at
+// `dst`.  Returns the tensor scale.  `src`: the tokens' rows of X, `red`: 4
+// words.
+template <bool BF16, bool NV>
+__device__ __forceinline__ float quantize_tile(const QuantArgs& a, const Tile& x, int k0, int k1, uint8_t* dst, int* src,
+                                               uint32_t* red) {
+  using S = Fp4Lane<BF16, NV>;
+  constexpr int kSize = BF16 ? 2 : 4, kAcross = kStageK / S::kLane;
+  const int tid = threadIdx.x - 64;
+  auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+  if (tid < x.count) src[tid] = source_row(a, x.token + tid);
+  sync();
+  const char* X = static_cast<const char*>(a.X);
+  Unit u{1.0f, 1.0f, 1.0f, true};
+  if (NV) {
+    float t;
+    if (a.given) {
+      t = a.tensor_scale[x.g];
+    } else {
+      const int across = (a.n + S::kLane - 1) / S::kLane;
+      uint32_t m = thread_max<BF16, false, 4>(a, tid, 128, x.count * across, [&](int i, int& left) -> const char* {
+        const int r = i / across, col = (i - r * across) * S::kLane, row = src[r];
+        left = a.n - col;
+        return row < 0 ? nullptr : X + (row * a.ldx + col) * kSize;
+      });
+      m = __reduce_max_sync(0xffffffffu, m);
+      if (tid % 32 == 0) red[tid / 32] = m;
+      sync();
+      m = max(max(red[0], red[1]), max(red[2], red[3]));
+      t = fmaxf(__fdiv_rn(__uint_as_float(m), 2688.0f), FLT_MIN);
+    }
+    u = unit_of(t);
+  }
+  const int wide = (k1 - k0) * kAcross;  // a multiple of 32 or 16, so a block's lanes stay together
+  for (int i0 = 0; i0 < x.count * wide; i0 += 128) {
+    const int i = i0 + tid, r = i / wide, c = i - r * wide;
+    const bool in = r < x.count;
+    const int col = k0 * kStageK + c * S::kLane, left = a.n - col;
+    const int row = in ? src[r] : -1;
+    const char* p = row < 0 || left <= 0 ? nullptr : X + (row * a.ldx + col) * kSize;
+    uint32_t w[8];
+    if (p != nullptr) {
+      load_lane<BF16, false>(p, left, a.align, w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = 0;
+    }
+    uint32_t codes[S::kLane / 8], byte;
+    float s;
+    quantize_lane<BF16, NV>(w, p, u, codes, byte, s);
+    if (in) {
+      uint8_t* stage = dst + c / kAcross * kRawStageBytes;
+      const int at = c % kAcross * (S::kLane / 2);  // byte of the row's 128
+      uint8_t* d = stage + r * (kStageK / 2) + ((at / 16) ^ (r % 8)) * 16 + at % 16;
+      if (BF16)
+        *reinterpret_cast<uint2*>(d) = make_uint2(codes[0], codes[S::kLane / 8 - 1]);
+      else
+        *reinterpret_cast<uint32_t*>(d) = codes[0];
+      const int b = c % kAcross / S::kLanes;  // block of the stage; past the row's end it has scale 0
+      if (c % S::kLanes == 0)
+        stage[kRawTokens * (kStageK / 2) + b / 4 * kFp4TileBytes + r * 16 + b % 4] = static_cast<uint8_t>(left > 0 ? byte : 0);
+    }
+  }
+  fence_proxy_async();  // the tensor cores and their copies read it
+  return u.t;
+}
 
-template <bool NV, typename OUT>
-__global__ void __launch_bounds__(kStreamThreads, 2)
-    fp4_stream_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                      const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap, MatmulArgs a,
-                      StreamShape shape) {
+// RAW: 0 X is quantised; 1 bf16, 2 fp32 X of q.
+template <bool NV, typename OUT, int RAW>
+__global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
+    fp4_stream_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, MatmulArgs a,
+                      StreamShape shape, QuantArgs q) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int stage_bytes = stream_stage_bytes(shape.width), bbytes = stage_bytes - kABytes - 2 * kSfBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + shape.stages * stage_bytes);
+  const int stage_bytes = stream_stage_bytes(shape.width, RAW != 0);
+  const int bbytes = RAW ? 0 : stage_bytes - kABytes - 2 * kSfBytes;  // of a stage's tokens, before its scales
+  const int apart = stream_apart_bytes(shape.width, shape.splits);
+  uint8_t* collect = apart > 0 ? smem + shape.stages * stage_bytes : smem;
+  uint8_t* raw = smem + shape.stages * stage_bytes + apart;
+  uint64_t* full = reinterpret_cast<uint64_t*>(raw + (RAW ? shape.raw_stages * kRawStageBytes : 0));
   uint64_t* empty = full + kStreamMaxStages;
   uint64_t* acc_full = empty + kStreamMaxStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  uint64_t* sums_in = acc_full + 1;  // the cluster's sums for this CTA's tokens have arrived
+  uint64_t* x_ready = sums_in + 1;   // RAW: the tokens are quantised
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(x_ready + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* table = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 128);
+  int* table = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);
   const GroupTable t{table, table + a.groups + 1, table + 2 * (a.groups + 1)};
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
@@ -239,7 +348,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   constexpr int kStageQuads = kStageK / (4 * kBlk);
   constexpr int kQuadMmas = kBlk / 16;
   constexpr uint32_t kStageSf = kStageQuads * kFp4TileBytes;
-  const uint32_t tmem_cols = shape.width + shape.stages * 32 > 128 ? 256 : 128;
+  const uint32_t tmem_cols = stream_tmem_cols(shape.width, shape.stages);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < shape.stages; ++s) {
@@ -247,12 +356,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       mbar_init(empty + s, 1);
     }
     mbar_init(acc_full, 1);
+    mbar_init(sums_in, 1);
+    mbar_init(x_ready, 128);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&wmap);
-    prefetch_tensormap(&xmap);
-    prefetch_tensormap(&wsmap);
-    prefetch_tensormap(&xsmap);
+    if (!RAW) prefetch_tensormap(&xmap);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, tmem_cols);
@@ -262,12 +371,15 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // (the cluster's barriers exist once all have arrived; waited for before the first use across it)
+  if (shape.splits > 1) cluster_arrive();
   pdl_trigger();
   pdl_wait();
-  const bool ok_groups = group_table(t, a, shape.width);
+  int tiles;
+  const bool ok_groups = group_table(t, a, shape.width, tiles);
   const int wtiles = static_cast<int>((a.rows + kRows - 1) / kRows);
-  const int64_t items = ok_groups ? static_cast<int64_t>(t.tile[a.groups]) * wtiles : 0;
-  const int64_t item = blockIdx.x / shape.splits;
+  const uint32_t items = ok_groups ? static_cast<uint32_t>(tiles) * wtiles : 0;
+  const uint32_t item = blockIdx.x / shape.splits;
   const int rank = blockIdx.x % shape.splits;  // in the cluster
   const int quads = fp4_quads(a.n, NV);
   const int mmas = (a.n + 63) / 64;
@@ -280,24 +392,30 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 
   if (item < items) {
     const Tile x = tile_at(t, a, wtiles, shape.width, item);
+    const bool push = x.count <= kPushTokens;  // (the same in the whole cluster)
     if (warp == 0) {
       if (elect_one()) {
         // ---------------- producer ----------------
-        const int boxes = (x.cols + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = kABytes + boxes * kBoxBytes + 2 * kStageSf;
-        const int wy = static_cast<int>(x.g * a.rows) + x.wtile * kRows, wband = x.g * wtiles + x.wtile;
+        const int boxes = RAW ? 0 : (x.cols + kBoxRows - 1) / kBoxRows;
+        const int wy = static_cast<int>(x.g * a.rows) + x.wtile * kRows;
+        const uint8_t* wsc = a.wscales + (static_cast<int64_t>(x.g) * wtiles + x.wtile) * quads * kFp4TileBytes;
+        const uint8_t* xsc = a.xscales + static_cast<int64_t>(x.xband) * quads * kFp4TileBytes;
         uint32_t stage = 0, phase = 0;
         int issued = 0;
         for (int kb = k0; kb < k1; ++kb, ++issued) {
           if (!wait(empty + stage, phase ^ 1u)) break;
           uint8_t* sa = smem + stage * stage_bytes;
           uint8_t* sf = sa + kABytes + bbytes;
-          mbar_arrive_expect_tx(full + stage, bytes);
+          const uint32_t sf_bytes = min(kStageQuads, quads - kb * kStageQuads) * kFp4TileBytes;
+          const int64_t sf_at = static_cast<int64_t>(kb) * kStageSf;
+          mbar_arrive_expect_tx(full + stage, kABytes + boxes * kBoxBytes + (RAW ? 1 : 2) * sf_bytes);
           tma_load_2d(sa, &wmap, full + stage, kb * (kStageK / 2), wy);
-          tma_load_3d(sf, &wsmap, full + stage, 0, kb * kStageQuads, wband);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(sa + kABytes + b * kBoxBytes, &xmap, full + stage, kb * (kStageK / 2), x.token + b * kBoxRows);
-          tma_load_3d(sf + kStageSf, &xsmap, full + stage, 0, kb * kStageQuads, static_cast<int>(x.xband));
+          bulk_load(sf, wsc + sf_at, sf_bytes, full + stage);
+          if (!RAW) {
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d(sa + kABytes + b * kBoxBytes, &xmap, full + stage, kb * (kStageK / 2), x.token + b * kBoxRows);
+            bulk_load(sf + kStageSf, xsc + sf_at, sf_bytes, full + stage);
+          }
           if (++stage == static_cast<uint32_t>(shape.stages)) {
             stage = 0;
             phase ^= 1u;
@@ -315,15 +433,17 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         const uint32_t idesc = fp4_idesc(NV, 1, x.cols, 0);
         const uint32_t pair_bits = fp4_idesc(NV, 1, 0, 1) ^ fp4_idesc(NV, 1, 0, 0);
         const int whole = mmas / (kStageK / 64);
-        for (int kb = k0; kb < k1; ++kb) {
+        const bool x_ok = !RAW || wait(x_ready, 0u);
+        for (int kb = k0; kb < k1 && x_ok; ++kb) {
           if (!wait(full + stage, phase)) break;
           tc_fence_after();
           const uint32_t sa = ring + stage * stage_bytes;
-          const uint32_t ssa = sa + kABytes + bbytes, ssb = ssa + kStageSf;
+          const uint32_t sb = RAW ? smem_u32(raw) + (kb - k0) * kRawStageBytes : sa + kABytes;
+          const uint32_t ssa = sa + kABytes + bbytes, ssb = RAW ? sb + kRawTokens * (kStageK / 2) : ssa + kStageSf;
           // each ring stage has its own scale columns, 16 of W's and 16 of X's:
           // the stage is full again only after the products that read them
           const uint32_t tsa = tmem + shape.width + stage * 32, tsb = tsa + 16, tsx = tsb + x.xcol;
-          const uint64_t adesc = smem_desc_sw128(sa, 16, 1024), bdesc = smem_desc_sw128(sa + kABytes, 16, 1024);
+          const uint64_t adesc = smem_desc_sw128(sa, 16, 1024), bdesc = smem_desc_sw128(sb, 16, 1024);
           if (kb < whole) {
 #pragma unroll
             for (int i = 0; i < kStageQuads; ++i) {
@@ -356,73 +476,130 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     } else {
       // ---------------- epilogue ----------------
       const int quad = warp & 3;  // the tensor-memory lanes of this warp
-      int ok = 1;
-      if (lane == 0) ok = wait(acc_full, 0u);
-      ok = __shfl_sync(0xffffffffu, ok, 0) && !*abort_flag;
-      const int64_t r = static_cast<int64_t>(x.wtile) * kRows + quad * 32 + lane;
-      if (ok) {
-        tc_fence_after();
-        const Scale k = tile_scale(a, x.g);
-        OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
-        // (the ring is free: the products that read it are complete)
-        float* sums = reinterpret_cast<float*>(smem) + quad * 32 + lane;
-#pragma unroll 1
-        for (int c = 0; c < x.count; c += 32) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, v);
-          tmem_ld_wait();
-          if (shape.splits > 1) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < x.count) sums[(c + j) * kRows] = __uint_as_float(v[j]);
-          } else if (r < a.rows) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < x.count)
-                store_out(out + static_cast<int64_t>(c + j) * a.ldy, __uint_as_float(v[j]) * k.before * k.k);
-          }
-        }
-        tc_fence_before();
+      const int f = quad * 32 + lane;
+      float tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
+      if (RAW) {
+        tx = quantize_tile<RAW == 1, NV>(q, x, k0, k1, raw, reinterpret_cast<int*>(full) + 24, reinterpret_cast<uint32_t*>(full) + 40);
+        mbar_arrive(x_ready);
       }
-    }
-    __syncwarp();
-    if (shape.splits > 1) {
-      cluster_sync_all();
-      // A token's sums over the ranks, in rank order: a warp a token, a lane
-      // four features, four tokens in flight.  A CTA that gave up has no sums:
-      // the status word says so.
-      if (warp >= 2) {
-        const int64_t r = static_cast<int64_t>(x.wtile) * kRows + 4 * lane;
-        const Scale k = tile_scale(a, x.g);
-        OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
-        const bool vec = r + 4 <= a.rows && a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
-        uint32_t peer[8];
+      const Scale k = make_scale(a.wt != nullptr ? a.wt[x.g] : 1.0f, tx);
+      const int64_t r = static_cast<int64_t>(x.wtile) * kRows + f;
+      OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
+      int ok = 1;
+      if (lane == 0) ok = wait(acc_full, 0u) && !*abort_flag;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      tc_fence_after();
+      if (shape.splits == 1) {
+        if (ok) {
+#pragma unroll 1
+          for (int c = 0; c < x.count; c += 16) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, v);
+            tmem_ld_wait();
+            if (r < a.rows) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) peer[q] = smem_cluster_addr(smem, min(q, shape.splits - 1)) + 16 * lane;
-        const int step = 4 * shape.splits;  // the cluster's epilogue warps
-        for (int j0 = 4 * rank + warp - 2; j0 < x.count; j0 += 4 * step) {
-          float4 v[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (j0 + u * step < x.count) v[u] = ld_cluster_f32x4(peer[0] + (j0 + u * step) * kRows * 4);
-#pragma unroll
-          for (int q = 1; q < 8; ++q) {
-            if (q < shape.splits) {
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                if (j0 + u * step < x.count) {
-                  const float4 p = ld_cluster_f32x4(peer[q] + (j0 + u * step) * kRows * 4);
-                  v[u] = make_float4(v[u].x + p.x, v[u].y + p.y, v[u].z + p.z, v[u].w + p.w);
-                }
+              for (int j = 0; j < 16; ++j)
+                if (c + j < x.count)
+                  store_out(out + static_cast<int64_t>(c + j) * a.ldy, __uint_as_float(v[j]) * k.before * k.k);
             }
           }
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (j0 + u * step < x.count) store_four(out + static_cast<int64_t>(j0 + u * step) * a.ldy, v[u], k, vec, a.rows - r);
         }
+      } else {
+        // Token j belongs to rank j % splits, where it is row j / splits.  (A
+        // CTA that gave up passes on what its accumulator holds, as the others
+        // wait for it; the status word says that the result is not one.)
+        const int mine = (x.count - rank + shape.splits - 1) / shape.splits;
+        const int rows_each = (x.count + shape.splits - 1) / shape.splits;
+        if (push && warp == 2 && lane == 0) mbar_arrive_expect_tx(sums_in, mine * shape.splits * kRows * 4);
+        __syncwarp();
+        cluster_wait();  // every CTA's barriers exist
+        if (push) {
+          if (apart == 0) {  // the other CTAs' rings are free
+            cluster_arrive();
+            cluster_wait();
+          }
+          // the sums of source rank q stand at [q][row][feature]
+          const uint32_t at = smem_u32(collect) + (rank * rows_each * kRows + f) * 4, bar = smem_u32(sums_in);
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16), v);
+          tmem_ld_wait();
+          int owner = 0, row = 0;
+#pragma unroll
+          for (int j = 0; j < kPushTokens; ++j) {
+            if (j < x.count) st_async(at + row * kRows * 4, bar, owner, v[j]);
+            if (++owner == shape.splits) {
+              owner = 0;
+              ++row;
+            }
+          }
+          cluster_arrive();
+          if (lane == 0) ok = wait(sums_in, 0u) && ok;
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (ok && r < a.rows) {
+            const float* sums = reinterpret_cast<const float*>(collect) + f;
+            for (int j = 0; j < mine; ++j) {
+              float v = sums[j * kRows];
+#pragma unroll
+              for (int p = 1; p < 8; ++p)
+                if (p < shape.splits) v += sums[(p * rows_each + j) * kRows];
+              store_out(out + static_cast<int64_t>(j * shape.splits + rank) * a.ldy, v * k.before * k.k);
+            }
+          }
+        } else {
+          // this CTA's sums at [token][feature]; then a warp a token, a lane
+          // four features, four tokens in flight
+          float* sums = reinterpret_cast<float*>(collect) + f;
+#pragma unroll 1
+          for (int c = 0; c < x.count; c += 16) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < x.count) sums[(c + j) * kRows] = __uint_as_float(v[j]);
+          }
+          cluster_arrive();
+          cluster_wait();
+          const int64_t r4 = static_cast<int64_t>(x.wtile) * kRows + 4 * lane;
+          OUT* o4 = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r4;
+          const bool vec = r4 + 4 <= a.rows && a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+          const int step = 4 * shape.splits;  // the cluster's epilogue warps
+          for (int j0 = 4 * rank + warp - 2; j0 < x.count; j0 += 4 * step) {
+            float4 v[4];
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+              if (p < shape.splits) {
+                const uint32_t peer = smem_cluster_addr(collect, p) + 16 * lane;
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                  if (j0 + w * step < x.count) {
+                    const float4 z = ld_cluster_f32x4(peer + (j0 + w * step) * kRows * 4);
+                    v[w] = p == 0 ? z : make_float4(v[w].x + z.x, v[w].y + z.y, v[w].z + z.z, v[w].w + z.w);
+                  }
+              }
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if (j0 + w * step < x.count) store_four(o4 + static_cast<int64_t>(j0 + w * step) * a.ldy, v[w], k, vec, a.rows - r4);
+          }
+          cluster_arrive();
+        }
+        cluster_wait();  // no CTA leaves while another may still use its memory
       }
-      cluster_sync_all();  // no CTA leaves while another reads its sums
+      tc_fence_before();
     }
+    __syncwarp();
+    if (shape.splits > 1 && warp < 2) {  // the barriers of the epilogue
+      cluster_wait();
+      if (!push || apart == 0) {
+        cluster_arrive();
+        cluster_wait();
+      }
+      cluster_arrive();
+      cluster_wait();
+    }
+  } else if (shape.splits > 1) {
+    cluster_wait();
   }
   tc_fence_before();
   __syncthreads();
@@ -548,7 +725,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // the same register for the whole warp
   const int lane = threadIdx.x % 32;
   const uint32_t rank = uniform(cluster_ctarank());
-  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const uint32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   constexpr int kBlk = NV ? 16 : 32;
   constexpr int kStageQuads = kStageK / (4 * kBlk);
   constexpr int kQuadMmas = kBlk / 16;
@@ -581,15 +758,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = uniform(*tmem_slot);
   pdl_trigger();
   pdl_wait();
-  const bool ok_groups = group_table(t, a, kTokens);
+  int token_tiles;
+  const bool ok_groups = group_table(t, a, kTokens, token_tiles);
   const int wtiles = static_cast<int>((a.rows + kPairRows - 1) / kPairRows);
   const int wbands = static_cast<int>((a.rows + kRows - 1) / kRows);
-  const int64_t items = ok_groups ? static_cast<int64_t>(uniform(t.tile[a.groups])) * wtiles : 0;
+  const uint32_t items = ok_groups ? static_cast<uint32_t>(token_tiles) * wtiles : 0;
   const int quads = fp4_quads(a.n, NV);
   const int mmas = (a.n + 63) / 64;
   const int kstages = (a.n + kStageK - 1) / kStageK;
 
-  auto tile_of = [&](int64_t item) { return tile_at(t, a, wtiles, kTokens, item); };
+  auto tile_of = [&](uint32_t item) { return tile_at(t, a, wtiles, kTokens, item); };
   // A single thread's wait.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, a.wait_ns, abort_flag, a.status);
@@ -601,7 +779,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
       const uint32_t full0 = smem_cluster_addr(full, 0);  // the even CTA's barriers
       bool ok = true;
-      for (int64_t item = pair; ok && item < items; item += pairs) {
+      for (uint32_t item = pair; ok && item < items; item += pairs) {
         const Tile x = tile_of(item);
         const int half = x.cols / 2;  // tokens of this CTA
         // one box of 128 rows, or boxes of 32 where that loads no more
@@ -609,7 +787,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t bytes = 2 * (kABytes + (boxes == 0 ? kPairBBytes : boxes * kBoxBytes) + 3 * kStageSf);
         // the odd CTA's rows may not exist: it then loads the last band's scales for nothing
         const int wband = x.g * wbands + min(2 * x.wtile + static_cast<int>(rank), wbands - 1);
-        const int xband = static_cast<int>(x.xband);
+        const int xband = x.xband;
         const int wy = static_cast<int>(x.g * a.rows) + x.wtile * kPairRows + static_cast<int>(rank) * kRows;
         const int xy = x.token + static_cast<int>(rank) * half;
         for (int kb = 0; kb < kstages; ++kb) {
@@ -661,7 +839,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         return true;
       };
       bool ok = true;
-      for (int64_t item = pair; ok && item < items; item += pairs, ++tiles) {
+      for (uint32_t item = pair; ok && item < items; item += pairs, ++tiles) {
         const Tile x = tile_of(item);
         const uint32_t idesc = fp4_idesc(NV, 2, x.cols, 0);
         const uint32_t acc = tmem + (tiles & 1u) * kAccShift;
@@ -724,7 +902,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int turn = (warp - 2) >> 2;     // which of the two warps with these lanes
     const Out o{&ymap, a.y_tma != 0, staging + (warp - 2) * kStageOutBytes, a.ldy};
     uint32_t tiles = 0;
-    for (int64_t item = pair; item < items; item += pairs, ++tiles) {
+    for (uint32_t item = pair; item < items; item += pairs, ++tiles) {
       const Tile x = tile_of(item);
       int ok = 1;
       if (lane == 0) ok = wait(acc_full, tiles & 1u);
@@ -784,6 +962,7 @@ StreamShape stream_shape(int64_t tokens, int groups, bool ragged, int64_t rows, 
   const int64_t each = ragged ? std::max<int64_t>(64, 2 * ceil_div(tokens, groups)) : tokens;
   s.width = each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : 128;
   s.stages = s.width <= 32 ? 4 : 3;
+  s.raw_stages = 0;
   const int kstages = static_cast<int>(ceil_div(n, kStageK));
   const int64_t tiles = (ragged ? std::min<int64_t>(groups, tokens) : ceil_div(tokens, s.width)) * ceil_div(rows, kRows);
   int64_t best = INT64_MAX;
@@ -799,25 +978,26 @@ StreamShape stream_shape(int64_t tokens, int groups, bool ragged, int64_t rows, 
   return s;
 }
 
-template <bool NV, typename OUT>
-gptq_status launch_stream(const CUtensorMap& wmap, const CUtensorMap& xmap, const CUtensorMap& wsmap,
-                          const CUtensorMap& xsmap, const MatmulArgs& a, const DeviceInfo* info, cudaStream_t st) {
+template <bool NV, typename OUT, int RAW>
+gptq_status launch_stream(const CUtensorMap& wmap, const CUtensorMap& xmap, const MatmulArgs& a, const StreamShape& s,
+                          const QuantArgs& q, const DeviceInfo* info, cudaStream_t st) {
   static std::atomic<bool> attr_set[64] = {};  // per device, shared by host threads
   if (!attr_set[info->device]) {
-    if (cudaFuncSetAttribute(fp4_stream_kernel<NV, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(fp4_stream_kernel<NV, OUT, RAW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kStreamMaxSmem)) != cudaSuccess)
       return GPTQ_ERR_CUDA;
     attr_set[info->device] = true;
   }
-  const bool ragged = a.offsets != nullptr;
-  const StreamShape s = stream_shape(a.tokens, a.groups, ragged, a.rows, a.n, info->sm_count);
   // token tiles: each group's last one may be part full
-  const int64_t tiles = ragged ? a.tokens / s.width + std::min<int64_t>(a.groups, a.tokens) : ceil_div(a.tokens, s.width);
+  const int64_t tiles =
+      a.offsets != nullptr ? a.tokens / s.width + std::min<int64_t>(a.groups, a.tokens) : ceil_div(a.tokens, s.width);
   const int64_t ctas = tiles * ceil_div(a.rows, kRows) * s.splits;
   if (ctas > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-  const size_t smem = 1024 + static_cast<size_t>(s.stages) * stream_stage_bytes(s.width) + 128 + table_bytes(a.groups);
-  return launch_cluster_pdl(fp4_stream_kernel<NV, OUT>, static_cast<unsigned>(ctas), kStreamThreads, smem, s.splits, st,
-                            wmap, xmap, wsmap, xsmap, a, s) == cudaSuccess
+  const size_t smem = 1024 + static_cast<size_t>(s.stages) * stream_stage_bytes(s.width, RAW != 0) +
+                      stream_apart_bytes(s.width, s.splits) + (RAW ? s.raw_stages * kRawStageBytes : 0) + 256 +
+                      table_bytes(a.groups);
+  return launch_cluster_pdl(fp4_stream_kernel<NV, OUT, RAW>, static_cast<unsigned>(ctas), kStreamThreads, smem, s.splits,
+                            st, wmap, xmap, a, s, q) == cudaSuccess
              ? launch_status()
              : GPTQ_ERR_CUDA;
 }
@@ -837,6 +1017,7 @@ gptq_status launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const 
   // token tiles: each group's last one may be part full
   const int64_t tiles = ragged ? a.tokens / kTokens + std::min<int64_t>(a.groups, a.tokens) : ceil_div(a.tokens, kTokens);
   const int64_t items = tiles * ceil_div(a.rows, kPairRows);
+  if (items > INT32_MAX - 2 * info->sm_count) return GPTQ_ERR_UNSUPPORTED;
   const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(items, std::max(1, info->sm_count / 2)));
   return launch_cluster_pdl(fp4_pair_kernel<NV, OUT>, grid, kPairThreads, kPairSmemBytes + table_bytes(a.groups), 2, st, wmap, xmap, xwide, wsmap,
                             xsmap, ymap, a) == cudaSuccess
@@ -855,23 +1036,12 @@ bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t quads, int64_t b
 
 }  // namespace
 
-gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const float* wt, int groups, int64_t rows,
-                       int n, const uint8_t* xq, const uint8_t* xscales, const float* xt, int64_t tokens,
-                       const int32_t* offsets, void* y, int y_bf16, int64_t ldy, cudaStream_t st) {
-  const DeviceInfo* info = device_info();
-  if (info == nullptr) return GPTQ_ERR_CUDA;
-  const int64_t pitch = fp4_pitch(n);
-  CUtensorMap wmap, xmap;
-  if (!make_tensor_map_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, pitch, static_cast<uint64_t>(groups) * rows, pitch,
-                          kStageK / 2, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tensor_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, pitch, tokens, pitch, kStageK / 2, kBoxRows,
-                          CU_TENSOR_MAP_SWIZZLE_128B))
-    return GPTQ_ERR_CUDA;
-  MatmulArgs a;
+// A product's arguments but for X's.
+static MatmulArgs product_args(const uint8_t* wscales, const float* wt, int groups, int64_t rows, int n, int64_t tokens,
+                               const int32_t* offsets, void* y, int64_t ldy, const DeviceInfo* info) {
+  MatmulArgs a = {};
   a.wscales = wscales;
-  a.xscales = xscales;
   a.wt = wt;
-  a.xt = xt;
   a.offsets = offsets;
   a.groups = groups;
   a.rows = rows;
@@ -879,23 +1049,91 @@ gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const
   a.n = n;
   a.y = y;
   a.ldy = ldy;
-  a.y_tma = 0;
   a.status = info->status;
   a.wait_ns = wait_limit_ns();
+  return a;
+}
+
+static bool weight_map(CUtensorMap* map, const uint8_t* wq, int groups, int64_t rows, int n) {
+  const int64_t pitch = fp4_pitch(n);
+  return make_tensor_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, pitch, static_cast<uint64_t>(groups) * rows, pitch,
+                            kStageK / 2, kRows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// How the product quantises X itself, or false where X is quantised first: a
+// few tokens whose values every CTA may read, and a K range that its shared
+// memory holds.
+static bool raw_shape(int64_t tokens, int groups, bool ragged, int64_t rows, int n, const DeviceInfo* info, StreamShape* s) {
+  if (tokens > kRawTokens || tokens * n > kFp4SelfValues) return false;
+  *s = stream_shape(tokens, groups, ragged, rows, n, info->sm_count);  // (the splits, and so the sums, of the two calls)
+  s->width = kRawTokens;
+  s->stages = 4;
+  s->raw_stages = static_cast<int>(ceil_div(ceil_div(n, kStageK), s->splits));
+  return s->raw_stages <= kRawMaxStages;
+}
+
+bool fp4_linear_raw(int64_t tokens, int groups, bool ragged, int64_t rows, int n) {
+  const DeviceInfo* info = device_info();
+  StreamShape s;
+  return info != nullptr && raw_shape(tokens, groups, ragged, rows, n, info, &s);
+}
+
+// The product of a few tokens that it quantises itself (fp4_linear_raw).
+gptq_status fp4_raw_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const float* wt, int groups, int64_t rows,
+                           int n, const void* X, int x_bf16, int64_t x_rows, int64_t ldx, const int32_t* row_index,
+                           const float* x_tensor, int64_t tokens, const int32_t* offsets, void* y, int y_bf16, int64_t ldy,
+                           cudaStream_t st) {
+  const DeviceInfo* info = device_info();
+  StreamShape s;
+  CUtensorMap wmap;
+  if (info == nullptr || !raw_shape(tokens, groups, offsets != nullptr, rows, n, info, &s) ||
+      !weight_map(&wmap, wq, groups, rows, n))
+    return GPTQ_ERR_CUDA;
+  const MatmulArgs a = product_args(wscales, wt, groups, rows, n, tokens, offsets, y, ldy, info);
+  const QuantArgs q = fp4_quant_args(X, x_bf16, x_rows, n, ldx, row_index, tokens, offsets, groups, x_tensor != nullptr,
+                                     const_cast<float*>(x_tensor), info->status);
+  if (nv && x_bf16)
+    return y_bf16 ? launch_stream<true, __nv_bfloat16, 1>(wmap, wmap, a, s, q, info, st)
+                  : launch_stream<true, float, 1>(wmap, wmap, a, s, q, info, st);
+  if (nv)
+    return y_bf16 ? launch_stream<true, __nv_bfloat16, 2>(wmap, wmap, a, s, q, info, st)
+                  : launch_stream<true, float, 2>(wmap, wmap, a, s, q, info, st);
+  if (x_bf16)
+    return y_bf16 ? launch_stream<false, __nv_bfloat16, 1>(wmap, wmap, a, s, q, info, st)
+                  : launch_stream<false, float, 1>(wmap, wmap, a, s, q, info, st);
+  return y_bf16 ? launch_stream<false, __nv_bfloat16, 2>(wmap, wmap, a, s, q, info, st)
+                : launch_stream<false, float, 2>(wmap, wmap, a, s, q, info, st);
+}
+
+gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const float* wt, int groups, int64_t rows,
+                       int n, const uint8_t* xq, const uint8_t* xscales, const float* xt, int64_t tokens,
+                       const int32_t* offsets, void* y, int y_bf16, int64_t ldy, cudaStream_t st) {
+  const DeviceInfo* info = device_info();
+  if (info == nullptr) return GPTQ_ERR_CUDA;
+  const int64_t pitch = fp4_pitch(n);
+  CUtensorMap wmap, xmap;
+  if (!weight_map(&wmap, wq, groups, rows, n) ||
+      !make_tensor_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, pitch, tokens, pitch, kStageK / 2, kBoxRows,
+                          CU_TENSOR_MAP_SWIZZLE_128B))
+    return GPTQ_ERR_CUDA;
+  MatmulArgs a = product_args(wscales, wt, groups, rows, n, tokens, offsets, y, ldy, info);
+  a.xscales = xscales;
+  a.xt = xt;
+  if (tokens <= kFp4Band * static_cast<int64_t>(groups)) {
+    const StreamShape s = stream_shape(tokens, groups, offsets != nullptr, rows, n, info->sm_count);
+    const QuantArgs none = {};
+    if (nv)
+      return y_bf16 ? launch_stream<true, __nv_bfloat16, 0>(wmap, xmap, a, s, none, info, st)
+                    : launch_stream<true, float, 0>(wmap, xmap, a, s, none, info, st);
+    return y_bf16 ? launch_stream<false, __nv_bfloat16, 0>(wmap, xmap, a, s, none, info, st)
+                  : launch_stream<false, float, 0>(wmap, xmap, a, s, none, info, st);
+  }
   const int64_t quads = fp4_quads(n, nv);
   const int64_t xbands = offsets != nullptr ? fp4_bands(tokens, groups, true) : ceil_div(tokens, kFp4Band);
-  const bool many = tokens > kFp4Band * static_cast<int64_t>(groups);
   CUtensorMap wsmap, xsmap;
   if (!scale_map(&wsmap, wscales, quads, fp4_bands(groups * rows, groups, false), nv, 1) ||
-      !scale_map(&xsmap, xscales, quads, xbands, nv, many ? 2 : 1))
+      !scale_map(&xsmap, xscales, quads, xbands, nv, 2))
     return GPTQ_ERR_CUDA;
-  if (!many) {
-    if (nv)
-      return y_bf16 ? launch_stream<true, __nv_bfloat16>(wmap, xmap, wsmap, xsmap, a, info, st)
-                    : launch_stream<true, float>(wmap, xmap, wsmap, xsmap, a, info, st);
-    return y_bf16 ? launch_stream<false, __nv_bfloat16>(wmap, xmap, wsmap, xsmap, a, info, st)
-                  : launch_stream<false, float>(wmap, xmap, wsmap, xsmap, a, info, st);
-  }
   CUtensorMap xwide, ymap = xmap;  // (ymap unused where y_tma is 0)
   if (!make_tensor_map_2d(&xwide, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, pitch, tokens, pitch, kStageK / 2, kTokens / 2,
                           CU_TENSOR_MAP_SWIZZLE_128B))

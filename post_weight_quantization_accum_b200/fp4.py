@@ -282,9 +282,10 @@ def fp4_linear(w, X, dtype=None, tensor_scale=None, row_index=None, offsets=None
 
     def call(where):
         o = y if y is not None else X.new_empty((tokens, rows), dtype=dtype)
-        nbytes = LIB.gptq_fp4_linear_workspace_size(tokens, n, code, groups, offsets is not None)
-        keep = ws if ws is not None else X.new_empty((nbytes + 256,), dtype=torch.uint8)
-        base, nbytes = _aligned(keep, nbytes)
+        nbytes, base = LIB.gptq_fp4_linear_workspace_size(tokens, rows, n, code, groups, offsets is not None), None
+        if nbytes > 0:
+            keep = ws if ws is not None else X.new_empty((nbytes + 256,), dtype=torch.uint8)
+            base, nbytes = _aligned(keep, nbytes)
         wt = w["tensor_scale"]
         check("gptq_fp4_linear",
               LIB.gptq_fp4_linear(code, wp.data_ptr(), w["scales"].data_ptr(), None if wt is None else wt.data_ptr(),

@@ -211,6 +211,70 @@ def test_a_layer_of_experts(fmt, tokens, top, experts):
             _check(y[a:b], xv[a:b] @ w_g.T, np.abs(xv[a:b]) @ np.abs(w_g).T, n + 64, torch.bfloat16, False)
 
 
+LINEAR = [(1, 32, 40), (1, 4096, 4096), (1, 4100, 300), (2, 2048, 129), (3, 777, 1000), (4, 4096, 700), (5, 1000, 64),
+          (16, 1024, 256), (16, 96, 130), (1, 16384, 128), (1, 16384, 20000), (17, 512, 128), (2, 9000, 64), (40, 1032, 300)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tokens,n,rows", LINEAR)
+def test_linear_equals_quantise_and_product(fmt, dtype, tokens, n, rows):
+    """One call or two: the same bits, where the product quantises its few
+    tokens itself and where it does not; rows of X with a pitch, values that
+    are zero and not finite, given tensor scales."""
+    gen = torch.Generator("cuda").manual_seed(tokens + n)
+    w = gq.gptq_fp4_quantize(torch.randn((rows, n), device="cuda", generator=gen) * 0.02, fmt)
+    base = torch.randn((tokens, n + 24), device="cuda", generator=gen)
+    base[:, 3] = 0
+    if tokens > 1:
+        base[1] = 0
+    for off in (0, 1, 8, 24):
+        X = base.to(dtype)[:, off:off + n]
+        want = gq.gptq_fp4_matmul(w, gq.gptq_fp4_quantize(X, fmt))
+        assert torch.equal(gq.fp4_linear(w, X, dtype=torch.float32), want)
+    if fmt == "nvfp4":
+        t = torch.tensor([0.0173], device="cuda")
+        want = gq.gptq_fp4_matmul(w, gq.gptq_fp4_quantize(X, fmt, tensor_scale=t))
+        assert torch.equal(gq.fp4_linear(w, X, dtype=torch.float32, tensor_scale=t), want)
+    X = X.clone()
+    X[tokens - 1, n - 1] = float("nan")
+    want = gq.gptq_fp4_matmul(w, gq.gptq_fp4_quantize(X, fmt), dtype=torch.bfloat16)
+    got = gq.fp4_linear(w, X, dtype=torch.bfloat16)
+    assert torch.isnan(got[tokens - 1]).all()
+    assert torch.equal(got[: tokens - 1], want[: tokens - 1]) and not torch.isnan(got[: tokens - 1]).any()
+    assert gq.gptq_get_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("counts,rows,n", [([1], 64, 32), ([0, 4, 0], 200, 4096), ([1, 1, 1, 1], 256, 4096), ([0, 0, 16, 0], 130, 1000),
+                                           ([3, 0, 5, 8], 129, 1024), ([1] * 16, 96, 96), ([0] * 30 + [2, 1], 512, 2056)])
+def test_linear_of_experts_equals_quantise_and_product(fmt, counts, rows, n):
+    """Few tokens through experts, gathered; the first rows belong to none."""
+    groups, tokens = len(counts), sum(counts)
+    gen = torch.Generator("cuda").manual_seed(groups + n)
+    w = gq.gptq_fp4_quantize(torch.randn((groups, rows, n), device="cuda", generator=gen) * 0.02, fmt)
+    X = torch.randn((7, n), device="cuda", generator=gen).to(torch.bfloat16)
+    idx = torch.randint(0, 7, (tokens,), device="cuda", generator=gen).int()
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32).cuda()
+    want = gq.gptq_fp4_grouped_matmul(w, gq.gptq_fp4_quantize(X, fmt, row_index=idx, offsets=off), off)
+    assert torch.equal(gq.fp4_linear(w, X, dtype=torch.float32, row_index=idx, offsets=off), want)
+    assert gq.gptq_get_device_status() == 0
+    if tokens >= 2:  # rows of no group are left alone; a bad index is a row of zeros and reported
+        off2 = off.clone()
+        off2.clamp_(min=1)
+        y = torch.full((tokens, rows), 7.0, device="cuda")
+        gq.fp4_linear(w, X, row_index=idx, offsets=off2, y=y)
+        assert (y[0] == 7).all() and not (y[1:] == 7).any()
+        idx[1] = 7
+        y = gq.fp4_linear(w, X, row_index=idx, offsets=off)
+        assert gq.gptq_get_device_status() == 1
+        assert (y[1] == 0).all()
+    off[-1] += 1
+    y = torch.full((tokens, rows), 7.0, device="cuda")
+    gq.fp4_linear(w, X, row_index=torch.zeros_like(idx), offsets=off, y=y)
+    assert gq.gptq_get_device_status() == 1 and (y == 7).all()
+
+
 def test_captured_and_replayed():
     """A quantise and product pair in a CUDA graph, replayed on new inputs."""
     w = gq.gptq_fp4_quantize((torch.randn((512, 2048), device="cuda") * 0.02), "nvfp4")
