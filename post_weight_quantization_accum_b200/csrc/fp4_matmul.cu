@@ -170,24 +170,36 @@ __device__ __forceinline__ void store_four(__nv_bfloat16* p, float4 v, Scale k, 
 }
 
 // The groups of the offsets in tiles of `width`; without offsets there is one
-// group of all tokens, and no table.  `tiles`: token tiles of all groups.
-__device__ __forceinline__ bool group_table(const GroupTable& t, const MatmulArgs& a, int width, int& tiles) {
-  tiles = static_cast<int>((a.tokens + width - 1) / width);
-  if (a.offsets == nullptr) return true;
-  const bool ok = build_groups(t, a.offsets, a.groups, a.tokens, width);
-  if (!ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, GPTQ_ERR_INVALID_ARG);
-  tiles = t.tile[a.groups];
-  return ok;
+// group of all tokens, which the table holds only with ALWAYS.  False where the
+// offsets are not valid.
+template <bool ALWAYS>
+__device__ __forceinline__ bool group_table(const GroupTable& t, const MatmulArgs& a, int width) {
+  if (a.offsets != nullptr) {
+    const bool ok = build_groups(t, a.offsets, a.groups, a.tokens, width);
+    if (!ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, GPTQ_ERR_INVALID_ARG);
+    return ok;
+  }
+  if (ALWAYS) {
+    if (threadIdx.x == 0) {
+      t.off[0] = t.band[0] = t.tile[0] = 0;
+      t.off[1] = static_cast<int>(a.tokens);
+      t.band[1] = static_cast<int>((a.tokens + kFp4Band - 1) / kFp4Band);
+      t.tile[1] = static_cast<int>((a.tokens + width - 1) / width);
+    }
+    __syncthreads();
+  }
+  return true;
 }
 
 // Items count token tiles first, then row tiles; the host has checked that
 // there are less than 2^31.
+template <bool ALWAYS>
 __device__ __forceinline__ Tile tile_at(const GroupTable& t, const MatmulArgs& a, int wtiles, int width, uint32_t item) {
   Tile x;
   const int tt = static_cast<int>(item / wtiles);
   x.wtile = static_cast<int>(item - tt * wtiles);
   int first, last;
-  if (a.offsets == nullptr) {
+  if (!ALWAYS && a.offsets == nullptr) {
     x.g = 0;
     first = tt * width;
     x.token = first;
@@ -375,9 +387,9 @@ __global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
   if (shape.splits > 1) cluster_arrive();
   pdl_trigger();
   pdl_wait();
-  int tiles;
-  const bool ok_groups = group_table(t, a, shape.width, tiles);
+  const bool ok_groups = group_table<false>(t, a, shape.width);
   const int wtiles = static_cast<int>((a.rows + kRows - 1) / kRows);
+  const int tiles = a.offsets != nullptr ? t.tile[a.groups] : static_cast<int>((a.tokens + shape.width - 1) / shape.width);
   const uint32_t items = ok_groups ? static_cast<uint32_t>(tiles) * wtiles : 0;
   const uint32_t item = blockIdx.x / shape.splits;
   const int rank = blockIdx.x % shape.splits;  // in the cluster
@@ -391,7 +403,7 @@ __global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
   };
 
   if (item < items) {
-    const Tile x = tile_at(t, a, wtiles, shape.width, item);
+    const Tile x = tile_at<false>(t, a, wtiles, shape.width, item);
     const bool push = x.count <= kPushTokens;  // (the same in the whole cluster)
     if (warp == 0) {
       if (elect_one()) {
@@ -758,16 +770,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = uniform(*tmem_slot);
   pdl_trigger();
   pdl_wait();
-  int token_tiles;
-  const bool ok_groups = group_table(t, a, kTokens, token_tiles);
+  const bool ok_groups = group_table<true>(t, a, kTokens);
   const int wtiles = static_cast<int>((a.rows + kPairRows - 1) / kPairRows);
   const int wbands = static_cast<int>((a.rows + kRows - 1) / kRows);
-  const uint32_t items = ok_groups ? static_cast<uint32_t>(token_tiles) * wtiles : 0;
+  // (read from the table by every lane and passed through `uniform`: the
+  // compiler then knows the loops' end to be the same for the whole warp and
+  // keeps descriptors in uniform registers.  With the end chosen between the
+  // table and the arguments a stage took the MMA thread four times as long to
+  // issue, and 8192 x 4096 -> 11008 took 271 us instead of 148.)
+  const uint32_t items = ok_groups ? static_cast<uint32_t>(uniform(t.tile[a.groups])) * wtiles : 0;
   const int quads = fp4_quads(a.n, NV);
   const int mmas = (a.n + 63) / 64;
   const int kstages = (a.n + kStageK - 1) / kStageK;
 
-  auto tile_of = [&](uint32_t item) { return tile_at(t, a, wtiles, kTokens, item); };
+  auto tile_of = [&](uint32_t item) { return tile_at<true>(t, a, wtiles, kTokens, item); };
   // A single thread's wait.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, a.wait_ns, abort_flag, a.status);
