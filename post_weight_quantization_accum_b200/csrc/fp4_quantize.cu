@@ -39,8 +39,9 @@ struct Shape : Fp4Lane<BF16, NV> {
   static constexpr int kAhead = NV ? 1 : 2;
 };
 
+// (the first to leave L2: what is read again is X)
 __device__ __forceinline__ void store32(void* p, const float* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+  asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
                "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
 }
@@ -244,8 +245,10 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) 
     return;
   }
   const int chunks = (a.n + kChunk - 1) / kChunk;
-  const int64_t band = blockIdx.x / chunks;
-  const int chunk = blockIdx.x % chunks;
+  // (after a pass for the maxima: from its end, whose values are still in L2)
+  const unsigned at = NV && a.partial != nullptr ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  const int64_t band = at / chunks;
+  const int chunk = at % chunks;
   if (NV && !a.given && blockIdx.x == 0) {  // groups without rows have no CTA of their own
     for (int g = threadIdx.x; g < a.groups; g += kThreads)
       if (a.offsets != nullptr ? t.off[g] == t.off[g + 1] : a.group_rows == 0) a.tensor_scale[g] = FLT_MIN;
@@ -301,11 +304,11 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) 
     *reinterpret_cast<uint4*>(out + i) = *reinterpret_cast<const uint4*>(sc + i);
 }
 
-// Splits of a band's columns in the pass that takes the maxima: enough CTAs
-// for the chip when there are few bands.
-int amax_splits(int64_t bands, int n, int sms) {
+// Parts of a band's columns in the pass that takes the maxima: a chunk each, or
+// more where that would leave over 2048 maxima for every CTA to read.
+int amax_splits(int64_t bands, int n) {
   const int64_t chunks = ceil_div(n, kChunk);
-  return static_cast<int>(std::min<int64_t>(chunks, std::max<int64_t>(1, ceil_div(4 * sms, bands))));
+  return static_cast<int>(ceil_div(chunks, std::max<int64_t>(1, ceil_div(bands * chunks, 2048))));
 }
 
 template <bool BF16, bool NV>
@@ -324,10 +327,8 @@ gptq_status launch_quantize(QuantArgs& a, int64_t bands, const DeviceInfo* info,
 
 size_t fp4_quantize_workspace_size(int64_t rows, int n, bool nv, int groups, bool ragged) {
   if (!nv || rows * n <= kFp4SelfValues) return 0;
-  const DeviceInfo* info = device_info();
-  if (info == nullptr) return 0;
   const int64_t bands = fp4_bands(rows, groups, ragged);
-  return static_cast<size_t>(bands * amax_splits(bands, n, info->sm_count)) * sizeof(float);
+  return static_cast<size_t>(bands * amax_splits(bands, n)) * sizeof(float);
 }
 
 gptq_status fp4_quantize(const void* X, int x_bf16, int64_t x_rows, int n, int64_t ldx, const int32_t* row_index,
@@ -340,7 +341,7 @@ gptq_status fp4_quantize(const void* X, int x_bf16, int64_t x_rows, int n, int64
   a.packed = packed;
   a.scales = scales;
   a.deq = deq;
-  a.splits = amax_splits(bands, n, info->sm_count);
+  a.splits = amax_splits(bands, n);
   a.partial = nv && !given && rows * n > kFp4SelfValues ? static_cast<float*>(ws) : nullptr;
   if (nv)
     return x_bf16 ? launch_quantize<true, true>(a, bands, info, st) : launch_quantize<false, true>(a, bands, info, st);
