@@ -597,6 +597,9 @@ __global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
           cluster_arrive();
         }
         cluster_wait();  // no CTA leaves while another may still use its memory
+        // (after a wait that ran out: nor while sums that were sent are on their way)
+        if (push && !ok && lane == 0) mbar_wait(sums_in, 0u, kDrainNs);
+        __syncwarp();
       }
       tc_fence_before();
     }

@@ -115,7 +115,7 @@ def _aligned(ws, nbytes):
     """(pointer, bytes) of the 256-byte aligned part of a workspace tensor."""
     p = ws.data_ptr()
     a = (p + 255) & ~255
-    return a, ws.numel() * ws.element_size() - (a - p)
+    return a, max(0, ws.numel() * ws.element_size() - (a - p))
 
 
 def gptq_fp4_quantize(X, format="nvfp4", tensor_scale=None, row_index=None, offsets=None, want_deq=False, out=None,

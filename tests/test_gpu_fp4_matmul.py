@@ -92,7 +92,9 @@ def test_matmul_matches_the_exact_product(fmt, tokens, n, rows, exact):
 
 
 GROUPS = [([1], 64, 32), ([4, 0, 1, 0], 128, 96), ([0, 0, 7], 300, 1000), ([1] * 9, 257, 64), ([130, 1, 0, 255, 40], 200, 264),
-          ([300, 513, 16], 129, 520), ([0, 0], 64, 64), ([17] * 33, 64, 100)]
+          ([300, 513, 16], 129, 520), ([0, 0], 64, 64), ([17] * 33, 64, 100),
+          # few rows a group on average, some with several tiles
+          ([100] + [0] * 9, 136, 320), ([0, 65, 3] + [1] * 20, 200, 768), ([300] + [2] * 11, 64, 1030), ([129, 64, 200] + [0] * 30, 130, 264)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -291,6 +293,57 @@ def test_captured_and_replayed():
         assert torch.equal(got, gq.fp4_linear(w, X))
 
 
+def test_two_graphs_of_one_layer():
+    """Captured apart, replayed in turn and both at once on two streams."""
+    w = gq.gptq_fp4_quantize((torch.randn((1024, 2048), device="cuda") * 0.02), "nvfp4")
+    Xs = [torch.randn((t, 2048), device="cuda").to(torch.bfloat16) for t in (1, 200)]
+    want = [gq.fp4_linear(w, X) for X in Xs]
+    graphs, ys = [], []
+    for X in Xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ys.append(gq.fp4_linear(w, X))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for turn in range(3):
+        for y in ys:
+            y.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ys, want))
+
+
+def test_outputs_past_32_bits():
+    """Over 2^31 outputs: the last tokens like the same tokens alone."""
+    tokens, rows, n = 270000, 8192, 64
+    w = gq.gptq_fp4_quantize(torch.randn((rows, n), device="cuda"), "mxfp4")
+    X = torch.zeros((tokens, n), dtype=torch.bfloat16, device="cuda")
+    X[-400:] = torch.randn((400, n), device="cuda").to(torch.bfloat16)
+    y = gq.fp4_linear(w, X)
+    assert y.numel() > 2 ** 31
+    assert torch.equal(y[-400:], gq.fp4_linear(w, X[-400:].contiguous()))
+    assert not y[: tokens - 400: 1000].any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_tensor_scales_whose_product_leaves_the_normal_numbers(fmt):
+    """Weights of 1e-30 and activations of 1e-18 or 1e30: each scale is used in
+    turn where their product is no normal number."""
+    gen = torch.Generator("cuda").manual_seed(3)
+    W = torch.randn((130, 96), device="cuda", generator=gen)
+    X = torch.randn((300, 96), device="cuda", generator=gen)
+    for tokens in (5, 300):
+        want = gq.fp4_linear(gq.gptq_fp4_quantize(W, fmt), X[:tokens]).double()
+        for a, b in ((2.0 ** -100, 2.0 ** -20), (2.0 ** -60, 2.0 ** 100), (2.0 ** 50, 2.0 ** 60)):
+            y = gq.fp4_linear(gq.gptq_fp4_quantize(W * a, fmt), X[:tokens] * b).double() / (a * b)
+            # powers of two move no code; each product with a scale rounds, at most half of the least subnormal
+            bound = want.abs() * 2.0 ** -22 + 2.0 ** -149 / (a * b)
+            assert ((y - want).abs() <= bound).all()
+
+
 def test_on_another_stream():
     w = gq.gptq_fp4_quantize(torch.randn((300, 1024), device="cuda"), "nvfp4")
     X = torch.randn((70, 1024), device="cuda").to(torch.bfloat16)
@@ -302,16 +355,23 @@ def test_on_another_stream():
     assert all(torch.equal(want, y) for y in got)
 
 
-def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
-    w = gq.gptq_fp4_quantize(torch.randn((300, 1024), device="cuda"), "mxfp4")
-    x = gq.gptq_fp4_quantize(torch.randn((70, 1024), device="cuda"), "mxfp4")
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("tokens,rows", [(1, 300), (3, 9000), (12, 300), (70, 300), (128, 20000), (600, 300), (900, 4096)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(fmt, tokens, rows):
+    """Each kind of product (that quantises its tokens, cut along K or not, of
+    CTA pairs): every wait is bounded, and the GPU is as before afterwards."""
+    w = gq.gptq_fp4_quantize(torch.randn((rows, 2048), device="cuda"), fmt)
+    X = torch.randn((tokens, 2048), device="cuda")
+    x = gq.gptq_fp4_quantize(X, fmt)
     want = gq.gptq_fp4_matmul(w, x)
-    torch.cuda.synchronize()
-    gq.gptq_set_wait_limit_ns(0)
-    try:
-        gq.gptq_fp4_matmul(w, x)
+    for call in (lambda: gq.gptq_fp4_matmul(w, x), lambda: gq.fp4_linear(w, X)):
         torch.cuda.synchronize()
-    finally:
-        gq.gptq_set_wait_limit_ns(2 ** 64 - 1)
-    assert gq.gptq_get_device_status() == 6
-    assert torch.equal(want, gq.gptq_fp4_matmul(w, x))
+        gq.gptq_set_wait_limit_ns(0)
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            gq.gptq_set_wait_limit_ns(2 ** 64 - 1)
+        assert gq.gptq_get_device_status() == 6
+        assert torch.equal(want, call())
+        assert gq.gptq_get_device_status() == 0

@@ -232,3 +232,47 @@ def test_codes_are_the_same_every_time_and_on_another_stream():
     side.synchronize()
     for k in ("packed", "scales", "tensor_scale", "deq"):
         assert torch.equal(first[k], again[k]), k
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_offsets_past_32_bits(fmt):
+    """Over 2^31 values: the last rows like the same rows alone."""
+    rows, n = 530000, 4096
+    X = torch.empty((rows, n), dtype=torch.bfloat16, device="cuda")
+    X[:-300] = 0.5
+    X[-300:] = torch.randn((300, n), device="cuda").to(torch.bfloat16)
+    ts = torch.tensor([0.01], device="cuda") if fmt == "nvfp4" else None
+    q = gq.gptq_fp4_quantize(X, fmt, tensor_scale=ts)
+    tail = gq.gptq_fp4_quantize(X[-(rows % 128 + 128):], fmt, tensor_scale=ts)
+    assert torch.equal(q["packed"][-(rows % 128 + 128):], tail["packed"])
+    assert torch.equal(q["scales"][-2:], tail["scales"])
+    if fmt == "nvfp4":  # and the maximum over all of them
+        full = gq.gptq_fp4_quantize(X, fmt)
+        assert full["tensor_scale"].item() == (X[-300:].abs().max().float() / torch.tensor(2688.0, device="cuda")).item()
+
+
+def test_two_streams_at_once():
+    Xs = [torch.randn((2000, 1024), device="cuda") * (i + 1) for i in range(2)]
+    want = [gq.gptq_fp4_quantize(X, "nvfp4", want_deq=True) for X in Xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in Xs]
+    got = [[gq.gptq_fp4_quantize(X, "nvfp4", want_deq=True, stream=s) for X, s in zip(Xs, streams)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for run in got:
+        for a, b in zip(run, want):
+            assert all(torch.equal(a[k], b[k]) for k in ("packed", "scales", "tensor_scale", "deq"))
+
+
+def test_workspace_and_outputs_of_the_caller():
+    X = torch.randn((700, 520), device="cuda")
+    want = gq.gptq_fp4_quantize(X, "nvfp4", want_deq=True)
+    need = gq.LIB.gptq_fp4_quantize_workspace_size(700, 520, 1, 1, 0)
+    assert need > 0
+    ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")[3:]
+    out = {k: torch.empty_like(want[k]) for k in ("packed", "scales", "tensor_scale", "deq")}
+    got = gq.gptq_fp4_quantize(X, "nvfp4", want_deq=True, out=out, ws=ws[:need + 253])
+    assert all(got[k].data_ptr() == out[k].data_ptr() and torch.equal(out[k], want[k]) for k in out)
+    with pytest.raises(gq.GptqError, match="INVALID_ARG"):
+        gq.gptq_fp4_quantize(X, "nvfp4", ws=ws[:need - 1])
+    with pytest.raises(ValueError):
+        gq.gptq_fp4_quantize(X, "nvfp4", out={"packed": out["packed"][:-1]})
