@@ -44,7 +44,7 @@ gptq_status fp4_quantize(const void* X, int x_bf16, int64_t x_rows, int n, int64
                          uint8_t* packed, uint8_t* scales, float* deq, void* ws, cudaStream_t st);
 gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const float* wt, int groups, int64_t rows,
                        int n, const uint8_t* xq, const uint8_t* xscales, const float* xt, int64_t tokens,
-                       const int32_t* offsets, void* y, int y_bf16, int64_t ldy, cudaStream_t st);
+                       const int32_t* offsets, void* y, int y_bf16, int64_t ldy, bool early, cudaStream_t st);
 bool fp4_linear_raw(int64_t tokens, int groups, bool ragged, int64_t rows, int n);
 gptq_status fp4_raw_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const float* wt, int groups, int64_t rows,
                            int n, const void* X, int x_bf16, int64_t x_rows, int64_t ldx, const int32_t* row_index,
@@ -545,7 +545,7 @@ gptq_status gptq_fp4_matmul(gptq_fp4_format format, const uint8_t* w_packed, con
   const gptq_status s = check_product(format, w_packed, w_scales, w_tensor, 1, rows, n, x_packed, x_scales, x_tensor, tokens, y, ydt, ldy);
   if (s != GPTQ_OK || rows == 0 || tokens == 0) return s;
   return fp4_matmul(format == GPTQ_NVFP4, w_packed, w_scales, w_tensor, 1, rows, n, x_packed, x_scales, x_tensor, tokens, nullptr, y,
-                    ydt == GPTQ_BF16 ? 1 : 0, ldy, as_stream(stream));
+                    ydt == GPTQ_BF16 ? 1 : 0, ldy, false, as_stream(stream));
 }
 
 gptq_status gptq_fp4_grouped_matmul(gptq_fp4_format format, const uint8_t* w_packed, const uint8_t* w_scales, const float* w_tensor,
@@ -556,7 +556,7 @@ gptq_status gptq_fp4_grouped_matmul(gptq_fp4_format format, const uint8_t* w_pac
   if (s != GPTQ_OK || rows == 0 || tokens == 0) return s;
   if (offsets == nullptr || !aligned(offsets, 4)) return GPTQ_ERR_INVALID_ARG;
   return fp4_matmul(format == GPTQ_NVFP4, w_packed, w_scales, w_tensor, groups, rows, n, x_packed, x_scales, x_tensor, tokens, offsets, y,
-                    ydt == GPTQ_BF16 ? 1 : 0, ldy, as_stream(stream));
+                    ydt == GPTQ_BF16 ? 1 : 0, ldy, false, as_stream(stream));
 }
 
 size_t gptq_fp4_linear_workspace_size(int64_t tokens, int64_t rows, int32_t n, gptq_fp4_format format, int32_t groups,
@@ -596,7 +596,7 @@ gptq_status gptq_fp4_linear(gptq_fp4_format format, const uint8_t* w_packed, con
                    x_tensor != nullptr ? 1 : 0, xt, xq, xs, nullptr, base + l.partial, as_stream(stream));
   if (s != GPTQ_OK) return s;
   return fp4_matmul(nv, w_packed, w_scales, w_tensor, groups, rows, n, xq, xs, xt, tokens, offsets, y,
-                    ydt == GPTQ_BF16 ? 1 : 0, ldy, as_stream(stream));
+                    ydt == GPTQ_BF16 ? 1 : 0, ldy, true, as_stream(stream));
 }
 
 }  // extern "C"

@@ -46,6 +46,8 @@ struct MatmulArgs {
   void* y;
   int64_t ldy;
   int y_tma;  // y can be written by TMA (bf16, rows on 16 bytes)
+  int early;  // the kernel before this one is the quantiser of X, which starts it
+              // after its own wait: W and the offsets are there from the start
   int* status;
   uint64_t wait_ns;
 };
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
   // (the cluster's barriers exist once all have arrived; waited for before the first use across it)
   if (shape.splits > 1) cluster_arrive();
   pdl_trigger();
-  pdl_wait();
+  if (RAW || !a.early) pdl_wait();
   const bool ok_groups = group_table<false>(t, a, shape.width);
   const int wtiles = static_cast<int>((a.rows + kRows - 1) / kRows);
   const int tiles = a.offsets != nullptr ? t.tile[a.groups] : static_cast<int>((a.tokens + shape.width - 1) / shape.width);
@@ -412,22 +414,31 @@ __global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
         const int wy = static_cast<int>(x.g * a.rows) + x.wtile * kRows;
         const uint8_t* wsc = a.wscales + (static_cast<int64_t>(x.g) * wtiles + x.wtile) * quads * kFp4TileBytes;
         const uint8_t* xsc = a.xscales + static_cast<int64_t>(x.xband) * quads * kFp4TileBytes;
-        uint32_t stage = 0, phase = 0;
-        int issued = 0;
-        for (int kb = k0; kb < k1; ++kb, ++issued) {
-          if (!wait(empty + stage, phase ^ 1u)) break;
+        auto load_w = [&](int kb, uint32_t stage) {
           uint8_t* sa = smem + stage * stage_bytes;
-          uint8_t* sf = sa + kABytes + bbytes;
           const uint32_t sf_bytes = min(kStageQuads, quads - kb * kStageQuads) * kFp4TileBytes;
-          const int64_t sf_at = static_cast<int64_t>(kb) * kStageSf;
           mbar_arrive_expect_tx(full + stage, kABytes + boxes * kBoxBytes + (RAW ? 1 : 2) * sf_bytes);
           tma_load_2d(sa, &wmap, full + stage, kb * (kStageK / 2), wy);
-          bulk_load(sf, wsc + sf_at, sf_bytes, full + stage);
-          if (!RAW) {
-            for (int b = 0; b < boxes; ++b)
-              tma_load_2d(sa + kABytes + b * kBoxBytes, &xmap, full + stage, kb * (kStageK / 2), x.token + b * kBoxRows);
-            bulk_load(sf + kStageSf, xsc + sf_at, sf_bytes, full + stage);
-          }
+          bulk_load(sa + kABytes + bbytes, wsc + static_cast<int64_t>(kb) * kStageSf, sf_bytes, full + stage);
+        };
+        auto load_x = [&](int kb, uint32_t stage) {
+          if (RAW) return;
+          uint8_t* sa = smem + stage * stage_bytes;
+          const uint32_t sf_bytes = min(kStageQuads, quads - kb * kStageQuads) * kFp4TileBytes;
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(sa + kABytes + b * kBoxBytes, &xmap, full + stage, kb * (kStageK / 2), x.token + b * kBoxRows);
+          bulk_load(sa + kABytes + bbytes + kStageSf, xsc + static_cast<int64_t>(kb) * kStageSf, sf_bytes, full + stage);
+        };
+        // the ring's first round: W before X is there
+        int issued = min(shape.stages, k1 - k0);
+        for (int i = 0; i < issued; ++i) load_w(k0 + i, i);
+        if (!RAW && a.early) pdl_wait();
+        for (int i = 0; i < issued; ++i) load_x(k0 + i, i);
+        uint32_t stage = 0, phase = 1;
+        for (int kb = k0 + issued; kb < k1; ++kb, ++issued) {
+          if (!wait(empty + stage, phase ^ 1u)) break;
+          load_w(kb, stage);
+          load_x(kb, stage);
           if (++stage == static_cast<uint32_t>(shape.stages)) {
             stage = 0;
             phase ^= 1u;
@@ -489,6 +500,7 @@ __global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
       // ---------------- epilogue ----------------
       const int quad = warp & 3;  // the tensor-memory lanes of this warp
       const int f = quad * 32 + lane;
+      if (!RAW && a.early) pdl_wait();
       float tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
       if (RAW) {
         tx = quantize_tile<RAW == 1, NV>(q, x, k0, k1, raw, reinterpret_cast<int*>(full) + 24, reinterpret_cast<uint32_t*>(full) + 40);
@@ -616,6 +628,7 @@ __global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
   } else if (shape.splits > 1) {
     cluster_wait();
   }
+  if (!RAW && a.early) pdl_wait();  // (in every CTA: this kernel does not end before the quantiser)
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -1126,7 +1139,7 @@ gptq_status fp4_raw_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, c
 
 gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const float* wt, int groups, int64_t rows,
                        int n, const uint8_t* xq, const uint8_t* xscales, const float* xt, int64_t tokens,
-                       const int32_t* offsets, void* y, int y_bf16, int64_t ldy, cudaStream_t st) {
+                       const int32_t* offsets, void* y, int y_bf16, int64_t ldy, bool early, cudaStream_t st) {
   const DeviceInfo* info = device_info();
   if (info == nullptr) return GPTQ_ERR_CUDA;
   const int64_t pitch = fp4_pitch(n);
@@ -1138,6 +1151,7 @@ gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const
   MatmulArgs a = product_args(wscales, wt, groups, rows, n, tokens, offsets, y, ldy, info);
   a.xscales = xscales;
   a.xt = xt;
+  a.early = early;
   if (tokens <= kFp4Band * static_cast<int64_t>(groups)) {
     const StreamShape s = stream_shape(tokens, groups, offsets != nullptr, rows, n, info->sm_count);
     const QuantArgs none = {};

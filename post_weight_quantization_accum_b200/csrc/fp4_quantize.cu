@@ -119,8 +119,8 @@ __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(QuantArgs a) {
   __shared__ uint32_t red[32];
   __shared__ int src[kFp4Band];
   const GroupTable t{tab[0], tab[1], tab[2]};
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // (after the wait: what starts now may read all that was written before this kernel)
   if (a.offsets != nullptr && !build_groups(t, a.offsets, a.groups, a.rows, kFp4Band)) return;
   const int64_t band = blockIdx.x / a.splits;
   const int part = blockIdx.x % a.splits;
@@ -238,8 +238,8 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) 
   __shared__ int src[kFp4Band];
   __shared__ __align__(16) uint8_t sc[kFp4Band * (kChunk / S::kBlock)];
   const GroupTable t{tab[0], tab[1], tab[2]};
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // (after the wait: what starts now may read all that was written before this kernel)
   if (a.offsets != nullptr && !build_groups(t, a.offsets, a.groups, a.rows, kFp4Band)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, GPTQ_ERR_INVALID_ARG);
     return;

@@ -24,20 +24,28 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _on(device, stream, call):
-    """call(handle) with the tensors' device and the stream current, so that
-    what it allocates belongs to them."""
+def _enter(device, stream):
+    """(stream handle, guard): the tensors' device and the stream are current
+    until guard (None: they were) is left, so that what is allocated belongs to
+    them."""
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a CUDA device, not on {device}")
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return call(_raw_stream(device.index))
-    return call(_raw_stream(device.index))
+    index = device.index
+    if stream is None and index == torch.cuda.current_device():
+        return _raw_stream(index), None
+    if stream is None:
+        guard = torch.cuda.device(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    else:
+        guard = torch.cuda.stream(stream)
+    guard.__enter__()
+    return _raw_stream(index), guard
+
+
+def _leave(guard):
+    if guard is not None:
+        guard.__exit__(None, None, None)
 
 
 def _need(ok, why):
@@ -105,13 +113,13 @@ def fp4_check_quantize_args(X, format, tensor_scale=None, row_index=None, offset
 def _output(X, out, name, shape, dtype):
     t = out.get(name) if out else None
     if t is None:
-        return X.new_empty(shape, dtype=dtype)
+        return X.new_empty(*shape, dtype=dtype)
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != X.device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {X.device}")
     return t
 
 
-def _aligned(ws, nbytes):
+def _aligned(ws):
     """(pointer, bytes) of the 256-byte aligned part of a workspace tensor."""
     p = ws.data_ptr()
     a = (p + 255) & ~255
@@ -136,18 +144,19 @@ def gptq_fp4_quantize(X, format="nvfp4", tensor_scale=None, row_index=None, offs
     stack = len(shape) == 3
     x_rows, ldx = (rows, n) if stack else (shape[0], max(X.stride(0), n))
 
-    def call(where):
+    where, guard = _enter(X.device, stream)
+    try:
         packed = _output(X, out, "packed", (rows, 16 * ((n + 31) // 32)), torch.uint8)
         scales = _output(X, out, "scales", (_bands(rows, groups, ragged), (n + block - 1) // block, 512), torch.uint8)
         t, wp, wbytes, deq = tensor_scale, None, 0, None
-        q = {"packed": packed, "scales": scales, "tensor_scale": t, "rows": rows, "n": n, "format": format,
-             "groups": groups}
         if code == GPTQ_NVFP4 and t is None:
-            q["tensor_scale"] = t = _output(X, out, "tensor_scale", (groups,), torch.float32)
+            t = _output(X, out, "tensor_scale", (groups,), torch.float32)
             wbytes = LIB.gptq_fp4_quantize_workspace_size(rows, n, code, groups, ragged)
             if wbytes > 0:
-                keep = ws if ws is not None else X.new_empty((wbytes + 256,), dtype=torch.uint8)
-                wp, wbytes = _aligned(keep, wbytes)
+                keep = ws if ws is not None else X.new_empty(wbytes + 256, dtype=torch.uint8)
+                wp, wbytes = _aligned(keep)
+        q = {"packed": packed, "scales": scales, "tensor_scale": t, "rows": rows, "n": n, "format": format,
+             "groups": groups}
         if want_deq:
             q["deq"] = deq = _output(X, out, "deq", (rows, n), torch.float32)
         check("gptq_fp4_quantize",
@@ -157,8 +166,8 @@ def gptq_fp4_quantize(X, format="nvfp4", tensor_scale=None, row_index=None, offs
                                     tensor_scale is not None, None if t is None else t.data_ptr(), packed.data_ptr(),
                                     scales.data_ptr(), None if deq is None else deq.data_ptr(), wp, wbytes, where))
         return q
-
-    return _on(X.device, stream, call)
+    finally:
+        _leave(guard)
 
 
 def fp4_check_matrix(q, name, ragged=False):
@@ -214,11 +223,12 @@ def _product(w, x, offsets, dtype, y, stream):
     rows = w["rows"] // groups
     _check_y(y, dtype, tokens, rows, wp.device)
 
-    def call(where):
-        o = y if y is not None else wp.new_empty((tokens, rows), dtype=dtype)
+    where, guard = _enter(wp.device, stream)
+    try:
+        o = y if y is not None else wp.new_empty(tokens, rows, dtype=dtype)
         wt, xt = w["tensor_scale"], x["tensor_scale"]
         wt, xt = (None, None) if wt is None else (wt.data_ptr(), xt.data_ptr())
-        ldy = max(o.stride(0), rows)
+        ldy = rows if y is None else max(y.stride(0), rows)
         if offsets is None:
             check("gptq_fp4_matmul",
                   LIB.gptq_fp4_matmul(FP4_FORMATS[w["format"]], wp.data_ptr(), w["scales"].data_ptr(), wt, rows, n,
@@ -230,8 +240,8 @@ def _product(w, x, offsets, dtype, y, stream):
                                               groups, rows, n, xp.data_ptr(), x["scales"].data_ptr(), xt, tokens,
                                               offsets.data_ptr(), o.data_ptr(), _DTYPES[o.dtype], ldy, where))
         return o
-
-    return _on(wp.device, stream, call)
+    finally:
+        _leave(guard)
 
 
 def gptq_fp4_matmul(w, x, dtype=torch.float32, y=None, stream=None):
@@ -279,13 +289,13 @@ def fp4_linear(w, X, dtype=None, tensor_scale=None, row_index=None, offsets=None
         dtype = X.dtype
     _check_y(y, dtype, tokens, rows, wp.device)
     code = FP4_FORMATS[format]
-
-    def call(where):
-        o = y if y is not None else X.new_empty((tokens, rows), dtype=dtype)
+    where, guard = _enter(wp.device, stream)
+    try:
+        o = y if y is not None else X.new_empty(tokens, rows, dtype=dtype)
         nbytes, base = LIB.gptq_fp4_linear_workspace_size(tokens, rows, n, code, groups, offsets is not None), None
         if nbytes > 0:
-            keep = ws if ws is not None else X.new_empty((nbytes + 256,), dtype=torch.uint8)
-            base, nbytes = _aligned(keep, nbytes)
+            keep = ws if ws is not None else X.new_empty(nbytes + 256, dtype=torch.uint8)
+            base, nbytes = _aligned(keep)
         wt = w["tensor_scale"]
         check("gptq_fp4_linear",
               LIB.gptq_fp4_linear(code, wp.data_ptr(), w["scales"].data_ptr(), None if wt is None else wt.data_ptr(),
@@ -293,7 +303,7 @@ def fp4_linear(w, X, dtype=None, tensor_scale=None, row_index=None, offsets=None
                                   None if row_index is None else row_index.data_ptr(), tokens,
                                   None if offsets is None else offsets.data_ptr(),
                                   None if tensor_scale is None else tensor_scale.data_ptr(), o.data_ptr(),
-                                  _DTYPES[o.dtype], max(o.stride(0), rows), base, nbytes, where))
+                                  _DTYPES[o.dtype], rows if y is None else max(y.stride(0), rows), base, nbytes, where))
         return o
-
-    return _on(wp.device, stream, call)
+    finally:
+        _leave(guard)
