@@ -221,24 +221,27 @@ __device__ __forceinline__ Tile tile_at(const GroupTable& t, const MatmulArgs& a
 }
 
 // ---------------------------------------------------------------------------
-// The kernel for few tokens: one tile of 128 weight rows x up to `width` tokens
-// a CTA, its K range split over the CTAs of a cluster
+// The kernel for few tokens: tiles of 128 weight rows x up to `width` tokens
 // ---------------------------------------------------------------------------
 //
 // Bound by HBM: each weight is read once (128 * 4096 codes and their scales
-// are 288 KB of nvfp4).  Two or three CTAs share an SM, so that one streams
-// while another starts or ends, and a layer with too few row tiles for the
-// chip is cut along K.  The cluster's CTAs then add up their sums in rank
-// order, so the result does not depend on timing: of a few tokens each CTA
-// sends its sums to the one that owns the token, as asynchronous stores that
-// the owner's barrier counts; of many the owner reads them from the others.
+// are 288 KB of nvfp4).  With at least a tile an SM, one CTA an SM walks over
+// the tiles with a ring of up to eight stages that never runs dry between two
+// of them (64 tokens through 32 experts of 2048 x 4096: WALK us; a CTA a tile
+// took 32, as each starts with an empty ring).  A layer with fewer tiles is
+// cut along K: a cluster takes a tile, each of its CTAs a part of K, two CTAs
+// an SM, and the CTAs then add up their sums in rank order, so the result does
+// not depend on timing: of a few tokens each CTA sends its sums to the one that
+// owns the token, as asynchronous stores that the owner's barrier counts; of
+// many the owner reads them from the others.
 //
 // RAW: X is not quantised yet (gptq_fp4_linear of a few tokens).  The epilogue
 // warps then quantise the CTA's K range of its tokens into shared memory
 // while the first weights arrive, which costs less than a launch in between.
 
 constexpr int kStreamThreads = 192;  // producer, MMA, 4 epilogue warps
-constexpr int kStreamMaxStages = 4;
+constexpr int kStreamMaxStages = 8;
+constexpr int kStreamBarBytes = 384;
 constexpr int kPushTokens = 16;      // up to here sums are sent (an MMA's least columns)
 constexpr int kRawTokens = 16;       // of a RAW tile: one MMA's least columns
 constexpr int kRawMaxStages = 8;     // of a RAW CTA's K range
@@ -248,6 +251,7 @@ struct StreamShape {
   int width;   // tokens of a tile: 16, 32, 64 or 128
   int stages;
   int splits;  // CTAs of a cluster
+  int accs;    // accumulators: 2 where a CTA walks over tiles
   int raw_stages;  // RAW: most stages of a CTA's K range
 };
 __host__ __device__ inline int stream_stage_bytes(int width, bool raw) {
@@ -262,9 +266,15 @@ __host__ __device__ inline int stream_apart_bytes(int width, int splits) {
   const int bytes = splits * ((width + splits - 1) / splits) * kRows * 4;
   return splits > 1 && width <= 32 ? (bytes + 1023) / 1024 * 1024 : 0;  // (an operand may follow)
 }
-// Tensor memory of a CTA: the accumulator and 32 scale columns a stage.
-__host__ __device__ inline uint32_t stream_tmem_cols(int width, int stages) { return width + 32 * stages > 128 ? 256 : 128; }
-constexpr size_t kStreamMaxSmem = 1024 + 4 * (2 * kABytes + 2 * kSfBytes) + 256 + 12 * (kFp4MaxGroups + 1);
+// Tensor memory of a CTA: accumulators and 32 scale columns a stage (at most
+// 2 * 128 + 32 * 8).
+__host__ __device__ inline uint32_t stream_tmem_cols(int width, int accs, int stages) {
+  const int need = accs * width + 32 * stages;
+  return need > 256 ? 512 : need > 128 ? 256 : 128;
+}
+constexpr size_t kStreamMaxSmem = 226 * 1024;
+// A walking CTA has the SM to itself: what its ring may take.
+constexpr int kWalkRingBytes = 200 * 1024;
 
 // The epilogue warps' part of a RAW tile: x.count tokens, stages [k0, k1) of K,
 // as B operand rows (128-byte swizzle) and scale tiles, stage by stage at
@@ -336,7 +346,7 @@ __device__ __forceinline__ float quantize_tile(const QuantArgs& a, const Tile& x
 
 // RAW: 0 X is quantised; 1 bf16, 2 fp32 X of q.
 template <bool NV, typename OUT, int RAW>
-__global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
+__global__ void __launch_bounds__(kStreamThreads, 2)
     fp4_stream_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, MatmulArgs a,
                       StreamShape shape, QuantArgs q) {
   extern __shared__ uint8_t smem_raw[];
@@ -349,11 +359,15 @@ __global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
   uint64_t* full = reinterpret_cast<uint64_t*>(raw + (RAW ? shape.raw_stages * kRawStageBytes : 0));
   uint64_t* empty = full + kStreamMaxStages;
   uint64_t* acc_full = empty + kStreamMaxStages;
-  uint64_t* sums_in = acc_full + 1;  // the cluster's sums for this CTA's tokens have arrived
-  uint64_t* x_ready = sums_in + 1;   // RAW: the tokens are quantised
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(x_ready + 1);
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* sums_in = acc_empty + 2;  // the cluster's sums for this CTA's tokens have arrived
+  uint64_t* x_ready = sums_in + 1;    // RAW: the tokens are quantised
+  uint64_t* drain = x_ready + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* table = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);
+  int* raw_src = reinterpret_cast<int*>(tmem_slot + 2);                   // kRawTokens
+  uint32_t* raw_red = reinterpret_cast<uint32_t*>(raw_src + kRawTokens);  // 4
+  int* table = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + kStreamBarBytes);
   const GroupTable t{table, table + a.groups + 1, table + 2 * (a.groups + 1)};
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
@@ -362,16 +376,20 @@ __global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
   constexpr int kStageQuads = kStageK / (4 * kBlk);
   constexpr int kQuadMmas = kBlk / 16;
   constexpr uint32_t kStageSf = kStageQuads * kFp4TileBytes;
-  const uint32_t tmem_cols = stream_tmem_cols(shape.width, shape.stages);
+  const uint32_t tmem_cols = stream_tmem_cols(shape.width, shape.accs, shape.stages);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < shape.stages; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
     }
-    mbar_init(acc_full, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + b, 1);
+      mbar_init(acc_empty + b, 4);
+    }
     mbar_init(sums_in, 1);
     mbar_init(x_ready, 128);
+    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&wmap);
@@ -389,11 +407,12 @@ __global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
   if (shape.splits > 1) cluster_arrive();
   pdl_trigger();
   if (RAW || !a.early) pdl_wait();
-  const bool ok_groups = group_table<false>(t, a, shape.width);
+  const bool ok_groups = group_table<true>(t, a, shape.width);
   const int wtiles = static_cast<int>((a.rows + kRows - 1) / kRows);
-  const int tiles = a.offsets != nullptr ? t.tile[a.groups] : static_cast<int>((a.tokens + shape.width - 1) / shape.width);
-  const uint32_t items = ok_groups ? static_cast<uint32_t>(tiles) * wtiles : 0;
-  const uint32_t item = blockIdx.x / shape.splits;
+  // (uniform: see the pair kernel)
+  const uint32_t items = ok_groups ? static_cast<uint32_t>(uniform(t.tile[a.groups])) * wtiles : 0;
+  const uint32_t first = blockIdx.x / shape.splits;
+  const uint32_t stride = shape.splits > 1 ? items : gridDim.x;  // a cluster has one tile
   const int rank = blockIdx.x % shape.splits;  // in the cluster
   const int quads = fp4_quads(a.n, NV);
   const int mmas = (a.n + 63) / 64;
@@ -403,122 +422,160 @@ __global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, a.wait_ns, abort_flag, a.status);
   };
+  auto tile_of = [&](uint32_t item) { return tile_at<true>(t, a, wtiles, shape.width, item); };
 
-  if (item < items) {
-    const Tile x = tile_at<false>(t, a, wtiles, shape.width, item);
-    const bool push = x.count <= kPushTokens;  // (the same in the whole cluster)
+  if (first < items) {
+    // (of a cluster's one tile, and the same in all of its CTAs)
+    const bool push = shape.splits > 1 && tile_of(first).count <= kPushTokens;
     if (warp == 0) {
       if (elect_one()) {
         // ---------------- producer ----------------
-        const int boxes = RAW ? 0 : (x.cols + kBoxRows - 1) / kBoxRows;
-        const int wy = static_cast<int>(x.g * a.rows) + x.wtile * kRows;
-        const uint8_t* wsc = a.wscales + (static_cast<int64_t>(x.g) * wtiles + x.wtile) * quads * kFp4TileBytes;
-        const uint8_t* xsc = a.xscales + static_cast<int64_t>(x.xband) * quads * kFp4TileBytes;
-        auto load_w = [&](int kb, uint32_t stage) {
+        struct {
+          int wy, token, boxes;
+          const uint8_t* wsc;
+          const uint8_t* xsc;
+        } src;
+        uint32_t item;
+        int kb;
+        auto take = [&] {
+          const Tile x = tile_of(item);
+          src.wy = static_cast<int>(x.g * a.rows) + x.wtile * kRows;
+          src.token = x.token;
+          src.boxes = RAW ? 0 : (x.cols + kBoxRows - 1) / kBoxRows;
+          src.wsc = a.wscales + (static_cast<int64_t>(x.g) * wtiles + x.wtile) * quads * kFp4TileBytes;
+          src.xsc = a.xscales + static_cast<int64_t>(x.xband) * quads * kFp4TileBytes;
+        };
+        auto start = [&] {
+          item = first;
+          kb = k0;
+          take();
+        };
+        auto next = [&] {
+          if (++kb == k1) {
+            kb = k0;
+            item += stride;
+            if (item < items) take();
+          }
+        };
+        auto load_w = [&](uint32_t stage) {
           uint8_t* sa = smem + stage * stage_bytes;
           const uint32_t sf_bytes = min(kStageQuads, quads - kb * kStageQuads) * kFp4TileBytes;
-          mbar_arrive_expect_tx(full + stage, kABytes + boxes * kBoxBytes + (RAW ? 1 : 2) * sf_bytes);
-          tma_load_2d(sa, &wmap, full + stage, kb * (kStageK / 2), wy);
-          bulk_load(sa + kABytes + bbytes, wsc + static_cast<int64_t>(kb) * kStageSf, sf_bytes, full + stage);
+          mbar_arrive_expect_tx(full + stage, kABytes + src.boxes * kBoxBytes + (RAW ? 1 : 2) * sf_bytes);
+          tma_load_2d(sa, &wmap, full + stage, kb * (kStageK / 2), src.wy);
+          bulk_load(sa + kABytes + bbytes, src.wsc + static_cast<int64_t>(kb) * kStageSf, sf_bytes, full + stage);
         };
-        auto load_x = [&](int kb, uint32_t stage) {
+        auto load_x = [&](uint32_t stage) {
           if (RAW) return;
           uint8_t* sa = smem + stage * stage_bytes;
           const uint32_t sf_bytes = min(kStageQuads, quads - kb * kStageQuads) * kFp4TileBytes;
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(sa + kABytes + b * kBoxBytes, &xmap, full + stage, kb * (kStageK / 2), x.token + b * kBoxRows);
-          bulk_load(sa + kABytes + bbytes + kStageSf, xsc + static_cast<int64_t>(kb) * kStageSf, sf_bytes, full + stage);
+          for (int b = 0; b < src.boxes; ++b)
+            tma_load_2d(sa + kABytes + b * kBoxBytes, &xmap, full + stage, kb * (kStageK / 2), src.token + b * kBoxRows);
+          bulk_load(sa + kABytes + bbytes + kStageSf, src.xsc + static_cast<int64_t>(kb) * kStageSf, sf_bytes, full + stage);
         };
         // the ring's first round: W before X is there
-        int issued = min(shape.stages, k1 - k0);
-        for (int i = 0; i < issued; ++i) load_w(k0 + i, i);
+        uint32_t issued = 0;
+        const uint32_t ring_stages = shape.stages;
+        for (start(); issued < ring_stages && item < items; ++issued, next()) load_w(issued);
         if (!RAW && a.early) pdl_wait();
-        for (int i = 0; i < issued; ++i) load_x(k0 + i, i);
+        start();
+        for (uint32_t i = 0; i < issued; ++i, next()) load_x(i);
         uint32_t stage = 0, phase = 1;
-        for (int kb = k0 + issued; kb < k1; ++kb, ++issued) {
+        for (; item < items; next(), ++issued) {
           if (!wait(empty + stage, phase ^ 1u)) break;
-          load_w(kb, stage);
-          load_x(kb, stage);
-          if (++stage == static_cast<uint32_t>(shape.stages)) {
+          load_w(stage);
+          load_x(stage);
+          if (++stage == ring_stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         // every stage that was armed has received its bytes: the last use of each
-        for (int u = max(0, issued - shape.stages); u < issued; ++u)
-          if (!mbar_wait(full + u % shape.stages, u / shape.stages & 1u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
+        for (uint32_t u = issued > ring_stages ? issued - ring_stages : 0; u < issued; ++u)
+          if (!mbar_wait(full + u % ring_stages, u / ring_stages & 1u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
       }
     } else if (warp == 1) {
       if (elect_one()) {
         // ---------------- MMA issuer ----------------
-        uint32_t stage = 0, phase = 0;
+        uint32_t stage = 0, phase = 0, turn = 0;
         const uint32_t ring = smem_u32(smem);
-        const uint32_t idesc = fp4_idesc(NV, 1, x.cols, 0);
         const uint32_t pair_bits = fp4_idesc(NV, 1, 0, 1) ^ fp4_idesc(NV, 1, 0, 0);
+        const uint32_t sf_col = tmem + shape.accs * shape.width;
         const int whole = mmas / (kStageK / 64);
-        const bool x_ok = !RAW || wait(x_ready, 0u);
-        for (int kb = k0; kb < k1 && x_ok; ++kb) {
-          if (!wait(full + stage, phase)) break;
-          tc_fence_after();
-          const uint32_t sa = ring + stage * stage_bytes;
-          const uint32_t sb = RAW ? smem_u32(raw) + (kb - k0) * kRawStageBytes : sa + kABytes;
-          const uint32_t ssa = sa + kABytes + bbytes, ssb = RAW ? sb + kRawTokens * (kStageK / 2) : ssa + kStageSf;
-          // each ring stage has its own scale columns, 16 of W's and 16 of X's:
-          // the stage is full again only after the products that read them
-          const uint32_t tsa = tmem + shape.width + stage * 32, tsb = tsa + 16, tsx = tsb + x.xcol;
-          const uint64_t adesc = smem_desc_sw128(sa, 16, 1024), bdesc = smem_desc_sw128(sb, 16, 1024);
-          if (kb < whole) {
+        bool ok = !RAW || wait(x_ready, 0u);
+        for (uint32_t item = first; ok && item < items; item += stride, ++turn) {
+          const Tile x = tile_of(item);
+          const uint32_t idesc = fp4_idesc(NV, 1, x.cols, 0);
+          const uint32_t buf = shape.accs == 2 ? turn & 1u : 0u, acc = tmem + buf * shape.width;
+          // (turn 0 and 1 find their accumulators empty)
+          if (turn >= 2 && !(ok = wait(acc_empty + buf, (turn / 2 - 1) & 1u))) break;
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!(ok = wait(full + stage, phase))) break;
+            tc_fence_after();
+            const uint32_t sa = ring + stage * stage_bytes;
+            const uint32_t sb = RAW ? smem_u32(raw) + (kb - k0) * kRawStageBytes : sa + kABytes;
+            const uint32_t ssa = sa + kABytes + bbytes, ssb = RAW ? sb + kRawTokens * (kStageK / 2) : ssa + kStageSf;
+            // each ring stage has its own scale columns, 16 of W's and 16 of X's:
+            // the stage is full again only after the products that read them
+            const uint32_t tsa = sf_col + stage * 32, tsb = tsa + 16, tsx = tsb + x.xcol;
+            const uint64_t adesc = smem_desc_sw128(sa, 16, 1024), bdesc = smem_desc_sw128(sb, 16, 1024);
+            if (kb < whole) {
 #pragma unroll
-            for (int i = 0; i < kStageQuads; ++i) {
-              copy_scales<1>(tsa + 4 * i, ssa + i * kFp4TileBytes);
-              copy_scales<1>(tsb + 4 * i, ssb + i * kFp4TileBytes);
-            }
+              for (int i = 0; i < kStageQuads; ++i) {
+                copy_scales<1>(tsa + 4 * i, ssa + i * kFp4TileBytes);
+                copy_scales<1>(tsb + 4 * i, ssb + i * kFp4TileBytes);
+              }
 #pragma unroll
-            for (int i = 0; i < kStageK / 64; ++i)
-              mma_fp4<NV, 1>(tmem, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
-                             tsa + i / kQuadMmas * 4, tsx + i / kQuadMmas * 4, i > 0 || kb > k0);
-          } else {
-            const int q = quads - kb * kStageQuads, m = mmas - kb * (kStageK / 64);
-            for (int i = 0; i < q; ++i) {
-              copy_scales<1>(tsa + 4 * i, ssa + i * kFp4TileBytes);
-              copy_scales<1>(tsb + 4 * i, ssb + i * kFp4TileBytes);
+              for (int i = 0; i < kStageK / 64; ++i)
+                mma_fp4<NV, 1>(acc, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
+                               tsa + i / kQuadMmas * 4, tsx + i / kQuadMmas * 4, i > 0 || kb > k0);
+            } else {
+              const int q = quads - kb * kStageQuads, m = mmas - kb * (kStageK / 64);
+              for (int i = 0; i < q; ++i) {
+                copy_scales<1>(tsa + 4 * i, ssa + i * kFp4TileBytes);
+                copy_scales<1>(tsb + 4 * i, ssb + i * kFp4TileBytes);
+              }
+              for (int i = 0; i < m; ++i)
+                mma_fp4<NV, 1>(acc, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
+                               tsa + i / kQuadMmas * 4, tsx + i / kQuadMmas * 4, i > 0 || kb > k0);
             }
-            for (int i = 0; i < m; ++i)
-              mma_fp4<NV, 1>(tmem, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
-                             tsa + i / kQuadMmas * 4, tsx + i / kQuadMmas * 4, i > 0 || kb > k0);
+            mma_commit(empty + stage);
+            if (++stage == static_cast<uint32_t>(shape.stages)) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          mma_commit(empty + stage);
-          if (++stage == static_cast<uint32_t>(shape.stages)) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (ok) mma_commit(acc_full + buf);
         }
-        mma_commit(acc_full);  // (after an abort too: what was issued completes)
-        if (!mbar_wait(acc_full, 0u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
+        mma_commit(drain);
+        if (!mbar_wait(drain, 0u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
       }
     } else {
       // ---------------- epilogue ----------------
       const int quad = warp & 3;  // the tensor-memory lanes of this warp
       const int f = quad * 32 + lane;
       if (!RAW && a.early) pdl_wait();
-      float tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
-      if (RAW) {
-        tx = quantize_tile<RAW == 1, NV>(q, x, k0, k1, raw, reinterpret_cast<int*>(full) + 24, reinterpret_cast<uint32_t*>(full) + 40);
-        mbar_arrive(x_ready);
-      }
-      const Scale k = make_scale(a.wt != nullptr ? a.wt[x.g] : 1.0f, tx);
-      const int64_t r = static_cast<int64_t>(x.wtile) * kRows + f;
-      OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
-      int ok = 1;
-      if (lane == 0) ok = wait(acc_full, 0u) && !*abort_flag;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      tc_fence_after();
       if (shape.splits == 1) {
-        if (ok) {
+        uint32_t turn = 0;
+        for (uint32_t item = first; item < items; item += stride, ++turn) {
+          const Tile x = tile_of(item);
+          float tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
+          if (RAW) {
+            tx = quantize_tile<RAW == 1, NV>(q, x, k0, k1, raw, raw_src, raw_red);
+            mbar_arrive(x_ready);
+          }
+          const Scale k = make_scale(a.wt != nullptr ? a.wt[x.g] : 1.0f, tx);
+          const int64_t r = static_cast<int64_t>(x.wtile) * kRows + f;
+          OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
+          const uint32_t buf = shape.accs == 2 ? turn & 1u : 0u;
+          int ok = 1;
+          if (lane == 0) ok = wait(acc_full + buf, turn / 2 & 1u);
+          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+          tc_fence_after();
+          const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * shape.width;
 #pragma unroll 1
           for (int c = 0; c < x.count; c += 16) {
             uint32_t v[16];
-            tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, v);
+            tmem_ld_32x32b_x16(acc + c, v);
             tmem_ld_wait();
             if (r < a.rows) {
 #pragma unroll
@@ -527,8 +584,24 @@ __global__ void __launch_bounds__(kStreamThreads, RAW ? 2 : 3)
                   store_out(out + static_cast<int64_t>(c + j) * a.ldy, __uint_as_float(v[j]) * k.before * k.k);
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_empty + buf);
         }
       } else {
+        const Tile x = tile_of(first);
+        float tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
+        if (RAW) {
+          tx = quantize_tile<RAW == 1, NV>(q, x, k0, k1, raw, raw_src, raw_red);
+          mbar_arrive(x_ready);
+        }
+        const Scale k = make_scale(a.wt != nullptr ? a.wt[x.g] : 1.0f, tx);
+        const int64_t r = static_cast<int64_t>(x.wtile) * kRows + f;
+        OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
+        int ok = 1;
+        if (lane == 0) ok = wait(acc_full, 0u);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        tc_fence_after();
         // Token j belongs to rank j % splits, where it is row j / splits.  (A
         // CTA that gave up passes on what its accumulator holds, as the others
         // wait for it; the status word says that the result is not one.)
@@ -993,7 +1066,6 @@ StreamShape stream_shape(int64_t tokens, int groups, bool ragged, int64_t rows, 
   StreamShape s;
   const int64_t each = ragged ? std::max<int64_t>(64, 2 * ceil_div(tokens, groups)) : tokens;
   s.width = each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : 128;
-  s.stages = s.width <= 32 ? 4 : 3;
   s.raw_stages = 0;
   const int kstages = static_cast<int>(ceil_div(n, kStageK));
   const int64_t tiles = (ragged ? std::min<int64_t>(groups, tokens) : ceil_div(tokens, s.width)) * ceil_div(rows, kRows);
@@ -1007,6 +1079,9 @@ StreamShape stream_shape(int64_t tokens, int groups, bool ragged, int64_t rows, 
     }
     if (tiles * (k + 1) > 2 * sms) break;  // more would not run side by side
   }
+  s.accs = s.splits == 1 ? 2 : 1;
+  s.stages = s.splits == 1 ? std::min(kStreamMaxStages, kWalkRingBytes / stream_stage_bytes(s.width, false))
+                           : s.width <= 32 ? 4 : 3;
   return s;
 }
 
@@ -1023,10 +1098,11 @@ gptq_status launch_stream(const CUtensorMap& wmap, const CUtensorMap& xmap, cons
   // token tiles: each group's last one may be part full
   const int64_t tiles =
       a.offsets != nullptr ? a.tokens / s.width + std::min<int64_t>(a.groups, a.tokens) : ceil_div(a.tokens, s.width);
-  const int64_t ctas = tiles * ceil_div(a.rows, kRows) * s.splits;
-  if (ctas > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  const int64_t items = tiles * ceil_div(a.rows, kRows);
+  if (items * s.splits > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  const int64_t ctas = s.accs == 2 ? std::min<int64_t>(items, info->sm_count) : items * s.splits;
   const size_t smem = 1024 + static_cast<size_t>(s.stages) * stream_stage_bytes(s.width, RAW != 0) +
-                      stream_apart_bytes(s.width, s.splits) + (RAW ? s.raw_stages * kRawStageBytes : 0) + 256 +
+                      stream_apart_bytes(s.width, s.splits) + (RAW ? s.raw_stages * kRawStageBytes : 0) + kStreamBarBytes +
                       table_bytes(a.groups);
   return launch_cluster_pdl(fp4_stream_kernel<NV, OUT, RAW>, static_cast<unsigned>(ctas), kStreamThreads, smem, s.splits,
                             st, wmap, xmap, a, s, q) == cudaSuccess
@@ -1100,6 +1176,7 @@ static bool raw_shape(int64_t tokens, int groups, bool ragged, int64_t rows, int
   *s = stream_shape(tokens, groups, ragged, rows, n, info->sm_count);  // (the splits, and so the sums, of the two calls)
   s->width = kRawTokens;
   s->stages = 4;
+  s->accs = 1;
   s->raw_stages = static_cast<int>(ceil_div(ceil_div(n, kStageK), s->splits));
   return s->raw_stages <= kRawMaxStages;
 }
