@@ -225,10 +225,10 @@ __device__ __forceinline__ Tile tile_at(const GroupTable& t, const MatmulArgs& a
 // ---------------------------------------------------------------------------
 //
 // Bound by HBM: each weight is read once (128 * 4096 codes and their scales
-// are 288 KB of nvfp4).  With at least a tile an SM, one CTA an SM walks over
-// the tiles with a ring of up to eight stages that never runs dry between two
-// of them (64 tokens through 32 experts of 2048 x 4096: WALK us; a CTA a tile
-// took 32, as each starts with an empty ring).  A layer with fewer tiles is
+// are 288 KB of nvfp4).  With about a tile an SM or more, one CTA an SM walks
+// over the tiles with a ring of up to eight stages that never runs dry between two
+// of them, in clusters of two that share the last tile of an odd number.  A
+// layer with fewer tiles is
 // cut along K: a cluster takes a tile, each of its CTAs a part of K, two CTAs
 // an SM, and the CTAs then add up their sums in rank order, so the result does
 // not depend on timing: of a few tokens each CTA sends its sums to the one that
@@ -411,22 +411,37 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   const int wtiles = static_cast<int>((a.rows + kRows - 1) / kRows);
   // (uniform: see the pair kernel)
   const uint32_t items = ok_groups ? static_cast<uint32_t>(uniform(t.tile[a.groups])) * wtiles : 0;
-  const uint32_t first = blockIdx.x / shape.splits;
-  const uint32_t stride = shape.splits > 1 ? items : gridDim.x;  // a cluster has one tile
-  const int rank = blockIdx.x % shape.splits;  // in the cluster
+  // This cluster's tiles are items `cluster`, + clusters, ...: `whole` of them
+  // by single CTAs in turn, then what is left (`last`, one tile) by all of its
+  // CTAs, each a part of K.
+  const uint32_t clusters = gridDim.x / shape.splits, cluster = blockIdx.x / shape.splits;
+  const int rank = blockIdx.x % shape.splits;
+  const uint32_t mine_all = cluster < items ? (items - cluster + clusters - 1) / clusters : 0;
+  const uint32_t whole_tiles = shape.splits == 1 ? mine_all : shape.accs == 2 ? mine_all / shape.splits * shape.splits : 0;
+  const bool last = mine_all > whole_tiles;
   const int quads = fp4_quads(a.n, NV);
   const int mmas = (a.n + 63) / 64;
   const int kstages = (a.n + kStageK - 1) / kStageK;
-  const int k0 = kstages * rank / shape.splits, k1 = kstages * (rank + 1) / shape.splits;
+  const int k0 = kstages * rank / shape.splits, k1 = kstages * (rank + 1) / shape.splits;  // of the last tile
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, a.wait_ns, abort_flag, a.status);
   };
-  auto tile_of = [&](uint32_t item) { return tile_at<true>(t, a, wtiles, shape.width, item); };
+  // this CTA's tiles, as m: rank, rank + splits, ... below whole_tiles, then the last one
+  constexpr uint32_t kEnd = 0xffffffffu;
+  const uint32_t after = last ? whole_tiles : kEnd;
+  const uint32_t first_m = static_cast<uint32_t>(rank) < whole_tiles ? rank : after;
+  auto next_m = [&](uint32_t m) {
+    if (m >= whole_tiles) return kEnd;
+    m += shape.splits;
+    return m < whole_tiles ? m : after;
+  };
+  // the cluster's m-th tile
+  auto tile_of = [&](uint32_t m) { return tile_at<true>(t, a, wtiles, shape.width, cluster + m * clusters); };
 
-  if (first < items) {
-    // (of a cluster's one tile, and the same in all of its CTAs)
-    const bool push = shape.splits > 1 && tile_of(first).count <= kPushTokens;
+  if (mine_all > 0) {
+    // (the same in all CTAs of the cluster)
+    const bool push = last && tile_of(whole_tiles).count <= kPushTokens;
     if (warp == 0) {
       if (elect_one()) {
         // ---------------- producer ----------------
@@ -435,10 +450,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           const uint8_t* wsc;
           const uint8_t* xsc;
         } src;
-        uint32_t item;
-        int kb;
+        uint32_t m;
+        int kb, kend;
         auto take = [&] {
-          const Tile x = tile_of(item);
+          kb = m < whole_tiles ? 0 : k0;
+          kend = m < whole_tiles ? kstages : k1;
+          const Tile x = tile_of(m);
           src.wy = static_cast<int>(x.g * a.rows) + x.wtile * kRows;
           src.token = x.token;
           src.boxes = RAW ? 0 : (x.cols + kBoxRows - 1) / kBoxRows;
@@ -446,15 +463,13 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           src.xsc = a.xscales + static_cast<int64_t>(x.xband) * quads * kFp4TileBytes;
         };
         auto start = [&] {
-          item = first;
-          kb = k0;
+          m = first_m;
           take();
         };
         auto next = [&] {
-          if (++kb == k1) {
-            kb = k0;
-            item += stride;
-            if (item < items) take();
+          if (++kb == kend) {
+            m = next_m(m);
+            if (m != kEnd) take();
           }
         };
         auto load_w = [&](uint32_t stage) {
@@ -475,12 +490,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         // the ring's first round: W before X is there
         uint32_t issued = 0;
         const uint32_t ring_stages = shape.stages;
-        for (start(); issued < ring_stages && item < items; ++issued, next()) load_w(issued);
+        for (start(); issued < ring_stages && m != kEnd; ++issued, next()) load_w(issued);
         if (!RAW && a.early) pdl_wait();
         start();
         for (uint32_t i = 0; i < issued; ++i, next()) load_x(i);
         uint32_t stage = 0, phase = 1;
-        for (; item < items; next(), ++issued) {
+        for (; m != kEnd; next(), ++issued) {
           if (!wait(empty + stage, phase ^ 1u)) break;
           load_w(stage);
           load_x(stage);
@@ -502,17 +517,18 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         const uint32_t sf_col = tmem + shape.accs * shape.width;
         const int whole = mmas / (kStageK / 64);
         bool ok = !RAW || wait(x_ready, 0u);
-        for (uint32_t item = first; ok && item < items; item += stride, ++turn) {
-          const Tile x = tile_of(item);
+        for (uint32_t m = first_m; ok && m != kEnd; m = next_m(m), ++turn) {
+          const Tile x = tile_of(m);
+          const int kbeg = m < whole_tiles ? 0 : k0, kend = m < whole_tiles ? kstages : k1;
           const uint32_t idesc = fp4_idesc(NV, 1, x.cols, 0);
           const uint32_t buf = shape.accs == 2 ? turn & 1u : 0u, acc = tmem + buf * shape.width;
           // (turn 0 and 1 find their accumulators empty)
           if (turn >= 2 && !(ok = wait(acc_empty + buf, (turn / 2 - 1) & 1u))) break;
-          for (int kb = k0; kb < k1; ++kb) {
+          for (int kb = kbeg; kb < kend; ++kb) {
             if (!(ok = wait(full + stage, phase))) break;
             tc_fence_after();
             const uint32_t sa = ring + stage * stage_bytes;
-            const uint32_t sb = RAW ? smem_u32(raw) + (kb - k0) * kRawStageBytes : sa + kABytes;
+            const uint32_t sb = RAW ? smem_u32(raw) + (kb - kbeg) * kRawStageBytes : sa + kABytes;
             const uint32_t ssa = sa + kABytes + bbytes, ssb = RAW ? sb + kRawTokens * (kStageK / 2) : ssa + kStageSf;
             // each ring stage has its own scale columns, 16 of W's and 16 of X's:
             // the stage is full again only after the products that read them
@@ -527,16 +543,16 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 #pragma unroll
               for (int i = 0; i < kStageK / 64; ++i)
                 mma_fp4<NV, 1>(acc, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
-                               tsa + i / kQuadMmas * 4, tsx + i / kQuadMmas * 4, i > 0 || kb > k0);
+                               tsa + i / kQuadMmas * 4, tsx + i / kQuadMmas * 4, i > 0 || kb > kbeg);
             } else {
-              const int q = quads - kb * kStageQuads, m = mmas - kb * (kStageK / 64);
+              const int q = quads - kb * kStageQuads, left = mmas - kb * (kStageK / 64);
               for (int i = 0; i < q; ++i) {
                 copy_scales<1>(tsa + 4 * i, ssa + i * kFp4TileBytes);
                 copy_scales<1>(tsb + 4 * i, ssb + i * kFp4TileBytes);
               }
-              for (int i = 0; i < m; ++i)
+              for (int i = 0; i < left; ++i)
                 mma_fp4<NV, 1>(acc, adesc + 2 * i, bdesc + 2 * i, i % kQuadMmas ? idesc | pair_bits : idesc,
-                               tsa + i / kQuadMmas * 4, tsx + i / kQuadMmas * 4, i > 0 || kb > k0);
+                               tsa + i / kQuadMmas * 4, tsx + i / kQuadMmas * 4, i > 0 || kb > kbeg);
             }
             mma_commit(empty + stage);
             if (++stage == static_cast<uint32_t>(shape.stages)) {
@@ -554,42 +570,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       const int quad = warp & 3;  // the tensor-memory lanes of this warp
       const int f = quad * 32 + lane;
       if (!RAW && a.early) pdl_wait();
-      if (shape.splits == 1) {
-        uint32_t turn = 0;
-        for (uint32_t item = first; item < items; item += stride, ++turn) {
-          const Tile x = tile_of(item);
-          float tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
-          if (RAW) {
-            tx = quantize_tile<RAW == 1, NV>(q, x, k0, k1, raw, raw_src, raw_red);
-            mbar_arrive(x_ready);
-          }
-          const Scale k = make_scale(a.wt != nullptr ? a.wt[x.g] : 1.0f, tx);
-          const int64_t r = static_cast<int64_t>(x.wtile) * kRows + f;
-          OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
-          const uint32_t buf = shape.accs == 2 ? turn & 1u : 0u;
-          int ok = 1;
-          if (lane == 0) ok = wait(acc_full + buf, turn / 2 & 1u);
-          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-          tc_fence_after();
-          const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * shape.width;
-#pragma unroll 1
-          for (int c = 0; c < x.count; c += 16) {
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(acc + c, v);
-            tmem_ld_wait();
-            if (r < a.rows) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (c + j < x.count)
-                  store_out(out + static_cast<int64_t>(c + j) * a.ldy, __uint_as_float(v[j]) * k.before * k.k);
-            }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(acc_empty + buf);
-        }
-      } else {
-        const Tile x = tile_of(first);
+      uint32_t turn = 0;
+      bool going = true;
+      for (uint32_t m = rank; m < whole_tiles; m += shape.splits, ++turn) {
+        const Tile x = tile_of(m);
         float tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
         if (RAW) {
           tx = quantize_tile<RAW == 1, NV>(q, x, k0, k1, raw, raw_src, raw_red);
@@ -598,8 +582,45 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         const Scale k = make_scale(a.wt != nullptr ? a.wt[x.g] : 1.0f, tx);
         const int64_t r = static_cast<int64_t>(x.wtile) * kRows + f;
         OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
+        const uint32_t buf = shape.accs == 2 ? turn & 1u : 0u;
         int ok = 1;
-        if (lane == 0) ok = wait(acc_full, 0u);
+        if (lane == 0) ok = wait(acc_full + buf, turn / 2 & 1u);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) {
+          going = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * shape.width;
+#pragma unroll 1
+        for (int c = 0; c < x.count; c += 16) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(acc + c, v);
+          tmem_ld_wait();
+          if (r < a.rows) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < x.count)
+                store_out(out + static_cast<int64_t>(c + j) * a.ldy, __uint_as_float(v[j]) * k.before * k.k);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + buf);
+      }
+      if (last) {
+        const Tile x = tile_of(whole_tiles);
+        float tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
+        if (RAW) {
+          tx = quantize_tile<RAW == 1, NV>(q, x, k0, k1, raw, raw_src, raw_red);
+          mbar_arrive(x_ready);
+        }
+        const Scale k = make_scale(a.wt != nullptr ? a.wt[x.g] : 1.0f, tx);
+        const int64_t r = static_cast<int64_t>(x.wtile) * kRows + f;
+        OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
+        const uint32_t buf = shape.accs == 2 ? turn & 1u : 0u;
+        const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * shape.width;
+        int ok = going;
+        if (lane == 0 && going) ok = wait(acc_full + buf, turn / 2 & 1u);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         tc_fence_after();
         // Token j belongs to rank j % splits, where it is row j / splits.  (A
@@ -618,7 +639,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           // the sums of source rank q stand at [q][row][feature]
           const uint32_t at = smem_u32(collect) + (rank * rows_each * kRows + f) * 4, bar = smem_u32(sums_in);
           uint32_t v[16];
-          tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16), v);
+          tmem_ld_32x32b_x16(acc, v);
           tmem_ld_wait();
           int owner = 0, row = 0;
 #pragma unroll
@@ -649,7 +670,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 #pragma unroll 1
           for (int c = 0; c < x.count; c += 16) {
             uint32_t v[16];
-            tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, v);
+            tmem_ld_32x32b_x16(acc + c, v);
             tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 16; ++j)
@@ -689,7 +710,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       tc_fence_before();
     }
     __syncwarp();
-    if (shape.splits > 1 && warp < 2) {  // the barriers of the epilogue
+    if (last && warp < 2) {  // the barriers of the epilogue
       cluster_wait();
       if (!push || apart == 0) {
         cluster_arrive();
@@ -698,9 +719,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       cluster_arrive();
       cluster_wait();
     }
-  } else if (shape.splits > 1) {
-    cluster_wait();
   }
+  if (shape.splits > 1 && !last) cluster_wait();
   if (!RAW && a.early) pdl_wait();  // (in every CTA: this kernel does not end before the quantiser)
   tc_fence_before();
   __syncthreads();
@@ -1060,8 +1080,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // How few tokens are laid out.  Tiles are as wide as the tokens; groups, whose
 // sizes the host does not know, take 64 or 128 (a group's second tile of 64
 // starts at the third scale column of its band; a narrower one would start
-// inside a column).  K is split so that the chip's SMs get about the same
-// number of stages: cost(S) = stages that the busiest SM works off.
+// inside a column).  Clusters are chosen for the stages of K that the busiest
+// SM works off: two CTAs that walk over whole tiles and share an odd last one,
+// or k CTAs a tile.  (One token, n = 4096: 32 row tiles take 4 CTAs each; 48
+// tokens, 86 row tiles: 3 each, 12 stages instead of 16.)
 StreamShape stream_shape(int64_t tokens, int groups, bool ragged, int64_t rows, int n, int sms) {
   StreamShape s;
   const int64_t each = ragged ? std::max<int64_t>(64, 2 * ceil_div(tokens, groups)) : tokens;
@@ -1069,19 +1091,20 @@ StreamShape stream_shape(int64_t tokens, int groups, bool ragged, int64_t rows, 
   s.raw_stages = 0;
   const int kstages = static_cast<int>(ceil_div(n, kStageK));
   const int64_t tiles = (ragged ? std::min<int64_t>(groups, tokens) : ceil_div(tokens, s.width)) * ceil_div(rows, kRows);
-  int64_t best = INT64_MAX;
-  s.splits = 1;
-  for (int k = 1; k <= 8 && k <= kstages; ++k) {
+  const int64_t share = ceil_div(tiles, std::max(1, sms / 2));  // tiles of a walking pair
+  int64_t best = kstages >= 2 ? share / 2 * kstages + share % 2 * ((kstages + 1) / 2) : ceil_div(tiles, sms);
+  s.splits = 0;
+  for (int k = 2; k <= 8 && k <= kstages && tiles * k <= 2 * sms; ++k) {  // (more would not run side by side)
     const int64_t cost = ceil_div(tiles * k, sms) * ceil_div(kstages, k);
-    if (cost < best) {
+    if (cost < best || (cost == best && s.splits == 0)) {
       best = cost;
       s.splits = k;
     }
-    if (tiles * (k + 1) > 2 * sms) break;  // more would not run side by side
   }
-  s.accs = s.splits == 1 ? 2 : 1;
-  s.stages = s.splits == 1 ? std::min(kStreamMaxStages, kWalkRingBytes / stream_stage_bytes(s.width, false))
-                           : s.width <= 32 ? 4 : 3;
+  s.accs = s.splits == 0 ? 2 : 1;
+  s.stages = s.accs == 2 ? std::min(kStreamMaxStages, kWalkRingBytes / stream_stage_bytes(s.width, false))
+                         : s.width <= 32 ? 4 : 3;
+  if (s.splits == 0) s.splits = kstages >= 2 ? 2 : 1;
   return s;
 }
 
@@ -1100,7 +1123,8 @@ gptq_status launch_stream(const CUtensorMap& wmap, const CUtensorMap& xmap, cons
       a.offsets != nullptr ? a.tokens / s.width + std::min<int64_t>(a.groups, a.tokens) : ceil_div(a.tokens, s.width);
   const int64_t items = tiles * ceil_div(a.rows, kRows);
   if (items * s.splits > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-  const int64_t ctas = s.accs == 2 ? std::min<int64_t>(items, info->sm_count) : items * s.splits;
+  // clusters walk over the items, or have one each
+  const int64_t ctas = s.splits * (s.accs == 2 ? std::min<int64_t>(items, std::max(1, info->sm_count / s.splits)) : items);
   const size_t smem = 1024 + static_cast<size_t>(s.stages) * stream_stage_bytes(s.width, RAW != 0) +
                       stream_apart_bytes(s.width, s.splits) + (RAW ? s.raw_stages * kRawStageBytes : 0) + kStreamBarBytes +
                       table_bytes(a.groups);
@@ -1174,9 +1198,9 @@ static bool weight_map(CUtensorMap* map, const uint8_t* wq, int groups, int64_t 
 static bool raw_shape(int64_t tokens, int groups, bool ragged, int64_t rows, int n, const DeviceInfo* info, StreamShape* s) {
   if (tokens > kRawTokens || tokens * n > kFp4SelfValues) return false;
   *s = stream_shape(tokens, groups, ragged, rows, n, info->sm_count);  // (the splits, and so the sums, of the two calls)
+  if (s->accs == 2) return false;  // (it walks)
   s->width = kRawTokens;
   s->stages = 4;
-  s->accs = 1;
   s->raw_stages = static_cast<int>(ceil_div(ceil_div(n, kStageK), s->splits));
   return s->raw_stages <= kRawMaxStages;
 }
