@@ -344,8 +344,9 @@ __device__ __forceinline__ float quantize_tile(const QuantArgs& a, const Tile& x
   return u.t;
 }
 
-// RAW: 0 X is quantised; 1 bf16, 2 fp32 X of q.
-template <bool NV, typename OUT, int RAW>
+// RAW: 0 X is quantised; 1 bf16, 2 fp32 X of q.  WALK: the CTAs walk over the
+// tiles; without, a cluster has one tile (and no table of a single group).
+template <bool NV, typename OUT, int RAW, bool WALK>
 __global__ void __launch_bounds__(kStreamThreads, 2)
     fp4_stream_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, MatmulArgs a,
                       StreamShape shape, QuantArgs q) {
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   constexpr int kStageQuads = kStageK / (4 * kBlk);
   constexpr int kQuadMmas = kBlk / 16;
   constexpr uint32_t kStageSf = kStageQuads * kFp4TileBytes;
-  const uint32_t tmem_cols = stream_tmem_cols(shape.width, shape.accs, shape.stages);
+  const uint32_t tmem_cols = stream_tmem_cols(shape.width, WALK ? 2 : 1, shape.stages);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < shape.stages; ++s) {
@@ -407,17 +408,20 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   if (shape.splits > 1) cluster_arrive();
   pdl_trigger();
   if (RAW || !a.early) pdl_wait();
-  const bool ok_groups = group_table<true>(t, a, shape.width);
+  const bool ok_groups = group_table<WALK>(t, a, shape.width);
   const int wtiles = static_cast<int>((a.rows + kRows - 1) / kRows);
   // (uniform: see the pair kernel)
-  const uint32_t items = ok_groups ? static_cast<uint32_t>(uniform(t.tile[a.groups])) * wtiles : 0;
+  const uint32_t token_tiles = WALK || a.offsets != nullptr ? uniform(t.tile[a.groups])
+                                                            : static_cast<int>((a.tokens + shape.width - 1) / shape.width);
+  const uint32_t items = ok_groups ? token_tiles * wtiles : 0;
   // This cluster's tiles are items `cluster`, + clusters, ...: `whole` of them
   // by single CTAs in turn, then what is left (`last`, one tile) by all of its
   // CTAs, each a part of K.
   const uint32_t clusters = gridDim.x / shape.splits, cluster = blockIdx.x / shape.splits;
   const int rank = blockIdx.x % shape.splits;
-  const uint32_t mine_all = cluster < items ? (items - cluster + clusters - 1) / clusters : 0;
-  const uint32_t whole_tiles = shape.splits == 1 ? mine_all : shape.accs == 2 ? mine_all / shape.splits * shape.splits : 0;
+  const uint32_t mine_all = cluster >= items ? 0 : WALK ? (items - cluster + clusters - 1) / clusters : 1;
+  const uint32_t whole_tiles = WALK ? mine_all / shape.splits * shape.splits : 0;
+  constexpr int kAccs = WALK ? 2 : 1;
   const bool last = mine_all > whole_tiles;
   const int quads = fp4_quads(a.n, NV);
   const int mmas = (a.n + 63) / 64;
@@ -437,7 +441,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     return m < whole_tiles ? m : after;
   };
   // the cluster's m-th tile
-  auto tile_of = [&](uint32_t m) { return tile_at<true>(t, a, wtiles, shape.width, cluster + m * clusters); };
+  auto tile_of = [&](uint32_t m) { return tile_at<WALK>(t, a, wtiles, shape.width, WALK ? cluster + m * clusters : cluster); };
 
   if (mine_all > 0) {
     // (the same in all CTAs of the cluster)
@@ -514,16 +518,16 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         uint32_t stage = 0, phase = 0, turn = 0;
         const uint32_t ring = smem_u32(smem);
         const uint32_t pair_bits = fp4_idesc(NV, 1, 0, 1) ^ fp4_idesc(NV, 1, 0, 0);
-        const uint32_t sf_col = tmem + shape.accs * shape.width;
+        const uint32_t sf_col = tmem + kAccs * shape.width;
         const int whole = mmas / (kStageK / 64);
         bool ok = !RAW || wait(x_ready, 0u);
         for (uint32_t m = first_m; ok && m != kEnd; m = next_m(m), ++turn) {
           const Tile x = tile_of(m);
           const int kbeg = m < whole_tiles ? 0 : k0, kend = m < whole_tiles ? kstages : k1;
           const uint32_t idesc = fp4_idesc(NV, 1, x.cols, 0);
-          const uint32_t buf = shape.accs == 2 ? turn & 1u : 0u, acc = tmem + buf * shape.width;
+          const uint32_t buf = WALK ? turn & 1u : 0u, acc = tmem + buf * shape.width;
           // (turn 0 and 1 find their accumulators empty)
-          if (turn >= 2 && !(ok = wait(acc_empty + buf, (turn / 2 - 1) & 1u))) break;
+          if (WALK && turn >= 2 && !(ok = wait(acc_empty + buf, (turn / 2 - 1) & 1u))) break;
           for (int kb = kbeg; kb < kend; ++kb) {
             if (!(ok = wait(full + stage, phase))) break;
             tc_fence_after();
@@ -574,15 +578,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       bool going = true;
       for (uint32_t m = rank; m < whole_tiles; m += shape.splits, ++turn) {
         const Tile x = tile_of(m);
-        float tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
-        if (RAW) {
-          tx = quantize_tile<RAW == 1, NV>(q, x, k0, k1, raw, raw_src, raw_red);
-          mbar_arrive(x_ready);
-        }
+        const float tx = a.xt != nullptr ? a.xt[x.g] : 1.0f;
         const Scale k = make_scale(a.wt != nullptr ? a.wt[x.g] : 1.0f, tx);
         const int64_t r = static_cast<int64_t>(x.wtile) * kRows + f;
         OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
-        const uint32_t buf = shape.accs == 2 ? turn & 1u : 0u;
+        const uint32_t buf = WALK ? turn & 1u : 0u;
         int ok = 1;
         if (lane == 0) ok = wait(acc_full + buf, turn / 2 & 1u);
         if (!__shfl_sync(0xffffffffu, ok, 0)) {
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         const Scale k = make_scale(a.wt != nullptr ? a.wt[x.g] : 1.0f, tx);
         const int64_t r = static_cast<int64_t>(x.wtile) * kRows + f;
         OUT* out = static_cast<OUT*>(a.y) + static_cast<int64_t>(x.token) * a.ldy + r;
-        const uint32_t buf = shape.accs == 2 ? turn & 1u : 0u;
+        const uint32_t buf = WALK ? turn & 1u : 0u;
         const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * shape.width;
         int ok = going;
         if (lane == 0 && going) ok = wait(acc_full + buf, turn / 2 & 1u);
@@ -878,8 +878,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
   pdl_trigger();
-  pdl_wait();
+  if (!a.early) pdl_wait();
   const bool ok_groups = group_table<true>(t, a, kTokens);
+  if (a.early) pdl_wait();
   const int wtiles = static_cast<int>((a.rows + kPairRows - 1) / kPairRows);
   const int wbands = static_cast<int>((a.rows + kRows - 1) / kRows);
   // (read from the table by every lane and passed through `uniform`: the
@@ -1103,17 +1104,17 @@ StreamShape stream_shape(int64_t tokens, int groups, bool ragged, int64_t rows, 
   }
   s.accs = s.splits == 0 ? 2 : 1;
   s.stages = s.accs == 2 ? std::min(kStreamMaxStages, kWalkRingBytes / stream_stage_bytes(s.width, false))
-                         : s.width <= 32 ? 4 : 3;
+                         : s.width <= 16 ? 4 : 3;  // (two CTAs an SM, with 32 rows of sums apart)
   if (s.splits == 0) s.splits = kstages >= 2 ? 2 : 1;
   return s;
 }
 
-template <bool NV, typename OUT, int RAW>
+template <bool NV, typename OUT, int RAW, bool WALK>
 gptq_status launch_stream(const CUtensorMap& wmap, const CUtensorMap& xmap, const MatmulArgs& a, const StreamShape& s,
                           const QuantArgs& q, const DeviceInfo* info, cudaStream_t st) {
   static std::atomic<bool> attr_set[64] = {};  // per device, shared by host threads
   if (!attr_set[info->device]) {
-    if (cudaFuncSetAttribute(fp4_stream_kernel<NV, OUT, RAW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(fp4_stream_kernel<NV, OUT, RAW, WALK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kStreamMaxSmem)) != cudaSuccess)
       return GPTQ_ERR_CUDA;
     attr_set[info->device] = true;
@@ -1128,7 +1129,7 @@ gptq_status launch_stream(const CUtensorMap& wmap, const CUtensorMap& xmap, cons
   const size_t smem = 1024 + static_cast<size_t>(s.stages) * stream_stage_bytes(s.width, RAW != 0) +
                       stream_apart_bytes(s.width, s.splits) + (RAW ? s.raw_stages * kRawStageBytes : 0) + kStreamBarBytes +
                       table_bytes(a.groups);
-  return launch_cluster_pdl(fp4_stream_kernel<NV, OUT, RAW>, static_cast<unsigned>(ctas), kStreamThreads, smem, s.splits,
+  return launch_cluster_pdl(fp4_stream_kernel<NV, OUT, RAW, WALK>, static_cast<unsigned>(ctas), kStreamThreads, smem, s.splits,
                             st, wmap, xmap, a, s, q) == cudaSuccess
              ? launch_status()
              : GPTQ_ERR_CUDA;
@@ -1155,6 +1156,28 @@ gptq_status launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const 
                             xsmap, ymap, a) == cudaSuccess
              ? launch_status()
              : GPTQ_ERR_CUDA;
+}
+
+// Whether the pair kernel takes it.  Both are timed on nvfp4 products, in us:
+//   tokens                 8     32    64    96    128   256
+//   4096 x 4096   stream   6.5   7.7   9.5   11.0  12.4  12.8
+//                 pair     9.7   9.4   9.6   9.8   10.0  10.6
+//   4096 x 11008  stream   8.8   9.6   12.2  14.0  15.4  18.8   (rows x columns)
+//                 pair     17.9  17.8  17.9  18.2  18.5  19.6
+// The stream kernel pays for tokens (sums to exchange), the pair kernel, which
+// does not cut K, for its depth.  Above 128 tokens it is the pair kernel, up to
+// 64 the other, and between them the sums below, which are fitted to these
+// times.  Groups: 32 of 2048 x 4096 take 32.7 and 34.2 us at 32 tokens each,
+// 38.9 and 36.4 at 96; 8 of 2048 x 2048 8.5 and 8.6 at 8, 10.2 and 8.4 at 32.
+bool many_tokens(int64_t tokens, int groups, bool ragged, int64_t rows, int n, int sms) {
+  if (ragged) return tokens > 32 * static_cast<int64_t>(groups);
+  if (tokens <= 64 || tokens > kFp4Band) return tokens > kFp4Band;
+  const int kstages = static_cast<int>(ceil_div(n, kStageK));
+  const StreamShape s = stream_shape(tokens, groups, ragged, rows, n, sms);
+  const int64_t tiles = ceil_div(rows, kRows) * (s.accs == 2 ? 1 : s.splits);
+  const double stream = 5.5 + 0.04 * tokens + 0.43 * ceil_div(tiles, sms) * ceil_div(kstages, s.accs == 2 ? 1 : s.splits);
+  const double pair = 4.5 + 0.31 * kstages * ceil_div(ceil_div(rows, kPairRows), std::max(1, sms / 2));
+  return pair < stream;
 }
 
 // Scale tiles as bytes x quads x bands, `bands` bands a box.
@@ -1196,7 +1219,7 @@ static bool weight_map(CUtensorMap* map, const uint8_t* wq, int groups, int64_t 
 // few tokens whose values every CTA may read, and a K range that its shared
 // memory holds.
 static bool raw_shape(int64_t tokens, int groups, bool ragged, int64_t rows, int n, const DeviceInfo* info, StreamShape* s) {
-  if (tokens > kRawTokens || tokens * n > kFp4SelfValues) return false;
+  if (tokens > kRawTokens || tokens * n > kFp4RawValues) return false;
   *s = stream_shape(tokens, groups, ragged, rows, n, info->sm_count);  // (the splits, and so the sums, of the two calls)
   if (s->accs == 2) return false;  // (it walks)
   s->width = kRawTokens;
@@ -1226,16 +1249,16 @@ gptq_status fp4_raw_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, c
   const QuantArgs q = fp4_quant_args(X, x_bf16, x_rows, n, ldx, row_index, tokens, offsets, groups, x_tensor != nullptr,
                                      const_cast<float*>(x_tensor), info->status);
   if (nv && x_bf16)
-    return y_bf16 ? launch_stream<true, __nv_bfloat16, 1>(wmap, wmap, a, s, q, info, st)
-                  : launch_stream<true, float, 1>(wmap, wmap, a, s, q, info, st);
+    return y_bf16 ? launch_stream<true, __nv_bfloat16, 1, false>(wmap, wmap, a, s, q, info, st)
+                  : launch_stream<true, float, 1, false>(wmap, wmap, a, s, q, info, st);
   if (nv)
-    return y_bf16 ? launch_stream<true, __nv_bfloat16, 2>(wmap, wmap, a, s, q, info, st)
-                  : launch_stream<true, float, 2>(wmap, wmap, a, s, q, info, st);
+    return y_bf16 ? launch_stream<true, __nv_bfloat16, 2, false>(wmap, wmap, a, s, q, info, st)
+                  : launch_stream<true, float, 2, false>(wmap, wmap, a, s, q, info, st);
   if (x_bf16)
-    return y_bf16 ? launch_stream<false, __nv_bfloat16, 1>(wmap, wmap, a, s, q, info, st)
-                  : launch_stream<false, float, 1>(wmap, wmap, a, s, q, info, st);
-  return y_bf16 ? launch_stream<false, __nv_bfloat16, 2>(wmap, wmap, a, s, q, info, st)
-                : launch_stream<false, float, 2>(wmap, wmap, a, s, q, info, st);
+    return y_bf16 ? launch_stream<false, __nv_bfloat16, 1, false>(wmap, wmap, a, s, q, info, st)
+                  : launch_stream<false, float, 1, false>(wmap, wmap, a, s, q, info, st);
+  return y_bf16 ? launch_stream<false, __nv_bfloat16, 2, false>(wmap, wmap, a, s, q, info, st)
+                : launch_stream<false, float, 2, false>(wmap, wmap, a, s, q, info, st);
 }
 
 gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const float* wt, int groups, int64_t rows,
@@ -1253,14 +1276,21 @@ gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const
   a.xscales = xscales;
   a.xt = xt;
   a.early = early;
-  if (tokens <= kFp4Band * static_cast<int64_t>(groups)) {
+  if (!many_tokens(tokens, groups, offsets != nullptr, rows, n, info->sm_count)) {
     const StreamShape s = stream_shape(tokens, groups, offsets != nullptr, rows, n, info->sm_count);
     const QuantArgs none = {};
+    if (s.accs == 2) {
+      if (nv)
+        return y_bf16 ? launch_stream<true, __nv_bfloat16, 0, true>(wmap, xmap, a, s, none, info, st)
+                      : launch_stream<true, float, 0, true>(wmap, xmap, a, s, none, info, st);
+      return y_bf16 ? launch_stream<false, __nv_bfloat16, 0, true>(wmap, xmap, a, s, none, info, st)
+                    : launch_stream<false, float, 0, true>(wmap, xmap, a, s, none, info, st);
+    }
     if (nv)
-      return y_bf16 ? launch_stream<true, __nv_bfloat16, 0>(wmap, xmap, a, s, none, info, st)
-                    : launch_stream<true, float, 0>(wmap, xmap, a, s, none, info, st);
-    return y_bf16 ? launch_stream<false, __nv_bfloat16, 0>(wmap, xmap, a, s, none, info, st)
-                  : launch_stream<false, float, 0>(wmap, xmap, a, s, none, info, st);
+      return y_bf16 ? launch_stream<true, __nv_bfloat16, 0, false>(wmap, xmap, a, s, none, info, st)
+                    : launch_stream<true, float, 0, false>(wmap, xmap, a, s, none, info, st);
+    return y_bf16 ? launch_stream<false, __nv_bfloat16, 0, false>(wmap, xmap, a, s, none, info, st)
+                  : launch_stream<false, float, 0, false>(wmap, xmap, a, s, none, info, st);
   }
   const int64_t quads = fp4_quads(n, nv);
   const int64_t xbands = offsets != nullptr ? fp4_bands(tokens, groups, true) : ceil_div(tokens, kFp4Band);

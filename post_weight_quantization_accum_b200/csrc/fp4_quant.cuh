@@ -12,9 +12,16 @@
 namespace gptq {
 
 // Up to here every CTA reads its group's values itself instead of waiting for
-// another kernel's maxima: 32 KB of bf16 take it about a microsecond, a second
-// launch and its maxima three.
-constexpr int64_t kFp4SelfValues = 16384;
+// another kernel's maxima: 128 KB of bf16 take it about two microseconds, a
+// second launch and its maxima three.  Groups count by their mean size (if all
+// rows were in one, its CTAs would read it at L2's pace).
+constexpr int64_t kFp4SelfValues = 65536;
+inline bool fp4_self_max(int64_t rows, int n, int groups, bool ragged) {
+  return ragged ? rows * n <= 32 * kFp4SelfValues && rows * n <= kFp4SelfValues / 2 * groups : rows / groups * n <= kFp4SelfValues;
+}
+// Up to here the CTAs of a product quantise its tokens themselves, each all of
+// its part of K and, for the maximum, each all values.
+constexpr int64_t kFp4RawValues = 16384;
 
 struct QuantArgs {
   const void* X;
@@ -31,6 +38,7 @@ struct QuantArgs {
   float* deq;
   float* partial;  // amax of (band, split); nullptr: each CTA takes its group's maximum itself
   int splits;      // of a band's columns in `partial`
+  int strips;      // a band's rows are quantised by that many CTAs: 1, or 4 of 32 rows
   int given;  // tensor_scale is read, not made
   int align;  // bytes (32, 16 or 0) that every row of X starts on
   int* status;

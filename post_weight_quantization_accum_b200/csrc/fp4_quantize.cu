@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) 
   const int chunks = (a.n + kChunk - 1) / kChunk;
   // (after a pass for the maxima: from its end, whose values are still in L2)
   const unsigned at = NV && a.partial != nullptr ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-  const int64_t band = at / chunks;
-  const int chunk = at % chunks;
+  const int64_t band = at / chunks / a.strips;
+  const int strip = at / chunks % a.strips, chunk = at % chunks;
   if (NV && !a.given && blockIdx.x == 0) {  // groups without rows have no CTA of their own
     for (int g = threadIdx.x; g < a.groups; g += kThreads)
       if (a.offsets != nullptr ? t.off[g] == t.off[g + 1] : a.group_rows == 0) a.tensor_scale[g] = FLT_MIN;
@@ -279,11 +279,14 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) 
         m = cta_max(m, red);
       }
       tensor = fmaxf(__fdiv_rn(__uint_as_float(m), 2688.0f), FLT_MIN);
-      if (band == b.first && chunk == 0 && threadIdx.x == 0) a.tensor_scale[b.g] = tensor;
+      if (band == b.first && chunk == 0 && strip == 0 && threadIdx.x == 0) a.tensor_scale[b.g] = tensor;
     }
     u = unit_of(tensor);
   }
-  if (b.rows < kFp4Band || (chunk + 1) * kChunk > a.n) {  // bytes that have no row or block are zero
+  const int height = kFp4Band / a.strips;
+  b.r0 += strip * height;
+  b.rows = max(0, min(height, b.rows - strip * height));
+  if (b.rows < height || (chunk + 1) * kChunk > a.n) {  // bytes that have no row or block are zero
     for (int i = threadIdx.x; i < int(sizeof(sc)) / 4; i += kThreads) reinterpret_cast<uint32_t*>(sc)[i] = 0;
   }
   band_rows(a, b.r0, b.rows, src);
@@ -300,8 +303,13 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) 
   const int q0 = chunk * kQuads;
   const int bytes = min(kQuads, quads - q0) * kFp4TileBytes;
   uint8_t* out = a.scales + (band * quads + q0) * kFp4TileBytes;
-  for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16)
-    *reinterpret_cast<uint4*>(out + i) = *reinterpret_cast<const uint4*>(sc + i);
+  if (a.strips == 1) {
+    for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16)
+      *reinterpret_cast<uint4*>(out + i) = *reinterpret_cast<const uint4*>(sc + i);
+  } else {  // rows 32 strip .. 32 strip + 31 are the strip-th word of each 16 bytes, and stand at the first in `sc`
+    for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16)
+      *reinterpret_cast<uint32_t*>(out + i + 4 * strip) = *reinterpret_cast<const uint32_t*>(sc + i);
+  }
 }
 
 // Parts of a band's columns in the pass that takes the maxima: a chunk each, or
@@ -314,11 +322,14 @@ int amax_splits(int64_t bands, int n) {
 template <bool BF16, bool NV>
 gptq_status launch_quantize(QuantArgs& a, int64_t bands, const DeviceInfo* info, cudaStream_t st) {
   const int64_t chunks = ceil_div(a.n, kChunk);
+  // few bands: a CTA takes 32 rows of one, so that more SMs have work (48 and
+  // 128 rows of 4096: STRIPS)
+  a.strips = bands * chunks <= info->sm_count && a.rows > 32 ? 4 : 1;
   if (a.partial != nullptr) {
     if (launch_pdl(fp4_amax_kernel<BF16, NV>, static_cast<unsigned>(bands * a.splits), kThreads, 0, st, a) != cudaSuccess)
       return GPTQ_ERR_CUDA;
   }
-  if (launch_pdl(fp4_quantize_kernel<BF16, NV>, static_cast<unsigned>(bands * chunks), kThreads, 0, st, a) != cudaSuccess)
+  if (launch_pdl(fp4_quantize_kernel<BF16, NV>, static_cast<unsigned>(bands * a.strips * chunks), kThreads, 0, st, a) != cudaSuccess)
     return GPTQ_ERR_CUDA;
   return launch_status();
 }
@@ -326,7 +337,7 @@ gptq_status launch_quantize(QuantArgs& a, int64_t bands, const DeviceInfo* info,
 }  // namespace
 
 size_t fp4_quantize_workspace_size(int64_t rows, int n, bool nv, int groups, bool ragged) {
-  if (!nv || rows * n <= kFp4SelfValues) return 0;
+  if (!nv || fp4_self_max(rows, n, groups, ragged)) return 0;
   const int64_t bands = fp4_bands(rows, groups, ragged);
   return static_cast<size_t>(bands * amax_splits(bands, n)) * sizeof(float);
 }
@@ -342,7 +353,7 @@ gptq_status fp4_quantize(const void* X, int x_bf16, int64_t x_rows, int n, int64
   a.scales = scales;
   a.deq = deq;
   a.splits = amax_splits(bands, n);
-  a.partial = nv && !given && rows * n > kFp4SelfValues ? static_cast<float*>(ws) : nullptr;
+  a.partial = nv && !given && !fp4_self_max(rows, n, groups, offsets != nullptr) ? static_cast<float*>(ws) : nullptr;
   if (nv)
     return x_bf16 ? launch_quantize<true, true>(a, bands, info, st) : launch_quantize<false, true>(a, bands, info, st);
   return x_bf16 ? launch_quantize<true, false>(a, bands, info, st) : launch_quantize<false, false>(a, bands, info, st);

@@ -120,7 +120,7 @@ def test_sizes():
     assert size(7, 64, NV, 2, 0) == 0 and size(7, 64, 2, 1, 0) == 0 and size(-1, 64, NV, 1, 0) == 0
     assert size(7, 64, NV, 513, 1) == 0 and size(7, 0, NV, 1, 0) == 0
     ws = LIB.gptq_fp4_quantize_workspace_size
-    assert ws(8192, 4096, MX, 1, 0) == 0 and ws(4, 4096, NV, 1, 0) == 0
+    assert ws(8192, 4096, MX, 1, 0) == 0 and ws(16, 4096, NV, 1, 0) == 0
     assert ws(8192, 4096, NV, 1, 0) == 64 * 16 * 4   # a maximum a band and chunk of 256 columns
     assert ws(8192, 4096, NV, 24, 1) > 0 and ws(8192, 4096, NV, 600, 1) == 0
     lin = LIB.gptq_fp4_linear_workspace_size
@@ -143,8 +143,8 @@ def _quantize(**kw):
     dict(offsets=P(256), groups=513), dict(offsets=P(258), groups=2), dict(given=2), dict(t=None), dict(t=P(258)),
     dict(format=MX), dict(format=MX, t=None, given=1), dict(X=None), dict(X=P(258)), dict(X=P(257), xdt=BF16),
     dict(packed=None), dict(packed=P(264)), dict(scales=None), dict(scales=P(264)), dict(deq=P(258)), dict(index=P(258)),
-    dict(rows=1024, x_rows=1024, ws=None), dict(rows=1024, x_rows=1024, ws=P(128 + 16)),
-    dict(rows=1024, x_rows=1024, ws_bytes=4)])
+    dict(rows=2048, x_rows=2048, ws=None), dict(rows=2048, x_rows=2048, ws=P(128 + 16)),
+    dict(rows=2048, x_rows=2048, ws_bytes=4)])
 def test_quantize_refuses(bad):
     assert _quantize(**bad) == 1
 
