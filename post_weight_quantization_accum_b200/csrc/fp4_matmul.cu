@@ -326,7 +326,7 @@ __device__ __forceinline__ float quantize_tile(const QuantArgs& a, const Tile& x
     }
     uint32_t codes[S::kLane / 8], byte;
     float s;
-    quantize_lane<BF16, NV>(w, p, u, codes, byte, s);
+    quantize_lane<BF16, NV>(w, p, left, u, codes, byte, s);
     if (in) {
       uint8_t* stage = dst + c / kAcross * kRawStageBytes;
       const int at = c % kAcross * (S::kLane / 2);  // byte of the row's 128
@@ -754,7 +754,8 @@ static_assert(kPairSfCol + kPairSfSets * kPairSfStride <= kTmemCols, "tensor mem
 // A warp's block of 32 features x 32 tokens, from tensor memory to y.  bf16:
 // read as matrix fragments, transposed by stmatrix into rows of 64 bytes (32
 // features of a token, 64-byte swizzle) and written by a TMA store; the end of
-// a group's rows, and a y that TMA cannot address, row by row.  fp32: a lane a
+// a group's rows or of W's (a TMA store is cut at 16 bytes, not at an element),
+// and a y that TMA cannot address, row by row.  fp32: a lane a
 // feature, each row of 32 lanes a line.
 template <typename OUT>
 struct Block;
@@ -791,7 +792,7 @@ struct Block<__nv_bfloat16> {
     const uint32_t swz = ((lane / 8) ^ (lane / 2 % 4)) * 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) stmatrix_x4_trans(at + 512 * i + swz, p[2 * i], p[2 * i + 1], p[8 + 2 * i], p[8 + 2 * i + 1]);
-    if (o.tma && tokens >= 32) {
+    if (o.tma && tokens >= 32 && features >= 32) {
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) {

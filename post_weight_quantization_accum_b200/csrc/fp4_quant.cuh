@@ -13,11 +13,11 @@ namespace gptq {
 
 // Up to here every CTA reads its group's values itself instead of waiting for
 // another kernel's maxima: 128 KB of bf16 take it about two microseconds, a
-// second launch and its maxima three.  Groups count by their mean size (if all
-// rows were in one, its CTAs would read it at L2's pace).
+// second launch and its maxima three.  Groups count by their mean size, and all
+// of them for no more than four times as much, in case one has all the rows.
 constexpr int64_t kFp4SelfValues = 65536;
 inline bool fp4_self_max(int64_t rows, int n, int groups, bool ragged) {
-  return ragged ? rows * n <= 32 * kFp4SelfValues && rows * n <= kFp4SelfValues / 2 * groups : rows / groups * n <= kFp4SelfValues;
+  return ragged ? rows * n <= 4 * kFp4SelfValues && rows * n <= kFp4SelfValues / 2 * groups : rows / groups * n <= kFp4SelfValues;
 }
 // Up to here the CTAs of a product quantise its tokens themselves, each all of
 // its part of K and, for the maximum, each all values.
@@ -297,10 +297,10 @@ __device__ __forceinline__ void mul2(float& a, float& b, float x, float y, float
 
 // A lane's part of a block: its codes, and the block's scale byte and s (NaN
 // for a block with a value that is not finite: it must not pass for a number,
-// and its codes are zero).  p: where the lane's values are in memory.  Called
-// by whole warps.
+// and its codes are zero).  p: where the lane's values are in memory, `left` of
+// them (the others are zero, and are not read).  Called by whole warps.
 template <bool BF16, bool NV>
-__device__ __forceinline__ void quantize_lane(const uint32_t (&w)[8], const char* p, const Unit& u,
+__device__ __forceinline__ void quantize_lane(const uint32_t (&w)[8], const char* p, int left, const Unit& u,
                                               uint32_t (&codes)[Fp4Lane<BF16, NV>::kLane / 8], uint32_t& byte, float& s) {
   using S = Fp4Lane<BF16, NV>;
   uint32_t m = lane_max<BF16>(w);
@@ -359,7 +359,7 @@ __device__ __forceinline__ void quantize_lane(const uint32_t (&w)[8], const char
   if (!u.plain) {
 #pragma unroll 1
     for (int i = 0; i < S::kLane; ++i) {
-      const uint32_t at = 4 * (i % 8), c = exact_code(p == nullptr ? 0.0f : memory_value<BF16>(p, i), s, u.t) << at;
+      const uint32_t at = 4 * (i % 8), c = exact_code(p == nullptr || i >= left ? 0.0f : memory_value<BF16>(p, i), s, u.t) << at;
       if (i < 8)
         codes[0] = (codes[0] & ~(15u << at)) | c;
       else

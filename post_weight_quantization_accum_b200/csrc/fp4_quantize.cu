@@ -190,7 +190,7 @@ __device__ __forceinline__ void quantize_rows(const QuantArgs& a, const Band& b,
     fetch(p[S::kAhead], w[S::kAhead]);
     uint32_t codes[S::kLane / 8], byte;
     float s;
-    quantize_lane<BF16, NV>(w[0], p[0], u, codes, byte, s);
+    quantize_lane<BF16, NV>(w[0], p[0], left, u, codes, byte, s);
     if (r < b.rows) {
       if (col / 2 < pitch) {
         if (BF16)

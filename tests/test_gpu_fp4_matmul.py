@@ -137,13 +137,34 @@ def test_rows_of_no_group_and_columns_past_the_rows_are_left_alone(fmt):
     np.testing.assert_array_equal(y[9:40].double().cpu().numpy(), xv[4:] @ wv[2 * rows:].T * k)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,pitch", [(70, 72), (70, 71), (264, 512), (300, 301)])
+def test_many_rows_stay_in_their_groups_and_columns(dtype, rows, pitch):
+    """The same of the kernel for many tokens, with outputs that TMA can
+    address and others."""
+    fmt, n, off = "mxfp4", 160, np.array([3, 400, 400, 817])
+    w, wv, wt = _matrix(3 * rows, n, fmt, 5, list(np.arange(4) * rows), True)
+    x, xv, xt = _matrix(814, n, fmt, 6, [0, 397, 397, 814], True)
+    packed = torch.zeros((830, x["packed"].shape[1]), dtype=torch.uint8, device="cuda")
+    packed[3:817] = x["packed"]
+    x = dict(x, packed=packed, rows=830)
+    wide = torch.full((830, pitch), 7.0, dtype=dtype, device="cuda")
+    y = gq.gptq_fp4_grouped_matmul(w, x, torch.tensor(off, dtype=torch.int32).cuda(), y=wide[:, :rows])
+    torch.cuda.synchronize()
+    assert (wide[:3] == 7).all() and (wide[817:] == 7).all() and (wide[:, rows:] == 7).all()
+    _check(y[3:400], xv[:397] @ wv[:rows].T, None, n, dtype, True)
+    _check(y[400:817], xv[397:] @ wv[2 * rows:].T, None, n, dtype, True)
+
+
 @pytest.mark.parametrize("off", [[0, 9, 5, 20], [0, 5, 21, 20], [-1, 5, 9, 20], [0, 5, 9, 21]])
-def test_bad_offsets_touch_nothing_and_are_reported(off):
+@pytest.mark.parametrize("times", [1, 30])
+def test_bad_offsets_touch_nothing_and_are_reported(off, times):
+    """Of the kernels for few tokens and for many."""
     w, _, _ = _matrix(3 * 32, 64, "mxfp4", 5, [0, 32, 64, 96])
-    x, _, _ = _matrix(20, 64, "mxfp4", 6, [0, 5, 9, 20])
+    x, _, _ = _matrix(20 * times, 64, "mxfp4", 6, [0, 5 * times, 9 * times, 20 * times])
     gq.gptq_get_device_status()
-    y = torch.full((20, 32), 7.0, device="cuda")
-    gq.gptq_fp4_grouped_matmul(w, x, torch.tensor(off, dtype=torch.int32).cuda(), y=y)
+    y = torch.full((20 * times, 32), 7.0, device="cuda")
+    gq.gptq_fp4_grouped_matmul(w, x, torch.tensor(off, dtype=torch.int32).cuda() * times, y=y)
     assert gq.gptq_get_device_status() == 1
     assert (y == 7).all()
 

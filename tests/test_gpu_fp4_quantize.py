@@ -74,6 +74,19 @@ def test_quantize_one_value_everywhere(fmt, value):
     _compare(gq.gptq_fp4_quantize(X.cuda(), fmt, want_deq=True), X, fmt)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [2.0 ** -120, 2.0 ** 118])
+@pytest.mark.parametrize("n", [1, 17, 33, 300])
+def test_tensor_scales_at_the_ends_of_the_range(dtype, scale, n):
+    """Values whose tensor scale, or 1 / (s t), is near the ends of fp32: the
+    decisions are then taken in 64 bits, at the rows' ends too."""
+    X = (_x(40, n, 3, "f32") * scale).to(DTYPES[dtype])
+    _compare(gq.gptq_fp4_quantize(X.cuda(), "nvfp4", want_deq=True), X, "nvfp4")
+    ts = torch.tensor([scale / 100])
+    _compare(gq.gptq_fp4_quantize(X.cuda(), "nvfp4", tensor_scale=ts.cuda(), want_deq=True), X, "nvfp4",
+             tensor_scale=ts.numpy())
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_values_that_are_not_finite_make_their_block_nan(fmt, dtype):
