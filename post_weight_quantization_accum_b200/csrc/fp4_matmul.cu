@@ -319,7 +319,7 @@ __device__ __forceinline__ float quantize_tile(const QuantArgs& a, const Tile& x
     const char* p = row < 0 || left <= 0 ? nullptr : X + (row * a.ldx + col) * kSize;
     uint32_t w[8];
     if (p != nullptr) {
-      load_lane<BF16, false>(p, left, a.align, w);
+      load_lane<BF16, false>(p, left, col, w);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = 0;

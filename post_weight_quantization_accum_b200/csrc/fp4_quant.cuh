@@ -40,7 +40,7 @@ struct QuantArgs {
   int splits;      // of a band's columns in `partial`
   int strips;      // a band's rows are quantised by that many CTAs: 1, or 4 of 32 rows
   int given;  // tensor_scale is read, not made
-  int align;  // bytes (32, 16 or 0) that every row of X starts on
+  int vec;  // every row of X starts on 32 bytes
   int* status;
 };
 
@@ -60,7 +60,7 @@ inline QuantArgs fp4_quant_args(const void* X, int x_bf16, int64_t x_rows, int n
   a.tensor_scale = tensor_scale;
   a.given = given;
   const uintptr_t at = reinterpret_cast<uintptr_t>(X) | static_cast<uintptr_t>(ldx * (x_bf16 ? 2 : 4));
-  a.align = at % 32 == 0 ? 32 : at % 16 == 0 ? 16 : 0;
+  a.vec = at % 32 == 0;
   a.status = status;
   return a;
 }
@@ -81,13 +81,19 @@ __device__ __forceinline__ void load32(const void* p, uint32_t* w) {
 }
 
 // A lane's values as raw words, zeros past the row's end: `left` columns are
-// there.  VEC: all of them, in a 32-byte load.
+// there, and `before` of the row's values stand before them.  VEC: all of
+// them, in a 32-byte load.  Else in the widest loads that the place of the row
+// allows (4-byte words shifted by 16 bits for bf16 on odd places), never
+// touching a byte outside the row.
 template <bool BF16, bool VEC>
-__device__ __forceinline__ void load_lane(const char* p, int left, int align, uint32_t (&w)[8]) {
+__device__ __forceinline__ void load_lane(const char* p, int left, int before, uint32_t (&w)[8]) {
   constexpr int kLane = BF16 ? 16 : 8;
   if (VEC) {
     load32(p, w);
-  } else if (left >= kLane && align >= 16) {
+    return;
+  }
+  const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+  if (left >= kLane && at % 16 == 0) {
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
       const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
@@ -95,6 +101,19 @@ __device__ __forceinline__ void load_lane(const char* p, int left, int align, ui
       w[i + 1] = v.y;
       w[i + 2] = v.z;
       w[i + 3] = v.w;
+    }
+  } else if (left >= kLane && at % 4 == 0) {
+    const uint32_t* f = reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = f[i];
+  } else if (BF16 && left > kLane && before > 0) {
+    const uint32_t* f = reinterpret_cast<const uint32_t*>(p - 2);
+    uint32_t lo = f[0];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t hi = f[i + 1];
+      w[i] = __funnelshift_r(lo, hi, 16);
+      lo = hi;
     }
   } else if (BF16) {
     const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
@@ -177,7 +196,7 @@ __device__ __forceinline__ uint32_t thread_max(const QuantArgs& a, int first, in
       int left = 0;
       const char* p = i < count ? at(i, left) : nullptr;
       if (p != nullptr) {
-        load_lane<BF16, VEC>(p, left, a.align, w[u]);
+        load_lane<BF16, VEC>(p, left, a.n - left, w[u]);
       } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[u][k] = 0;

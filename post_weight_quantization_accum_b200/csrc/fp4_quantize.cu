@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(QuantArgs a) {
       left = a.n - col;
       return row < 0 || left <= 0 ? nullptr : X + (row * a.ldx + col) * kSize;
     };
-    const uint32_t t = a.align == 32 && (c + 1) * kChunk <= a.n
+    const uint32_t t = a.vec && (c + 1) * kChunk <= a.n
                            ? thread_max<BF16, true, 4>(a, threadIdx.x / S::kAcross, S::kRowsAtOnce, b.rows, at)
                            : thread_max<BF16, false, 4>(a, threadIdx.x / S::kAcross, S::kRowsAtOnce, b.rows, at);
     m = max(m, t);
@@ -150,15 +150,25 @@ __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(QuantArgs a) {
   if (threadIdx.x == 0) a.partial[blockIdx.x] = __uint_as_float(m);
 }
 
-// A lane's values down the band's rows.
+// Whether the rows of the dequantised values start on 32 bytes.
+__device__ __forceinline__ bool wide_values(const QuantArgs& a) {
+  return a.n % 8 == 0 && reinterpret_cast<uintptr_t>(a.deq) % 32 == 0;
+}
+
+// A lane's values down the band's rows.  VEC: whole 32-byte loads, and 32-byte
+// stores of the values that they stand for.
 template <bool BF16, bool NV, bool VEC>
 __device__ __forceinline__ void quantize_rows(const QuantArgs& a, const Band& b, const Unit& u, const int* src, int col,
-                                              int64_t pitch, uint8_t* sc) {
+                                              int64_t pitch, uint8_t* sc, float* stage) {
   using S = Shape<BF16, NV>;
   constexpr int kSize = BF16 ? 2 : 4;
   const char* X = static_cast<const char*>(a.X);
-  const int left = a.n - col;
-  const bool wide = left >= S::kLane && a.n % 8 == 0 && reinterpret_cast<uintptr_t>(a.deq) % 32 == 0;
+  const int left = a.n - col, chunk0 = col - threadIdx.x % S::kAcross * S::kLane;
+  // values go out in 32-byte stores, or, where their rows do not start on 32
+  // bytes, through shared memory (512 floats a warp) as whole lines
+  const bool wide = VEC || wide_values(a);
+  constexpr int kRowsWarp = 32 / S::kAcross;  // rows of a warp
+  float* mine = stage + threadIdx.x / 32 * 512;
   const int cb = threadIdx.x % S::kAcross / S::kLanes;  // block of the chunk
   const bool first = threadIdx.x % S::kLanes == 0 && left > 0;  // the lane that writes the block's scale
   uint8_t* sc_col = sc + cb / 4 * kFp4TileBytes + cb % 4;
@@ -168,7 +178,7 @@ __device__ __forceinline__ void quantize_rows(const QuantArgs& a, const Band& b,
   };
   auto fetch = [&](const char* p, uint32_t (&w)[8]) {
     if (p != nullptr) {
-      load_lane<BF16, VEC>(p, left, a.align, w);
+      load_lane<BF16, VEC>(p, left, col, w);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = 0;
@@ -199,24 +209,36 @@ __device__ __forceinline__ void quantize_rows(const QuantArgs& a, const Band& b,
           *reinterpret_cast<uint32_t*>(dst) = codes[0];
       }
       if (first) sc_col[r % 32 * 16 + r / 32 * 4] = static_cast<uint8_t>(byte);
-      if (a.deq != nullptr && left > 0) {
+    }
+    if (a.deq != nullptr) {
 #pragma unroll
-        for (int i = 0; i < S::kLane / 8; ++i) {
-          float f[8];
-          from_e2m1(codes[i], f);
+      for (int i = 0; i < S::kLane / 8; ++i) {
+        float f[8];
+        from_e2m1(codes[i], f);
 #pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            mul2(f[j], f[j + 1], f[j], f[j + 1], s);
-            if (NV) mul2(f[j], f[j + 1], f[j], f[j + 1], u.t);
-          }
-          if (wide) {
-            store32(deq + 8 * i, f);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (8 * i + j < left) deq[8 * i + j] = f[j];
-          }
+        for (int j = 0; j < 8; j += 2) {
+          mul2(f[j], f[j + 1], f[j], f[j + 1], s);
+          if (NV) mul2(f[j], f[j + 1], f[j], f[j + 1], u.t);
         }
+        if (!wide) {
+          float4* m = reinterpret_cast<float4*>(mine + threadIdx.x % 32 * S::kLane + 8 * i);
+          m[0] = make_float4(f[0], f[1], f[2], f[3]);
+          m[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else if (r < b.rows && 8 * i < left) {
+          store32(deq + 8 * i, f);
+        }
+      }
+      if (!wide) {
+        __syncwarp();
+        const int lane = threadIdx.x % 32, row0 = r - threadIdx.x % 32 / S::kAcross;
+#pragma unroll
+        for (int q = 0; q < kRowsWarp; ++q) {
+          float* out = a.deq + (b.r0 + row0 + q) * a.n + chunk0 + lane;
+#pragma unroll
+          for (int i = 0; i < kChunk / 32; ++i)
+            if (row0 + q < b.rows && chunk0 + 32 * i + lane < a.n) out[32 * i] = mine[q * kChunk + 32 * i + lane];
+        }
+        __syncwarp();
       }
     }
     dst += S::kRowsAtOnce * pitch;
@@ -236,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) 
   __shared__ int tab[3][kFp4MaxGroups + 1];
   __shared__ uint32_t red[32];
   __shared__ int src[kFp4Band];
+  __shared__ __align__(16) float stage[kThreads * 16];
   __shared__ __align__(16) uint8_t sc[kFp4Band * (kChunk / S::kBlock)];
   const GroupTable t{tab[0], tab[1], tab[2]};
   pdl_wait();
@@ -293,10 +316,10 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) 
 
   const int col = chunk * kChunk + threadIdx.x % S::kAcross * S::kLane;
   const int64_t pitch = fp4_pitch(a.n);
-  if (a.align == 32 && (chunk + 1) * kChunk <= a.n)
-    quantize_rows<BF16, NV, true>(a, b, u, src, col, pitch, sc);
+  if (a.vec && (chunk + 1) * kChunk <= a.n && (a.deq == nullptr || wide_values(a)))
+    quantize_rows<BF16, NV, true>(a, b, u, src, col, pitch, sc, stage);
   else
-    quantize_rows<BF16, NV, false>(a, b, u, src, col, pitch, sc);
+    quantize_rows<BF16, NV, false>(a, b, u, src, col, pitch, sc, stage);
   __syncthreads();
   const int quads = fp4_quads(a.n, NV);
   constexpr int kQuads = kChunk / (4 * S::kBlock);  // scale tiles across the chunk
