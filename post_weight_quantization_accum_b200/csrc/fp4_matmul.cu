@@ -802,6 +802,7 @@ struct Block<__nv_bfloat16> {
     } else {
       __syncwarp();
       if (lane < features) {
+#pragma unroll 8
         for (int j = 0; j < min(tokens, 32); ++j) {
           const int chunk = (lane / 8) ^ (j / 2 % 4);
           y[j * o.ldy + lane] = *reinterpret_cast<const __nv_bfloat16*>(o.stg + 64 * j + 16 * chunk + 2 * (lane % 8));
@@ -826,7 +827,8 @@ struct Block<float> {
   }
 };
 
-template <bool NV, typename OUT>
+// WIDTH: tokens of a tile, 256 or 128.
+template <bool NV, typename OUT, int WIDTH>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                     const __grid_constant__ CUtensorMap xwide, const __grid_constant__ CUtensorMap wsmap,
@@ -880,7 +882,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = uniform(*tmem_slot);
   pdl_trigger();
   if (!a.early) pdl_wait();
-  const bool ok_groups = group_table<true>(t, a, kTokens);
+  const bool ok_groups = group_table<true>(t, a, WIDTH);
   if (a.early) pdl_wait();
   const int wtiles = static_cast<int>((a.rows + kPairRows - 1) / kPairRows);
   const int wbands = static_cast<int>((a.rows + kRows - 1) / kRows);
@@ -894,7 +896,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int mmas = (a.n + 63) / 64;
   const int kstages = (a.n + kStageK - 1) / kStageK;
 
-  auto tile_of = [&](uint32_t item) { return tile_at<true>(t, a, wtiles, kTokens, item); };
+  auto tile_of = [&](uint32_t item) { return tile_at<true>(t, a, wtiles, WIDTH, item); };
   // A single thread's wait.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, a.wait_ns, abort_flag, a.status);
@@ -1136,34 +1138,45 @@ gptq_status launch_stream(const CUtensorMap& wmap, const CUtensorMap& xmap, cons
              : GPTQ_ERR_CUDA;
 }
 
-template <bool NV, typename OUT>
-gptq_status launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const CUtensorMap& xwide,
+template <bool NV, typename OUT, int WIDTH>
+gptq_status launch_pair_of(const CUtensorMap& wmap, const CUtensorMap& xmap, const CUtensorMap& xwide,
                         const CUtensorMap& wsmap, const CUtensorMap& xsmap, const CUtensorMap& ymap, const MatmulArgs& a, const DeviceInfo* info,
                         cudaStream_t st) {
   static std::atomic<bool> attr_set[64] = {};  // per device, shared by host threads
   if (!attr_set[info->device]) {
-    if (cudaFuncSetAttribute(fp4_pair_kernel<NV, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(fp4_pair_kernel<NV, OUT, WIDTH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kPairSmemBytes + table_bytes(kFp4MaxGroups))) != cudaSuccess)
       return GPTQ_ERR_CUDA;
     attr_set[info->device] = true;
   }
   const bool ragged = a.offsets != nullptr;
   // token tiles: each group's last one may be part full
-  const int64_t tiles = ragged ? a.tokens / kTokens + std::min<int64_t>(a.groups, a.tokens) : ceil_div(a.tokens, kTokens);
+  const int64_t tiles = ragged ? a.tokens / WIDTH + std::min<int64_t>(a.groups, a.tokens) : ceil_div(a.tokens, WIDTH);
   const int64_t items = tiles * ceil_div(a.rows, kPairRows);
   if (items > INT32_MAX - 2 * info->sm_count) return GPTQ_ERR_UNSUPPORTED;
   const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(items, std::max(1, info->sm_count / 2)));
-  return launch_cluster_pdl(fp4_pair_kernel<NV, OUT>, grid, kPairThreads, kPairSmemBytes + table_bytes(a.groups), 2, st, wmap, xmap, xwide, wsmap,
+  return launch_cluster_pdl(fp4_pair_kernel<NV, OUT, WIDTH>, grid, kPairThreads, kPairSmemBytes + table_bytes(a.groups), 2, st, wmap, xmap, xwide, wsmap,
                             xsmap, ymap, a) == cudaSuccess
              ? launch_status()
              : GPTQ_ERR_CUDA;
 }
 
+// Tiles of 128 tokens where those of 256 would leave half of the pairs idle
+// (777 tokens, 1111 x 2000: 9.6 us instead of 12.0).
+template <bool NV, typename OUT>
+gptq_status launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const CUtensorMap& xwide,
+                        const CUtensorMap& wsmap, const CUtensorMap& xsmap, const CUtensorMap& ymap, const MatmulArgs& a,
+                        const DeviceInfo* info, cudaStream_t st) {
+  if (a.offsets == nullptr && ceil_div(a.tokens, kTokens) * ceil_div(a.rows, kPairRows) * 4 <= info->sm_count)
+    return launch_pair_of<NV, OUT, kTokens / 2>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st);
+  return launch_pair_of<NV, OUT, kTokens>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st);
+}
+
 // Whether the pair kernel takes it.  Both are timed on nvfp4 products, in us:
-//   tokens                 8     32    64    96    128   256
+//   rows x n, tokens       8     32    64    96    128   256
 //   4096 x 4096   stream   6.5   7.7   9.5   11.0  12.4  12.8
 //                 pair     9.7   9.4   9.6   9.8   10.0  10.6
-//   4096 x 11008  stream   8.8   9.6   12.2  14.0  15.4  18.8   (rows x columns)
+//   4096 x 11008  stream   8.8   9.6   12.2  14.0  15.4  18.8
 //                 pair     17.9  17.8  17.9  18.2  18.5  19.6
 // The stream kernel pays for tokens (sums to exchange), the pair kernel, which
 // does not cut K, for its depth.  Above 128 tokens it is the pair kernel, up to

@@ -57,9 +57,10 @@ def _vector(t, name, dtype, length, device):
     """An argument that is a contiguous vector (length None: any)."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or not t.is_contiguous() or (length is not None and t.shape[0] != length):
+    shape = t.shape
+    if len(shape) != 1 or not t.is_contiguous() or (length is not None and shape[0] != length):
         raise ValueError(f"{name} must be a contiguous vector{'' if length is None else f' of {length}'}, "
-                         f"got {tuple(t.shape)}")
+                         f"got {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
 
@@ -179,23 +180,26 @@ def fp4_check_matrix(q, name, ragged=False):
     except KeyError as e:
         raise ValueError(f"{name} is no quantised matrix: it lacks {e}") from None
     _check_format(format)
-    block = 4 * FP4_BLOCK[format]
     if not ragged and rows % groups != 0:
         raise ValueError(f"{name} has {rows} rows, which is no multiple of its {groups} groups")
     if p.dtype != torch.uint8 or s.dtype != torch.uint8:
         raise TypeError(f"{name}'s codes and scales must be uint8")
-    if p.shape != (rows, 16 * ((n + 31) // 32)) or not p.is_contiguous():
-        raise ValueError(f"{name}['packed'] must be contiguous of shape {(rows, 16 * ((n + 31) // 32))}, "
-                         f"got {tuple(p.shape)}")
-    bands, quads = _bands(rows, groups, ragged), (n + block - 1) // block
-    if s.dim() != 3 or s.shape[0] < bands or s.shape[1:] != (quads, 512) or not s.is_contiguous():
-        raise ValueError(f"{name}['scales'] must be contiguous of shape {(bands, quads, 512)}, got {tuple(s.shape)}")
+    pitch = 16 * ((n + 31) // 32)
+    if p.shape != (rows, pitch) or not p.is_contiguous():
+        raise ValueError(f"{name}['packed'] must be contiguous of shape {(rows, pitch)}, got {tuple(p.shape)}")
+    bands, block, shape = _bands(rows, groups, ragged), 4 * FP4_BLOCK[format], s.shape
+    if len(shape) != 3 or shape[0] < bands or shape != (shape[0], (n + block - 1) // block, 512) or not s.is_contiguous():
+        raise ValueError(f"{name}['scales'] must be contiguous of shape {(bands, (n + block - 1) // block, 512)}, "
+                         f"got {tuple(shape)}")
     device = p.device
     if s.device != device:
         raise ValueError(f"{name}'s tensors are on different devices")
-    if (t is not None) != (format == "nvfp4"):
-        raise ValueError(f"{name}: nvfp4 has tensor scales, mxfp4 none")
-    if t is not None:
+    if format == "mxfp4":
+        if t is not None:
+            raise ValueError(f"{name}: mxfp4 has no tensor scales")
+    elif t is None:
+        raise ValueError(f"{name}: nvfp4 has tensor scales")
+    else:
         _vector(t, "a matrix's tensor_scale", torch.float32, groups, device)
 
 
