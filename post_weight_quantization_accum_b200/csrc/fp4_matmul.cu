@@ -226,18 +226,23 @@ __device__ __forceinline__ Tile tile_at(const GroupTable& t, const MatmulArgs& a
 //
 // Bound by HBM: each weight is read once (128 * 4096 codes and their scales
 // are 288 KB of nvfp4).  With about a tile an SM or more, one CTA an SM walks
-// over the tiles with a ring of up to eight stages that never runs dry between two
-// of them, in clusters of two that share the last tile of an odd number.  A
-// layer with fewer tiles is
-// cut along K: a cluster takes a tile, each of its CTAs a part of K, two CTAs
-// an SM, and the CTAs then add up their sums in rank order, so the result does
-// not depend on timing: of a few tokens each CTA sends its sums to the one that
-// owns the token, as asynchronous stores that the owner's barrier counts; of
-// many the owner reads them from the others.
+// over the tiles with a ring of up to eight stages that never runs dry between
+// two of them, in clusters of two that share the last tile of an odd number
+// (64 tokens through 32 experts of 2048 x 4096, mxfp4: 30 us = 4.8 TB/s; from
+// the first load to the last product it is 6.7 TB/s, the rest is the group
+// table and the burst of first loads, 4 us, and the last tile's sums).  A
+// layer with fewer tiles is cut along K: a cluster takes a tile, each of its
+// CTAs a part of K, two CTAs an SM, and they then add up their sums in rank
+// order, so the result does not depend on timing: of a few tokens each CTA
+// sends its sums to the one that owns the token, as asynchronous stores that
+// the owner's barrier counts; of many the owner reads them from the others
+// (one token, 4096 x 4096: a CTA a tile 21 us, cut along K 6.5; the exchange
+// through two cluster barriers and remote loads took 1 us more).
 //
 // RAW: X is not quantised yet (gptq_fp4_linear of a few tokens).  The epilogue
 // warps then quantise the CTA's K range of its tokens into shared memory
-// while the first weights arrive, which costs less than a launch in between.
+// while the first weights arrive, which costs less than a launch in between
+// (one token, 4096 x 4096, nvfp4: 8.3 us in two launches, 7.4 in one).
 
 constexpr int kStreamThreads = 192;  // producer, MMA, 4 epilogue warps
 constexpr int kStreamMaxStages = 8;
@@ -734,6 +739,22 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 // ---------------------------------------------------------------------------
 // The kernel for many tokens: CTA pairs, 256 weight rows x up to 256 tokens
 // ---------------------------------------------------------------------------
+//
+// Bound by shared memory and the tensor cores: a stage of 256 columns brings
+// 38 KB to each CTA, which the products and scale copies read again, 76 KB at
+// 128 bytes a cycle = 608 cycles, while its four products of 256 x 256 x 64
+// take 4 x 131 and its twelve scale copies 10 each.  Measured 610 to 625
+// cycles a stage.  A tile of one CTA (128 x 256) would move 108 KB.  The
+// accumulators of two tiles overlap, as two of 256 columns and the scales do
+// not fit: the next tile's products wait until the epilogue has read the
+// overlap, about 850 cycles.  8192 tokens, 11008 x 4096, nvfp4, bf16 out: 148 us
+// = 5.0 PFLOP/s, 3.0 times the card's bf16 rate (170 us when it is kept at it:
+// the clock falls to 1.5 GHz under the power limit).  Steps on the way: one
+// CTA a tile 487 us; pairs and overlapped accumulators 390; loops run by whole
+// warps 242; whole stages issued without conditions 181 (a branch around each
+// instruction cost more than the instruction); single-thread roles and a
+// rolled epilogue 163; an arrival that does not wait for the epilogue's own
+// stores 158; the epilogue through stmatrix and TMA stores 148.
 
 constexpr int kPairRows = 256;
 constexpr int kPairStages = 5;
