@@ -23,8 +23,9 @@
 // runs backwards, still finds in L2; a small X is read twice by the one
 // kernel.  Measured with the values (B200): mxfp4 of fp32 11008 x 4096 63 us =
 // 6.1 TB/s, 0.93 of the copy rate; nvfp4 of bf16 8192 x 4096 50 us = 4.4 TB/s
-// on the bytes of one pass: 15 us of it the maxima, and the second pass issues
-// about 250 instructions for a warp's 512 values, which bound it.
+// on the bytes of one pass: 15 us of it the maxima, and the second pass
+// issues 200 instructions for a warp's 512 values (counted without writing
+// values), which bound it.
 #include <algorithm>
 
 #include "fp4_quant.cuh"
