@@ -302,7 +302,7 @@ __device__ __forceinline__ float quantize_tile(const QuantArgs& a, const Tile& x
       t = a.tensor_scale[x.g];
     } else {
       const int across = (a.n + S::kLane - 1) / S::kLane;
-      uint32_t m = thread_max<BF16, false, 4>(a, tid, 128, x.count * across, [&](int i, int& left) -> const char* {
+      uint32_t m = thread_max<BF16, 0, 4>(a, tid, 128, x.count * across, [&](int i, int& left) -> const char* {
         const int r = i / across, col = (i - r * across) * S::kLane, row = src[r];
         left = a.n - col;
         return row < 0 ? nullptr : X + (row * a.ldx + col) * kSize;
@@ -324,7 +324,7 @@ __device__ __forceinline__ float quantize_tile(const QuantArgs& a, const Tile& x
     const char* p = row < 0 || left <= 0 ? nullptr : X + (row * a.ldx + col) * kSize;
     uint32_t w[8];
     if (p != nullptr) {
-      load_lane<BF16, false>(p, left, col, w);
+      load_lane<BF16, 0>(p, left, col, w);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = 0;

@@ -40,7 +40,7 @@ struct QuantArgs {
   int splits;      // of a band's columns in `partial`
   int strips;      // a band's rows are quantised by that many CTAs: 1, or 4 of 32 rows
   int given;  // tensor_scale is read, not made
-  int vec;  // every row of X starts on 32 bytes
+  int vec;  // rows of X start on 32 bytes: 2, on 16: 1, else 0
   int* status;
 };
 
@@ -60,7 +60,7 @@ inline QuantArgs fp4_quant_args(const void* X, int x_bf16, int64_t x_rows, int n
   a.tensor_scale = tensor_scale;
   a.given = given;
   const uintptr_t at = reinterpret_cast<uintptr_t>(X) | static_cast<uintptr_t>(ldx * (x_bf16 ? 2 : 4));
-  a.vec = at % 32 == 0;
+  a.vec = at % 32 == 0 ? 2 : at % 16 == 0 ? 1 : 0;
   a.status = status;
   return a;
 }
@@ -82,18 +82,18 @@ __device__ __forceinline__ void load32(const void* p, uint32_t* w) {
 
 // A lane's values as raw words, zeros past the row's end: `left` columns are
 // there, and `before` of the row's values stand before them.  VEC: all of
-// them, in a 32-byte load.  Else in the widest loads that the place of the row
-// allows (4-byte words shifted by 16 bits for bf16 on odd places), never
-// touching a byte outside the row.
-template <bool BF16, bool VEC>
+// them, in a 32-byte load (2) or two of 16 (1).  Else in the widest loads that
+// the place of the row allows (4-byte words shifted by 16 bits for bf16 on odd
+// places), never touching a byte outside the row.
+template <bool BF16, int VEC>
 __device__ __forceinline__ void load_lane(const char* p, int left, int before, uint32_t (&w)[8]) {
   constexpr int kLane = BF16 ? 16 : 8;
-  if (VEC) {
+  if (VEC == 2) {
     load32(p, w);
     return;
   }
   const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
-  if (left >= kLane && at % 16 == 0) {
+  if (VEC == 1 || (left >= kLane && at % 16 == 0)) {
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
       const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
@@ -185,7 +185,7 @@ __device__ __forceinline__ int source_row(const QuantArgs& a, int64_t r) {
 
 // Largest finite magnitude of a thread's runs of values: kRows of them in flight, given
 // by at(i) as pointer (nullptr: none) and columns left.
-template <bool BF16, bool VEC, int kRows, typename At>
+template <bool BF16, int VEC, int kRows, typename At>
 __device__ __forceinline__ uint32_t thread_max(const QuantArgs& a, int first, int step, int count, At at) {
   uint32_t m = 0;
   for (int i0 = first; i0 < count; i0 += kRows * step) {

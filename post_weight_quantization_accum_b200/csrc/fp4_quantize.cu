@@ -22,7 +22,7 @@
 // of nvfp4 take a pass of their own over X, whose end the second pass, which
 // runs backwards, still finds in L2; a small X is read twice by the one
 // kernel.  Measured with the values (B200): mxfp4 of fp32 11008 x 4096 63 us =
-// 6.1 TB/s, 0.93 of the copy rate; nvfp4 of bf16 8192 x 4096 50 us = 4.4 TB/s
+// 6.1 TB/s, 0.93 of the copy rate; nvfp4 of bf16 8192 x 4096 49 us = 4.5 TB/s
 // on the bytes of one pass: 15 us of it the maxima, and the second pass
 // issues 200 instructions for a warp's 512 values (counted without writing
 // values), which bound it.
@@ -148,9 +148,10 @@ __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(QuantArgs a) {
       left = a.n - col;
       return row < 0 || left <= 0 ? nullptr : X + (row * a.ldx + col) * kSize;
     };
-    const uint32_t t = a.vec && (c + 1) * kChunk <= a.n
-                           ? thread_max<BF16, true, 4>(a, threadIdx.x / S::kAcross, S::kRowsAtOnce, b.rows, at)
-                           : thread_max<BF16, false, 4>(a, threadIdx.x / S::kAcross, S::kRowsAtOnce, b.rows, at);
+    const int r = threadIdx.x / S::kAcross, vec = (c + 1) * kChunk <= a.n ? a.vec : 0;
+    const uint32_t t = vec == 2   ? thread_max<BF16, 2, 4>(a, r, S::kRowsAtOnce, b.rows, at)
+                       : vec == 1 ? thread_max<BF16, 1, 4>(a, r, S::kRowsAtOnce, b.rows, at)
+                                  : thread_max<BF16, 0, 4>(a, r, S::kRowsAtOnce, b.rows, at);
     m = max(m, t);
   }
   m = cta_max(m, red);
@@ -162,9 +163,10 @@ __device__ __forceinline__ bool wide_values(const QuantArgs& a) {
   return a.n % 8 == 0 && reinterpret_cast<uintptr_t>(a.deq) % 32 == 0;
 }
 
-// A lane's values down the band's rows.  VEC: whole 32-byte loads, and 32-byte
-// stores of the values that they stand for.
-template <bool BF16, bool NV, bool VEC>
+// A lane's values down the band's rows.  VEC: whole loads (load_lane), and
+// 32-byte stores of the values that they stand for.  (Rows of 2056 bf16 start
+// on 16 bytes: 24.6 us with VEC 1, 25.4 with the loads that look at each place.)
+template <bool BF16, bool NV, int VEC>
 __device__ __forceinline__ void quantize_rows(const QuantArgs& a, const Band& b, const Unit& u, const int* src, int col,
                                               int64_t pitch, uint8_t* sc, float* stage) {
   using S = Shape<BF16, NV>;
@@ -173,7 +175,7 @@ __device__ __forceinline__ void quantize_rows(const QuantArgs& a, const Band& b,
   const int left = a.n - col, chunk0 = col - threadIdx.x % S::kAcross * S::kLane;
   // values go out in 32-byte stores, or, where their rows do not start on 32
   // bytes, through shared memory (512 floats a warp) as whole lines
-  const bool wide = VEC || wide_values(a);
+  const bool wide = VEC != 0 || wide_values(a);
   constexpr int kRowsWarp = 32 / S::kAcross;  // rows of a warp
   float* mine = stage + threadIdx.x / 32 * 512;
   const int cb = threadIdx.x % S::kAcross / S::kLanes;  // block of the chunk
@@ -268,23 +270,43 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) 
   __shared__ __align__(16) float stage[kThreads * 16];
   __shared__ __align__(16) uint8_t sc[kFp4Band * (kChunk / S::kBlock)];
   const GroupTable t{tab[0], tab[1], tab[2]};
-  pdl_wait();
-  pdl_trigger();  // (after the wait: what starts now may read all that was written before this kernel)
+  auto start = [] {
+    pdl_wait();
+    pdl_trigger();  // (after the wait: what starts now may read all that was written before this kernel)
+  };
+  // After a pass for the maxima, which let this kernel start when all before it
+  // was done, only the maxima are waited for (8192 x 4096: 51 -> 49 us; 6000
+  // gathered rows of 2056 in 24 groups: 26.1 -> 25.0).
+  const bool after = NV && a.partial != nullptr;
+  if (!after) start();
   if (a.offsets != nullptr && !build_groups(t, a.offsets, a.groups, a.rows, kFp4Band)) {
+    if (after) start();
     if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, GPTQ_ERR_INVALID_ARG);
     return;
   }
   const int chunks = (a.n + kChunk - 1) / kChunk;
   // (after a pass for the maxima: from its end, whose values are still in L2)
-  const unsigned at = NV && a.partial != nullptr ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  const unsigned at = after ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
   const int64_t band = at / chunks / a.strips;
   const int strip = at / chunks % a.strips, chunk = at % chunks;
   if (NV && !a.given && blockIdx.x == 0) {  // groups without rows have no CTA of their own
+    if (after) pdl_wait();
     for (int g = threadIdx.x; g < a.groups; g += kThreads)
       if (a.offsets != nullptr ? t.off[g] == t.off[g + 1] : a.group_rows == 0) a.tensor_scale[g] = FLT_MIN;
   }
   Band b;
-  if (!find_band(a, t, band, b)) return;
+  if (!find_band(a, t, band, b)) {
+    if (after) start();
+    return;
+  }
+  const int height = kFp4Band / a.strips;
+  b.r0 += strip * height;
+  b.rows = max(0, min(height, b.rows - strip * height));
+  if (b.rows < height || (chunk + 1) * kChunk > a.n) {  // bytes that have no row or block are zero
+    for (int i = threadIdx.x; i < int(sizeof(sc)) / 4; i += kThreads) reinterpret_cast<uint32_t*>(sc)[i] = 0;
+  }
+  band_rows(a, b.r0, b.rows, src);
+  if (after) start();
 
   Unit u{1.0f, 1.0f, 1.0f, true};
   if (NV) {
@@ -299,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) 
         m = cta_max(m, red);
       } else {
         const int across = (a.n + S::kLane - 1) / S::kLane;
-        m = thread_max<BF16, false, 4>(a, threadIdx.x, kThreads, static_cast<int>(b.g1 - b.g0) * across,
+        m = thread_max<BF16, 0, 4>(a, threadIdx.x, kThreads, static_cast<int>(b.g1 - b.g0) * across,
                                        [&](int i, int& left) -> const char* {
                                          const int row = source_row(a, b.g0 + i / across), col = i % across * S::kLane;
                                          left = a.n - col;
@@ -313,20 +335,16 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) 
     }
     u = unit_of(tensor);
   }
-  const int height = kFp4Band / a.strips;
-  b.r0 += strip * height;
-  b.rows = max(0, min(height, b.rows - strip * height));
-  if (b.rows < height || (chunk + 1) * kChunk > a.n) {  // bytes that have no row or block are zero
-    for (int i = threadIdx.x; i < int(sizeof(sc)) / 4; i += kThreads) reinterpret_cast<uint32_t*>(sc)[i] = 0;
-  }
-  band_rows(a, b.r0, b.rows, src);
 
   const int col = chunk * kChunk + threadIdx.x % S::kAcross * S::kLane;
   const int64_t pitch = fp4_pitch(a.n);
-  if (a.vec && (chunk + 1) * kChunk <= a.n && (a.deq == nullptr || wide_values(a)))
-    quantize_rows<BF16, NV, true>(a, b, u, src, col, pitch, sc, stage);
+  const int vec = (chunk + 1) * kChunk <= a.n && (a.deq == nullptr || wide_values(a)) ? a.vec : 0;
+  if (vec == 2)
+    quantize_rows<BF16, NV, 2>(a, b, u, src, col, pitch, sc, stage);
+  else if (vec == 1)
+    quantize_rows<BF16, NV, 1>(a, b, u, src, col, pitch, sc, stage);
   else
-    quantize_rows<BF16, NV, false>(a, b, u, src, col, pitch, sc, stage);
+    quantize_rows<BF16, NV, 0>(a, b, u, src, col, pitch, sc, stage);
   __syncthreads();
   const int quads = fp4_quads(a.n, NV);
   constexpr int kQuads = kChunk / (4 * S::kBlock);  // scale tiles across the chunk

@@ -157,6 +157,51 @@ def test_rows_with_a_pitch(fmt, pad):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype,pitch", [("f32", 516), ("bf16", 520)])
+@pytest.mark.parametrize("want_deq", [False, True])
+def test_rows_on_16_bytes(fmt, dtype, pitch, want_deq):
+    """Every other row starts between two 32-byte places; whole chunks of
+    columns and one that ends early, one matrix and groups with an empty one."""
+    X = _x(700, pitch, 12, dtype, "outliers")
+    for n in (512, 300):
+        _compare(gq.gptq_fp4_quantize(X.cuda()[:, :n], fmt, want_deq=want_deq), X[:, :n], fmt)
+        off = np.array([0, 130, 130, 700])
+        q = gq.gptq_fp4_quantize(X.cuda()[:, :n], fmt, offsets=torch.tensor(off, dtype=torch.int32).cuda(), want_deq=want_deq)
+        _compare(q, X[:, :n], fmt, off)
+
+
+def test_maxima_and_codes_of_calls_in_a_row():
+    """Calls that follow one another with one workspace, each other's inputs
+    being different, give what each gives alone."""
+    Xs = [(_x(700, 512, 20 + i, "bf16") * 10.0 ** i).to(torch.bfloat16).cuda() for i in range(3)]
+    alone = []
+    for X in Xs:
+        alone.append(gq.gptq_fp4_quantize(X, "nvfp4"))
+        torch.cuda.synchronize()
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    out = {k: torch.empty_like(alone[0][k]) for k in ("packed", "scales", "tensor_scale")}
+    seen = []
+    for _ in range(20):
+        for X in Xs:
+            q = gq.gptq_fp4_quantize(X, "nvfp4", out=out, ws=ws)
+            seen.append({k: q[k].clone() for k in out})
+    for i, q in enumerate(seen):
+        for k in out:
+            assert torch.equal(q[k], alone[i % 3][k]), (i, k)
+
+
+@pytest.mark.parametrize("counts_off", [[0, 400, 300, 700], [0, 100, 701], [-1, 700]])
+def test_bad_offsets_of_many_rows_touch_nothing(counts_off):
+    X = _x(700, 512, 5, "bf16").cuda()
+    out = {"packed": torch.full((700, 256), 0xA5, dtype=torch.uint8, device="cuda")}
+    q = gq.gptq_fp4_quantize(X, "nvfp4", offsets=torch.tensor(counts_off, dtype=torch.int32).cuda(), out=out)
+    torch.cuda.synchronize()
+    assert (q["packed"] == 0xA5).all()
+    assert gq.gptq_get_device_status() != 0
+    assert gq.gptq_get_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("counts", [[5], [0, 3, 0, 0, 130, 1, 0], [128, 128], [1] * 40, [300, 0, 257]])
 def test_ragged_groups(fmt, counts):
     rows, n = sum(counts), 272
