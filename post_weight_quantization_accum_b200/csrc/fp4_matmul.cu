@@ -45,7 +45,6 @@ struct MatmulArgs {
   int n;
   void* y;
   int64_t ldy;
-  int y_tma;  // y can be written by TMA (bf16, rows on 16 bytes)
   int early;  // the kernel before this one is the quantiser of X, which starts it
               // after its own wait: W and the offsets are there from the start
   int* status;
@@ -772,24 +771,52 @@ constexpr uint32_t kAccShift = 96;
 constexpr uint32_t kPairSfCol = kAccShift + kTokens, kPairSfStride = 48, kPairSfSets = 3;
 static_assert(kPairSfCol + kPairSfSets * kPairSfStride <= kTmemCols, "tensor memory");
 
-// A warp's block of 32 features x 32 tokens, from tensor memory to y.  bf16:
-// read as matrix fragments, transposed by stmatrix into rows of 64 bytes (32
-// features of a token, 64-byte swizzle) and written by a TMA store; the end of
-// a group's rows or of W's (a TMA store is cut at 16 bytes, not at an element),
-// and a y that TMA cannot address, row by row.  fp32: a lane a
-// feature, each row of 32 lanes a line.
-template <typename OUT>
-struct Block;
-
+// A warp's block of 32 features x 32 tokens, from tensor memory to y.  TMA
+// (bf16): read as matrix fragments, transposed by stmatrix into rows of 64
+// bytes (32 features of a token, 64-byte swizzle) and written by a TMA store;
+// the end of a group's rows or of W's (a TMA store is cut at 16 bytes, not at
+// an element) row by row.  Else: a lane a feature, row by row.
 struct Out {
   const CUtensorMap* map;
-  bool tma;
   uint8_t* stg;      // this warp's 2 KB
   int64_t ldy;
 };
 
+// store(row, j) for `last` rows, N at most; the pointer runs with them.  (The
+// epilogue is bound by its instructions: with an address made of j and a test
+// for each row, 28 of them to a row, 4614 tokens x 779 -> 3328 in fp32 took 35.7
+// us instead of 20.7.)
+template <int N, typename T, typename F>
+__device__ __forceinline__ void rows_of(T* row, int64_t step, int last, F store) {
+  if (last >= N) {
+#pragma unroll
+    for (int j = 0; j < N; ++j, row += step) store(row, j);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j, row += step) {
+      if (j >= last) break;
+      store(row, j);
+    }
+  }
+}
+
+template <typename OUT, bool TMA>
+struct Block {
+  static __device__ __forceinline__ void load(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld_32x32b_x32(taddr, v); }
+  static __device__ __forceinline__ void store(uint32_t (&v)[32], Scale k, const Out& o, OUT* y, int, int, int tokens,
+                                               int64_t features) {
+    const int lane = threadIdx.x & 31;
+    if (k.before != 1.0f) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * k.before);
+    }
+    if (lane < features)
+      rows_of<32>(y + lane, o.ldy, tokens, [&](OUT* q, int j) { store_out(q, __uint_as_float(v[j]) * k.k); });
+  }
+};
+
 template <>
-struct Block<__nv_bfloat16> {
+struct Block<__nv_bfloat16, true> {
   static __device__ __forceinline__ void load(uint32_t taddr, uint32_t (&v)[32]) {
     tmem_ld_16x256b_x4(taddr, v);
     tmem_ld_16x256b_x4(taddr + (16u << 16), v + 16);
@@ -813,7 +840,7 @@ struct Block<__nv_bfloat16> {
     const uint32_t swz = ((lane / 8) ^ (lane / 2 % 4)) * 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) stmatrix_x4_trans(at + 512 * i + swz, p[2 * i], p[2 * i + 1], p[8 + 2 * i], p[8 + 2 * i + 1]);
-    if (o.tma && tokens >= 32 && features >= 32) {
+    if (tokens >= 32 && features >= 32) {
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) {
@@ -823,10 +850,16 @@ struct Block<__nv_bfloat16> {
     } else {
       __syncwarp();
       if (lane < features) {
-#pragma unroll 8
-        for (int j = 0; j < min(tokens, 32); ++j) {
-          const int chunk = (lane / 8) ^ (j / 2 % 4);
-          y[j * o.ldy + lane] = *reinterpret_cast<const __nv_bfloat16*>(o.stg + 64 * j + 16 * chunk + 2 * (lane % 8));
+        const uint8_t* from = o.stg + 2 * (lane % 8);
+        __nv_bfloat16* row = y + lane;
+#pragma unroll 1
+        for (int left = min(tokens, 32); left > 0; left -= 8, from += 512) {
+          uint16_t u[8];  // (read before the first is written: the compiler cannot know that they are not the same)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] = *reinterpret_cast<const uint16_t*>(from + 16 * ((lane / 8) ^ (j / 2)) + 64 * j);
+#pragma unroll
+          for (int j = 0; j < 8; ++j, row += o.ldy)
+            if (j < left) *reinterpret_cast<uint16_t*>(row) = u[j];
         }
       }
       __syncwarp();
@@ -834,22 +867,8 @@ struct Block<__nv_bfloat16> {
   }
 };
 
-template <>
-struct Block<float> {
-  static __device__ __forceinline__ void load(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld_32x32b_x32(taddr, v); }
-  static __device__ __forceinline__ void store(uint32_t (&v)[32], Scale k, const Out& o, float* y, int, int, int tokens,
-                                               int64_t features) {
-    const int lane = threadIdx.x & 31;
-    if (lane < features) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < tokens) y[j * o.ldy + lane] = __uint_as_float(v[j]) * k.before * k.k;
-    }
-  }
-};
-
-// WIDTH: tokens of a tile, 256 or 128.
-template <bool NV, typename OUT, int WIDTH>
+// WIDTH: tokens of a tile, 256 or 128.  TMA: y is written by TMA.
+template <bool NV, typename OUT, int WIDTH, bool TMA>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                     const __grid_constant__ CUtensorMap xwide, const __grid_constant__ CUtensorMap wsmap,
@@ -1050,7 +1069,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // ---------------- epilogue (both CTAs) ----------------
     const int quad = warp & 3;            // the tensor-memory lanes of this warp
     const int turn = (warp - 2) >> 2;     // which of the two warps with these lanes
-    const Out o{&ymap, a.y_tma != 0, staging + (warp - 2) * kStageOutBytes, a.ldy};
+    const Out o{&ymap, staging + (warp - 2) * kStageOutBytes, a.ldy};
     uint32_t tiles = 0;
     for (uint32_t item = pair; item < items; item += pairs, ++tiles) {
       const Tile x = tile_of(item);
@@ -1064,9 +1083,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       // the first accumulator, [0, 160) of the second
       const int first = (tiles & 1u ? 0 : 3) + turn;
       uint32_t v0[32], v1[32], v2[32];
-      Block<OUT>::load(acc + first % 8 * 32, v0);
-      Block<OUT>::load(acc + (first + 2) % 8 * 32, v1);
-      Block<OUT>::load(acc + (first + 4) % 8 * 32, v2);
+      Block<OUT, TMA>::load(acc + first % 8 * 32, v0);
+      Block<OUT, TMA>::load(acc + (first + 2) % 8 * 32, v1);
+      Block<OUT, TMA>::load(acc + (first + 4) % 8 * 32, v2);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
@@ -1077,20 +1096,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int i = 0; i < 4; ++i) {  // (rolled: the code of one block stays in the instruction cache)
         const int c = (first + 2 * i) % 8 * 32;
         if (c < x.count && r0 < a.rows)
-          Block<OUT>::store(v0, k, o, out + c * a.ldy, x.token + c, static_cast<int>(r0), x.count - c, a.rows - r0);
+          Block<OUT, TMA>::store(v0, k, o, out + c * a.ldy, x.token + c, static_cast<int>(r0), x.count - c, a.rows - r0);
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           v0[j] = v1[j];
           v1[j] = v2[j];
         }
         if (i == 0) {
-          Block<OUT>::load(acc + (first + 6) % 8 * 32, v2);
+          Block<OUT, TMA>::load(acc + (first + 6) % 8 * 32, v2);
           tmem_ld_wait();
         }
       }
       tc_fence_before();
     }
-    if (lane == 0) bulk_wait();
+    if (TMA && lane == 0) bulk_wait();
   }
   tc_fence_before();
   __syncthreads();
@@ -1159,13 +1178,13 @@ gptq_status launch_stream(const CUtensorMap& wmap, const CUtensorMap& xmap, cons
              : GPTQ_ERR_CUDA;
 }
 
-template <bool NV, typename OUT, int WIDTH>
+template <bool NV, typename OUT, int WIDTH, bool TMA>
 gptq_status launch_pair_of(const CUtensorMap& wmap, const CUtensorMap& xmap, const CUtensorMap& xwide,
                         const CUtensorMap& wsmap, const CUtensorMap& xsmap, const CUtensorMap& ymap, const MatmulArgs& a, const DeviceInfo* info,
                         cudaStream_t st) {
   static std::atomic<bool> attr_set[64] = {};  // per device, shared by host threads
   if (!attr_set[info->device]) {
-    if (cudaFuncSetAttribute(fp4_pair_kernel<NV, OUT, WIDTH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(fp4_pair_kernel<NV, OUT, WIDTH, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kPairSmemBytes + table_bytes(kFp4MaxGroups))) != cudaSuccess)
       return GPTQ_ERR_CUDA;
     attr_set[info->device] = true;
@@ -1176,21 +1195,21 @@ gptq_status launch_pair_of(const CUtensorMap& wmap, const CUtensorMap& xmap, con
   const int64_t items = tiles * ceil_div(a.rows, kPairRows);
   if (items > INT32_MAX - 2 * info->sm_count) return GPTQ_ERR_UNSUPPORTED;
   const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(items, std::max(1, info->sm_count / 2)));
-  return launch_cluster_pdl(fp4_pair_kernel<NV, OUT, WIDTH>, grid, kPairThreads, kPairSmemBytes + table_bytes(a.groups), 2, st, wmap, xmap, xwide, wsmap,
+  return launch_cluster_pdl(fp4_pair_kernel<NV, OUT, WIDTH, TMA>, grid, kPairThreads, kPairSmemBytes + table_bytes(a.groups), 2, st, wmap, xmap, xwide, wsmap,
                             xsmap, ymap, a) == cudaSuccess
              ? launch_status()
              : GPTQ_ERR_CUDA;
 }
 
 // Tiles of 128 tokens where those of 256 would leave half of the pairs idle
-// (777 tokens, 1111 x 2000: 9.6 us instead of 12.0).
+// (777 tokens, 1111 x 2000: a fifth less).
 template <bool NV, typename OUT>
 gptq_status launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const CUtensorMap& xwide,
                         const CUtensorMap& wsmap, const CUtensorMap& xsmap, const CUtensorMap& ymap, const MatmulArgs& a,
                         const DeviceInfo* info, cudaStream_t st) {
   if (a.offsets == nullptr && ceil_div(a.tokens, kTokens) * ceil_div(a.rows, kPairRows) * 4 <= info->sm_count)
-    return launch_pair_of<NV, OUT, kTokens / 2>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st);
-  return launch_pair_of<NV, OUT, kTokens>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st);
+    return launch_pair_of<NV, OUT, kTokens / 2, false>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st);
+  return launch_pair_of<NV, OUT, kTokens, false>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st);
 }
 
 // Whether the pair kernel takes it.  Both are timed on nvfp4 products, in us:
@@ -1333,19 +1352,26 @@ gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const
   if (!scale_map(&wsmap, wscales, quads, fp4_bands(groups * rows, groups, false), nv, 1) ||
       !scale_map(&xsmap, xscales, quads, xbands, nv, 2))
     return GPTQ_ERR_CUDA;
-  CUtensorMap xwide, ymap = xmap;  // (ymap unused where y_tma is 0)
+  CUtensorMap xwide, ymap = xmap;  // (ymap unused without TMA)
   if (!make_tensor_map_2d(&xwide, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, pitch, tokens, pitch, kStageK / 2, kTokens / 2,
                           CU_TENSOR_MAP_SWIZZLE_128B))
     return GPTQ_ERR_CUDA;
-  a.y_tma = y_bf16 && reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy % 8 == 0;
-  if (a.y_tma && !make_tensor_map_2d(&ymap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, rows, tokens, ldy * 2, 32, 32,
-                                     CU_TENSOR_MAP_SWIZZLE_64B))
+  // Stores by TMA where pairs walk over many tiles of one matrix: they take less
+  // of shared memory's time from the products.  With a tile or less a pair, and
+  // with groups, whose tiles end early, a lane a feature is faster.  (nvfp4 8192
+  // x 4096 -> 11008: 150 us by TMA, 156 without; mxfp4 1555 x 2000 -> 4096 13.5
+  // and 14.0, -> 1112 9.0 and 8.3; 32 groups of 125 and 250 tokens x 2000 ->
+  // 2048 25.5 and 24.0, 34.2 and 32.2.)
+  const bool y_tma = y_bf16 && reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy % 8 == 0 && offsets == nullptr &&
+                     ceil_div(tokens, kTokens) * ceil_div(rows, kPairRows) * 2 > info->sm_count;
+  if (y_tma && !make_tensor_map_2d(&ymap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, rows, tokens, ldy * 2, 32, 32,
+                                   CU_TENSOR_MAP_SWIZZLE_64B))
     return GPTQ_ERR_CUDA;
-  if (nv)
-    return y_bf16 ? launch_pair<true, __nv_bfloat16>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st)
-                  : launch_pair<true, float>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st);
-  return y_bf16 ? launch_pair<false, __nv_bfloat16>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st)
-                : launch_pair<false, float>(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st);
+  auto run = [&](auto launch) { return launch(wmap, xmap, xwide, wsmap, xsmap, ymap, a, info, st); };
+  if (y_tma)
+    return nv ? run(launch_pair_of<true, __nv_bfloat16, kTokens, true>) : run(launch_pair_of<false, __nv_bfloat16, kTokens, true>);
+  if (y_bf16) return nv ? run(launch_pair<true, __nv_bfloat16>) : run(launch_pair<false, __nv_bfloat16>);
+  return nv ? run(launch_pair<true, float>) : run(launch_pair<false, float>);
 }
 
 }  // namespace gptq

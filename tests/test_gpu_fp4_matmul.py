@@ -156,6 +156,23 @@ def test_many_rows_stay_in_their_groups_and_columns(dtype, rows, pitch):
     _check(y[400:817], xv[397:] @ wv[2 * rows:].T, None, n, dtype, True)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tokens,n,rows,pitch", [(2100, 96, 2310, 2312), (2100, 96, 2304, 2304), (2305, 300, 2329, 2400),
+                                                 (2100, 96, 2310, 2311), (20000, 64, 33, 40), (20001, 64, 24, 24)])
+def test_many_tiles_of_one_matrix(fmt, dtype, tokens, n, rows, pitch):
+    """More tiles than pairs of CTAs, the last of them part full both ways;
+    rows of y that TMA can address and others, and what is beside them."""
+    w, wv, wt = _matrix(rows, n, fmt, 7, [0, rows], True)
+    x, xv, xt = _matrix(tokens, n, fmt, 8, [0, tokens], True)
+    wide = torch.full((tokens + 1, pitch), 7.0, dtype=dtype, device="cuda")
+    y = gq.gptq_fp4_matmul(w, x, y=wide[:tokens, :rows])
+    torch.cuda.synchronize()
+    assert (wide[tokens:] == 7).all() and (wide[:, rows:] == 7).all()
+    _check(y, xv @ wv.T * (float(wt[0]) * float(xt[0])), None, n, dtype, True)
+    assert gq.gptq_get_device_status() == 0
+
+
 @pytest.mark.parametrize("off", [[0, 9, 5, 20], [0, 5, 21, 20], [-1, 5, 9, 20], [0, 5, 9, 21]])
 @pytest.mark.parametrize("times", [1, 30])
 def test_bad_offsets_touch_nothing_and_are_reported(off, times):
