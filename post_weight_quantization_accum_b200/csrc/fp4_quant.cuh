@@ -215,6 +215,58 @@ __device__ __forceinline__ uint32_t thread_max(const QuantArgs& a, int first, in
   return m;
 }
 
+// Largest finite magnitude of runs of values on any place: at(r, lo, hi) sets
+// run r's bytes [lo, hi).  First its whole 16-byte pieces, kPieces at most a run
+// (0: `pieces`), 8 of a thread's in flight, then (ENDS) the values before and
+// behind them, a thread a run.
+template <bool BF16, int kPieces, typename At>
+__device__ __forceinline__ uint32_t runs_max(int first, int step, int runs, int pieces, bool ends, At at) {
+  constexpr int kFlight = 8;
+  const int each = kPieces ? kPieces : pieces, count = runs * each;
+  auto up = [](const char* p) { return p + (-reinterpret_cast<uintptr_t>(p) & 15); };
+  auto down = [](const char* p) { return p - (reinterpret_cast<uintptr_t>(p) & 15); };
+  uint32_t m = 0;
+  for (int i0 = first; i0 < count; i0 += kFlight * step) {
+    uint32_t w[kFlight][4];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int i = i0 + u * step, r = i / each;
+      const char *lo = nullptr, *hi = nullptr;
+      if (i < count) at(r, lo, hi);
+      const char* p = up(lo) + 16 * (i - r * each);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (p + 16 <= hi) v = *reinterpret_cast<const uint4*>(p);
+      w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
+    }
+    uint32_t b = 0;
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) b = max(b, lane_max<BF16>(w[u]));
+    if (b >= 0x7f800000u) {  // something not finite: leave it out
+      b = 0;
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) b = max(b, finite_max<BF16>(w[u]));
+    }
+    m = max(m, b);
+  }
+  if (!ends) return m;
+  constexpr int kSize = BF16 ? 2 : 4;
+  for (int r = first; r < runs; r += step) {
+    const char *lo = nullptr, *hi = nullptr;
+    at(r, lo, hi);
+    const char* head = up(lo) < hi ? up(lo) : hi;
+    const char* tail = down(hi) > head ? down(hi) : head;
+#pragma unroll
+    for (int k = 0; k < 16 / kSize - 1; ++k) {
+      float x = 0.0f, y = 0.0f;
+      if (lo + k * kSize < head) x = memory_value<BF16>(lo, k);
+      if (tail + k * kSize < hi) y = memory_value<BF16>(tail, k);
+      const uint32_t bx = __float_as_uint(fabsf(x)), by = __float_as_uint(fabsf(y));
+      m = max(m, max(bx < 0x7f800000u ? bx : 0u, by < 0x7f800000u ? by : 0u));
+    }
+  }
+  return m;
+}
+
 // Eight values to E2M1, the first in the low bits.
 __device__ __forceinline__ uint32_t to_e2m1(const float (&v)[8]) {
   uint32_t r;

@@ -120,8 +120,27 @@ __device__ __forceinline__ bool find_band(const QuantArgs& a, const GroupTable& 
   return true;
 }
 
+// A thread's part of the largest magnitude of chunk c of a band's rows on any
+// place: the whole 16-byte pieces of a row that start in the chunk, and the
+// row's two ends.  (Out of line: other calls do not fetch its code.)
+template <bool BF16>
+__device__ __noinline__ uint32_t chunk_max(const QuantArgs& a, const int* src, int rows, int c) {
+  constexpr int kSize = BF16 ? 2 : 4, kBytes = kChunk * kSize;
+  const char* X = static_cast<const char*>(a.X);
+  const int end = a.n * kSize;
+  const bool last = end <= (c + 1) * kBytes;
+  return runs_max<BF16, kBytes / 16>(threadIdx.x, kThreads, rows, 0, c == 0 || last, [&](int r, const char*& lo, const char*& hi) {
+    const int row = src[r];
+    if (row < 0) return;
+    const char* x = X + row * a.ldx * kSize;
+    const int shift = -reinterpret_cast<uintptr_t>(x) & 15, whole = end - ((end - shift) & 15);  // of the last piece's end
+    lo = x + (c == 0 ? 0 : min(c * kBytes + shift, whole));
+    hi = x + (last ? end : min((c + 1) * kBytes + shift, whole));
+  });
+}
+
 template <bool BF16, bool NV>
-__global__ void __launch_bounds__(kThreads) fp4_amax_kernel(QuantArgs a) {
+__global__ void __launch_bounds__(kThreads) fp4_amax_kernel(const __grid_constant__ QuantArgs a) {
   __shared__ int tab[3][kFp4MaxGroups + 1];
   __shared__ uint32_t red[32];
   __shared__ int src[kFp4Band];
@@ -142,16 +161,19 @@ __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(QuantArgs a) {
   constexpr int kSize = BF16 ? 2 : 4;
   uint32_t m = 0;
   for (int c = c0; c < c1; ++c) {
-    const int col = c * kChunk + threadIdx.x % S::kAcross * S::kLane;
-    auto at = [&](int r, int& left) -> const char* {
-      const int row = src[r];
-      left = a.n - col;
-      return row < 0 || left <= 0 ? nullptr : X + (row * a.ldx + col) * kSize;
-    };
-    const int r = threadIdx.x / S::kAcross, vec = (c + 1) * kChunk <= a.n ? a.vec : 0;
-    const uint32_t t = vec == 2   ? thread_max<BF16, 2, 4>(a, r, S::kRowsAtOnce, b.rows, at)
-                       : vec == 1 ? thread_max<BF16, 1, 4>(a, r, S::kRowsAtOnce, b.rows, at)
-                                  : thread_max<BF16, 0, 4>(a, r, S::kRowsAtOnce, b.rows, at);
+    uint32_t t;
+    if (a.vec == 0) {
+      t = chunk_max<BF16>(a, src, b.rows, c);
+    } else {
+      const int col = c * kChunk + threadIdx.x % S::kAcross * S::kLane, r = threadIdx.x / S::kAcross;
+      auto at = [&](int r, int& left) -> const char* {
+        const int row = src[r];
+        left = a.n - col;
+        return row < 0 || left <= 0 ? nullptr : X + (row * a.ldx + col) * kSize;
+      };
+      t = a.vec == 2 && (c + 1) * kChunk <= a.n ? thread_max<BF16, 2, 4>(a, r, S::kRowsAtOnce, b.rows, at)
+                                                : thread_max<BF16, 0, 4>(a, r, S::kRowsAtOnce, b.rows, at);
+    }
     m = max(m, t);
   }
   m = cta_max(m, red);
@@ -261,8 +283,32 @@ __device__ __forceinline__ void quantize_rows(const QuantArgs& a, const Band& b,
   }
 }
 
+// A thread's part of the largest magnitude of `count` rows from row g0 on.  (Out
+// of line: kernels that do not take it otherwise paid 1 to 2 us for its code.)
+template <bool BF16>
+__device__ __noinline__ uint32_t group_max(const QuantArgs& a, int64_t g0, int count) {
+  constexpr int kSize = BF16 ? 2 : 4;
+  const char* X = static_cast<const char*>(a.X);
+  const int bytes = a.n * kSize;
+  if (a.row_index == nullptr && a.ldx == a.n) {  // one run
+    const char* first = X + g0 * bytes;
+    const bool ends = (reinterpret_cast<uintptr_t>(first) | (count * bytes)) % 16 != 0;
+    return runs_max<BF16, 0>(threadIdx.x, kThreads, 1, count * bytes / 16, ends, [&](int, const char*& lo, const char*& hi) {
+      lo = first;
+      hi = lo + count * bytes;
+    });
+  }
+  return runs_max<BF16, 0>(threadIdx.x, kThreads, count, max(bytes / 16, 1), a.vec == 0 || bytes % 16 != 0,
+                           [&](int r, const char*& lo, const char*& hi) {
+                             const int row = source_row(a, g0 + r);
+                             if (row < 0) return;
+                             lo = X + row * a.ldx * kSize;
+                             hi = lo + bytes;
+                           });
+}
+
 template <bool BF16, bool NV>
-__global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const __grid_constant__ QuantArgs a) {
   using S = Shape<BF16, NV>;
   __shared__ int tab[3][kFp4MaxGroups + 1];
   __shared__ uint32_t red[32];
@@ -320,14 +366,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(QuantArgs a) 
         for (int64_t i = threadIdx.x; i < b.bands * a.splits; i += kThreads) m = max(m, __float_as_uint(p[i]));
         m = cta_max(m, red);
       } else {
-        const int across = (a.n + S::kLane - 1) / S::kLane;
-        m = thread_max<BF16, 0, 4>(a, threadIdx.x, kThreads, static_cast<int>(b.g1 - b.g0) * across,
-                                       [&](int i, int& left) -> const char* {
-                                         const int row = source_row(a, b.g0 + i / across), col = i % across * S::kLane;
-                                         left = a.n - col;
-                                         return row < 0 ? nullptr
-                                                        : static_cast<const char*>(a.X) + (row * a.ldx + col) * (BF16 ? 2 : 4);
-                                       });
+        m = group_max<BF16>(a, b.g0, static_cast<int>(b.g1 - b.g0));
         m = cta_max(m, red);
       }
       tensor = fmaxf(__fdiv_rn(__uint_as_float(m), 2688.0f), FLT_MIN);

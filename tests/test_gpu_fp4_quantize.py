@@ -170,6 +170,33 @@ def test_rows_on_16_bytes(fmt, dtype, pitch, want_deq):
         _compare(q, X[:, :n], fmt, off)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows", [20, 300])
+@pytest.mark.parametrize("n", [1, 5, 257, 513, 735, 1021])
+def test_the_maximum_is_found_anywhere(dtype, rows, n):
+    """One value larger than all others: in a first, last or middle column, of
+    rows on every place, dense, with a pitch and gathered; a larger one beside
+    the rows, infinities and NaN do not count."""
+    base = torch.ones(rows * (n + 3) + 16, dtype=dtype, device="cuda")
+    back = torch.arange(rows - 1, -1, -1, dtype=torch.int32, device="cuda")
+    places = sorted({c for c in (0, 1, 6, 7, 8, 254, 255, 256, 511, 512, n // 2, n - 2, n - 1) if 0 <= c < n})
+    want = torch.tensor([max(np.float32(5.0) / np.float32(2688.0), 2.0 ** -126)])
+    for off, pitch, index in ((0, n, None), (1, n, None), (3, n + 3, None), (5, n + 1, back), (0, n, back)):
+        base.fill_(4096.0)
+        X = base[off:off + rows * pitch].as_strided((rows, n), (pitch, 1))
+        X.fill_(1.0)
+        if n > 1:
+            X[rows // 2, n // 2] = float("inf")
+            X[0, n - 1] = float("nan")
+        for i, c in enumerate(places):
+            r = (7 * i) % rows
+            old = X[r, c].clone()
+            X[r, c] = -5.0
+            q = gq.gptq_fp4_quantize(X, "nvfp4", row_index=index)
+            assert torch.equal(q["tensor_scale"].cpu(), want), (off, pitch, index is not None, c)
+            X[r, c] = old
+
+
 def test_maxima_and_codes_of_calls_in_a_row():
     """Calls that follow one another with one workspace, each other's inputs
     being different, give what each gives alone."""
