@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "../../include/gptq.h"
+#include "pair_left.h"
 
 namespace gptq {
 
@@ -78,6 +79,11 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
+}
+
+// Counts `bytes` as arrived on the barrier, without a copy that brings them.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
 // One lane of a converged warp (the same one each time).
@@ -327,6 +333,45 @@ __device__ __forceinline__ void st_async(uint32_t addr, uint32_t bar, uint32_t r
       "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [a], %3, [b];\n\t}" ::"r"(addr),
       "r"(bar), "r"(rank), "r"(v)
       : "memory");
+}
+
+// The end of the two producers of a CTA pair, each of which has issued `issued`
+// uses of the ring (pair_left.h) with half_bytes(use) bytes from each: neither
+// CTA leaves while something is under way to its memory.  The odd one waits for
+// the products' last commit, `drain`, which arrives at both.  The even one waits
+// for all bytes that either loaded, as they count on its barriers `full`; uses
+// that, after a wait that ran out, one of the two alone issued (each gives up by
+// itself) are made whole first, when the products have ended.  odd_done is a
+// barrier of the even CTA for the 4 bytes of *odd_issued.  The roles' own waits
+// last `wait_ns` at most, a copy takes less than `copy_ns`.
+template <typename F>
+__device__ __forceinline__ void drain_pair(uint32_t rank, uint32_t issued, uint32_t stages, uint64_t* full, uint64_t* drain,
+                                           uint64_t* odd_done, volatile uint32_t* odd_issued, volatile int* abort_flag,
+                                           int* status, uint64_t wait_ns, uint64_t copy_ns, F half_bytes) {
+  const uint64_t role_ns = wait_ns + copy_ns < wait_ns ? ~uint64_t(0) : wait_ns + copy_ns;  // until another role has stopped
+  bool ok = true;
+  if (rank == 1) {
+    st_async(smem_u32(const_cast<uint32_t*>(odd_issued)), smem_u32(odd_done), 0, issued);
+    ok = mbar_wait(drain, 0u, role_ns);
+  } else {
+    ok = mbar_wait(odd_done, 0u, role_ns);
+    const PairLeft left = pair_left(issued, ok ? *odd_issued : issued, stages);
+    if (left.both < left.most) {
+      *abort_flag = 1;
+      ok = mbar_wait(drain, 0u, role_ns) && ok;
+    }
+    for (uint32_t u = left.first; u < left.most; ++u) {
+      uint64_t* bar = full + u % stages;
+      if (u >= left.both) {
+        if (left.most == issued)
+          mbar_complete_tx(bar, half_bytes(u));  // the odd CTA's half, which does not come
+        else
+          mbar_arrive_expect_tx(bar, half_bytes(u));
+      }
+      ok = mbar_wait(bar, u / stages & 1u, copy_ns) && ok;
+    }
+  }
+  if (!ok) set_status(status, GPTQ_ERR_TIMEOUT);
 }
 
 // Arrive on an mbarrier given by its cluster address (possibly the peer's).

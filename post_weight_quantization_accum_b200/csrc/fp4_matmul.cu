@@ -881,8 +881,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint64_t* acc_full = empty + kPairStages;  // one: a tile's products are complete
   uint64_t* acc_free = acc_full + 1;         // the overlap of a tile's accumulator has been read
   uint64_t* drain = acc_free + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* odd_done = drain + 1;            // of the even CTA: the odd one's producer has stopped, after *odd_issued stages
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(odd_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* odd_issued = tmem_slot + 2;
   int* table = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);
   const GroupTable t{table, table + a.groups + 1, table + 2 * (a.groups + 1)};
 
@@ -903,8 +905,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     mbar_init(acc_full, 1);
     mbar_init(acc_free, 2 * kPairEpiWarps);  // the epilogue warps of both CTAs
     mbar_init(drain, 1);
+    mbar_init(odd_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
+    if (rank == 0) mbar_arrive_expect_tx(odd_done, 4);
     prefetch_tensormap(&wmap);
     prefetch_tensormap(&xmap);
     prefetch_tensormap(&xwide);
@@ -945,15 +949,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (warp == 0) {
     if (elect_one()) {
       // ---------------- producer (both CTAs) ----------------
-      uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
+      uint32_t stage = 0, phase = 0, issued = 0;
       const uint32_t full0 = smem_cluster_addr(full, 0);  // the even CTA's barriers
+      // one box of 128 rows, or boxes of 32 where that loads no more
+      auto boxes_of = [](const Tile& x) { return x.cols / 2 > 96 ? 0 : (x.cols / 2 + kBoxRows - 1) / kBoxRows; };
+      // bytes of a stage in one CTA
+      auto half_bytes = [](int boxes) { return kABytes + (boxes == 0 ? kPairBBytes : boxes * kBoxBytes) + 3 * kStageSf; };
       bool ok = true;
       for (uint32_t item = pair; ok && item < items; item += pairs) {
         const Tile x = tile_of(item);
         const int half = x.cols / 2;  // tokens of this CTA
-        // one box of 128 rows, or boxes of 32 where that loads no more
-        const int boxes = half > 96 ? 0 : (half + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = 2 * (kABytes + (boxes == 0 ? kPairBBytes : boxes * kBoxBytes) + 3 * kStageSf);
+        const int boxes = boxes_of(x);
+        const uint32_t bytes = 2 * half_bytes(boxes);
         // the odd CTA's rows may not exist: it then loads the last band's scales for nothing
         const int wband = x.g * wbands + min(2 * x.wtile + static_cast<int>(rank), wbands - 1);
         const int xband = x.xband;
@@ -973,19 +980,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               tma_load_2d_pair(sa + kABytes + b * kBoxBytes, &xmap, bar, kb * (kStageK / 2), xy + b * kBoxRows);
           tma_load_3d_pair(sa + kABytes + kPairBBytes, &wsmap, bar, 0, kb * kStageQuads, wband);
           tma_load_3d_pair(sa + kABytes + kPairBBytes + kStageSf, &xsmap, bar, 0, kb * kStageQuads, xband);
-          issued |= 1u << stage;
-          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          ++issued;
           if (++stage == kPairStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      if (rank == 0) {  // every stage that was armed has received both CTAs' bytes
-        for (int s = 0; s < kPairStages; ++s)
-          if (issued & (1u << s))
-            if (!mbar_wait(full + s, (issued_parity >> s) & 1u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
-      }
+      drain_pair(rank, issued, kPairStages, full, drain, odd_done, odd_issued, abort_flag, a.status, a.wait_ns, kDrainNs,
+                 [&](uint32_t u) { return half_bytes(boxes_of(tile_of(pair + u / kstages * pairs))); });
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
@@ -1062,7 +1065,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (ok) mma_commit_pair(acc_full, 0x3);
       }
-      mma_commit_pair(drain, 0x1);
+      mma_commit_pair(drain, 0x3);  // (the odd CTA leaves after it too)
       if (!mbar_wait(drain, 0u, kDrainNs)) set_status(a.status, GPTQ_ERR_TIMEOUT);
     }
   } else {
