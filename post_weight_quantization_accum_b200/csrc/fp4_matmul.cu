@@ -867,6 +867,22 @@ struct Block<__nv_bfloat16, true> {
   }
 };
 
+// Boxes of 32 token rows that a CTA of a pair loads for a tile of `cols`
+// tokens: 0 stands for one box of 128 rows, where boxes of 32 load no less.
+__device__ __forceinline__ int pair_boxes(int cols) { return cols / 2 > 96 ? 0 : (cols / 2 + kBoxRows - 1) / kBoxRows; }
+// Bytes that a CTA of a pair loads a stage; `scales` of 128 rows.
+__device__ __forceinline__ uint32_t pair_bytes(int boxes, uint32_t scales) {
+  return kABytes + (boxes == 0 ? kPairBBytes : boxes * kBoxBytes) + 3 * scales;
+}
+// The same of an item's stages.  (Out of line: only the end of a run whose waits
+// ran out asks for it.)
+static __device__ __noinline__ uint32_t pair_item_bytes(const int* off, const int* tile, int groups, int wtiles, int width,
+                                                        uint32_t item, uint32_t scales) {
+  const int tt = static_cast<int>(item / wtiles), g = find_group(tile, groups, tt);
+  const int count = min(width, off[g + 1] - off[g] - (tt - tile[g]) * width);
+  return pair_bytes(pair_boxes((count + 15) / 16 * 16), scales);
+}
+
 // WIDTH: tokens of a tile, 256 or 128.  TMA: y is written by TMA.
 template <bool NV, typename OUT, int WIDTH, bool TMA>
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -951,16 +967,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       // ---------------- producer (both CTAs) ----------------
       uint32_t stage = 0, phase = 0, issued = 0;
       const uint32_t full0 = smem_cluster_addr(full, 0);  // the even CTA's barriers
-      // one box of 128 rows, or boxes of 32 where that loads no more
-      auto boxes_of = [](const Tile& x) { return x.cols / 2 > 96 ? 0 : (x.cols / 2 + kBoxRows - 1) / kBoxRows; };
-      // bytes of a stage in one CTA
-      auto half_bytes = [](int boxes) { return kABytes + (boxes == 0 ? kPairBBytes : boxes * kBoxBytes) + 3 * kStageSf; };
       bool ok = true;
       for (uint32_t item = pair; ok && item < items; item += pairs) {
         const Tile x = tile_of(item);
         const int half = x.cols / 2;  // tokens of this CTA
-        const int boxes = boxes_of(x);
-        const uint32_t bytes = 2 * half_bytes(boxes);
+        const int boxes = pair_boxes(x.cols);
+        const uint32_t bytes = 2 * pair_bytes(boxes, kStageSf);
         // the odd CTA's rows may not exist: it then loads the last band's scales for nothing
         const int wband = x.g * wbands + min(2 * x.wtile + static_cast<int>(rank), wbands - 1);
         const int xband = x.xband;
@@ -988,7 +1000,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
       }
       drain_pair(rank, issued, kPairStages, full, drain, odd_done, odd_issued, abort_flag, a.status, a.wait_ns, kDrainNs,
-                 [&](uint32_t u) { return half_bytes(boxes_of(tile_of(pair + u / kstages * pairs))); });
+                 [&](uint32_t u) {
+                   return pair_item_bytes(t.off, t.tile, a.groups, wtiles, WIDTH, pair + u / kstages * pairs, kStageSf);
+                 });
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
