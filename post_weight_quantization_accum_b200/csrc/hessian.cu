@@ -99,8 +99,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* odd_done = drain + 1;  // of the even CTA: the odd one's producer has stopped, after *odd_issued stages
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(odd_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* odd_issued = tmem_slot + 2;
 
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
@@ -118,8 +120,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(acc_empty + b, 8);  // four epilogue warps of each CTA
     }
     mbar_init(drain, 1);
+    mbar_init(odd_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
+    if (rank == 0) mbar_arrive_expect_tx(odd_done, 4);
     prefetch_tensormap(&xmap);
   }
   if (warp == 1) {
@@ -138,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- TMA producer (both CTAs) ----------------
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t issued = 0, issued_parity = 0;  // per-stage bits for the drain
+      uint32_t issued = 0;
       for (int u = pair; u < num_units && !*abort_flag; u += pairs) {
         int t, kb0, kb1, rb, cb;
         unit_range(p, u, t, kb0, kb1);
@@ -161,22 +165,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d_pair(a + kBoxBytes, &xmap, bar, fa + 64, y);
           tma_load_2d_pair(b, &xmap, bar, fb, y);
           tma_load_2d_pair(b + kBoxBytes, &xmap, bar, fb + 64, y);
-          issued |= 1u << stage;
-          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          ++issued;
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      // Drain (even CTA): every stage it armed has received both CTAs' bytes.
-      if (rank == 0) {
-        for (int s = 0; s < kStages; ++s) {
-          if (issued & (1u << s)) {
-            if (!mbar_wait(full + s, (issued_parity >> s) & 1u, kDrainNs)) set_status(p.status, GPTQ_ERR_TIMEOUT);
-          }
-        }
-      }
+      drain_pair(rank, issued, kStages, full, drain, odd_done, odd_issued, abort_flag, p.status, p.wait_ns, kDrainNs,
+                 [](uint32_t) { return static_cast<uint32_t>(kStageBytes); });
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
@@ -224,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit_pair(acc_full + buf, 0x3);
       }
       // Drain: all pair MMAs issued have completed (they read both CTAs' stages).
-      mma_commit_pair(drain, 0x1);
+      mma_commit_pair(drain, 0x3);  // (the odd CTA leaves after it too)
       if (!mbar_wait(drain, 0u, kDrainNs)) set_status(p.status, GPTQ_ERR_TIMEOUT);
     }
   } else {

@@ -39,3 +39,17 @@ def test_product_of_many_tokens(fmt, dtype, tokens, rows, n):
     assert _cut_short(lambda: gq.gptq_fp4_matmul(w, x, dtype=dtype)) > 0
     assert torch.equal(want, gq.gptq_fp4_matmul(w, x, dtype=dtype))
     assert gq.gptq_get_device_status() == 0
+
+
+@pytest.mark.parametrize("tokens,n", [(4096, 1024), (20000, 2048)])
+def test_hessian(tokens, n):
+    X = torch.randn((tokens, n), device="cuda", generator=torch.Generator("cuda").manual_seed(n)).to(torch.bfloat16)
+
+    def call():
+        return gq.gptq_hessian_accum(torch.zeros((n, n), device="cuda"), X, 2.0 / tokens)
+
+    want = call()
+    assert gq.gptq_get_device_status() == 0
+    assert _cut_short(call) > 0
+    assert torch.equal(want, call())
+    assert gq.gptq_get_device_status() == 0
