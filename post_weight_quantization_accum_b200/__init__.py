@@ -13,7 +13,8 @@ import ctypes
 
 import torch
 
-from ._lib import GPTQ_BF16, GPTQ_F32, LIB, GptqError, TraceEntry, check  # noqa: F401
+from ._lib import (GPTQ_BF16, GPTQ_F32, LIB, GptqError, TraceEntry, aligned_workspace, check,  # noqa: F401
+                   check_workspace)
 from .fp4 import (FP4_BLOCK, FP4_FORMATS, fp4_check_matrix, fp4_check_quantize_args, fp4_linear,  # noqa: F401
                   gptq_fp4_grouped_matmul, gptq_fp4_matmul, gptq_fp4_quantize)
 
@@ -69,9 +70,9 @@ def workspace(nbytes, device=None):
     return torch.empty(max(int(nbytes), 1) + 256, dtype=torch.uint8, device=device or "cuda")
 
 
-def _ws_ptr(ws):
-    base = ws.data_ptr()
-    return ctypes.c_void_p((base + 255) & ~255), ws.numel() - ((-base) % 256)
+def _ws_ptr(ws, device):
+    check_workspace(ws, device)
+    return aligned_workspace(ws)
 
 
 def gptq_get_device_status(stream=None):
@@ -118,7 +119,7 @@ def gptq_hessian_accum(H, X, alpha, hdiag=None, ws=None, stream=None):
     need = LIB.gptq_hessian_workspace_size(n, n_tok)
     if ws is None:
         ws = workspace(need, H.device)
-    wp, wbytes = _ws_ptr(ws)
+    wp, wbytes = _ws_ptr(ws, H.device)
     check("gptq_hessian_accum",
           LIB.gptq_hessian_accum(_ptr(H), _ptr(hdiag), _ptr(X), n_tok, n, ldx, ctypes.c_float(alpha), wp,
                                  wbytes, _stream(stream)))
@@ -134,7 +135,7 @@ def gptq_prepare_hinv(H, damp, act_order, hdiag=None, perm=None, dead=None, U=No
     dead = dead if dead is not None else torch.empty(n, dtype=torch.uint8, device=dev)
     if ws is None:
         ws = workspace(LIB.gptq_prepare_workspace_size(n), dev)
-    wp, wbytes = _ws_ptr(ws)
+    wp, wbytes = _ws_ptr(ws, dev)
     check("gptq_prepare_hinv",
           LIB.gptq_prepare_hinv(_ptr(H), _ptr(hdiag), n, ctypes.c_float(damp), int(bool(act_order)), _ptr(perm),
                                 _ptr(dead), _ptr(U), wp, wbytes, _stream(stream)))
@@ -158,7 +159,7 @@ def gptq_quantize_layer(W, U, bits, group, block=128, perm=None, dead=None, out=
         out.setdefault("row_loss", torch.empty(rows, dtype=torch.float32, device=dev))
     if ws is None:
         ws = workspace(LIB.gptq_quantize_workspace_size(rows, n, block), dev)
-    wp, wbytes = _ws_ptr(ws)
+    wp, wbytes = _ws_ptr(ws, dev)
     check("gptq_quantize_layer",
           LIB.gptq_quantize_layer(_ptr(W), _dtype_code(W), rows, n, _ptr(U), _ptr(perm), _ptr(dead), bits, group,
                                   block, _ptr(out["codes"]), _ptr(out["scales"]), _ptr(out["zeros"]),
@@ -202,7 +203,7 @@ def gptq_dequant_matvec(packed, scales, zeros, n, bits, group, x, g_idx=None, y=
     need = LIB.gptq_matvec_workspace_size(n, batch, xdt)
     wp, wb = ctypes.c_void_p(0), 0
     if need > 0:
-        wp, wb = _ws_ptr(ws if ws is not None else workspace(need, packed.device))
+        wp, wb = _ws_ptr(ws if ws is not None else workspace(need, packed.device), packed.device)
     x2 = x2.contiguous()
     check("gptq_dequant_matvec", LIB.gptq_dequant_matvec(_ptr(packed), _ptr(scales), _ptr(zeros), _ptr(g_idx), rows,
                                                          n, bits, group, _ptr(x2), xdt, batch, _ptr(y), wp, wb,
@@ -250,7 +251,7 @@ def gptq2d_round(W, UL, UR, scale=1.0, qmin=None, qmax=None, want_E=True, codes=
         E = torch.empty((m, n), dtype=torch.float32, device=dev)
     if ws is None:
         ws = workspace(LIB.gptq2d_workspace_size(m, n), dev)
-    wp, wbytes = _ws_ptr(ws)
+    wp, wbytes = _ws_ptr(ws, dev)
     check("gptq2d_round",
           LIB.gptq2d_round(_ptr(W), _dtype_code(W), m, n, _ptr(UL), _ptr(UR), ctypes.c_float(scale), clamp,
                            int(qmin or 0), int(qmax or 0), _ptr(codes), _ptr(E), wp, wbytes, _stream(stream)))

@@ -114,3 +114,19 @@ LIB = load()
 def check(func, code):
     if code != 0:
         raise GptqError(func, code)
+
+
+def check_workspace(ws, device):
+    """That ws (None: the call gets its own) is memory that a call on `device`
+    may write: its kernels take the address and the size of the whole tensor."""
+    if ws is not None and (ws.device != device or not ws.is_contiguous()):
+        raise ValueError(f"ws must be a contiguous tensor on {device}, got a"
+                         f"{'' if ws.is_contiguous() else ' strided'} tensor on {ws.device}")
+
+
+def aligned_workspace(ws):
+    """(pointer, bytes) of the 256-byte aligned part of a workspace tensor that
+    check_workspace has passed."""
+    p = ws.data_ptr()
+    a = (p + 255) & ~255
+    return a, max(0, ws.numel() * ws.element_size() - (a - p))

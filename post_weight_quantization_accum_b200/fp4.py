@@ -13,7 +13,7 @@ stream.
 """
 import torch
 
-from ._lib import GPTQ_BF16, GPTQ_F32, GPTQ_MXFP4, GPTQ_NVFP4, LIB, check
+from ._lib import GPTQ_BF16, GPTQ_F32, GPTQ_MXFP4, GPTQ_NVFP4, LIB, aligned_workspace, check, check_workspace
 
 FP4_FORMATS = {"mxfp4": GPTQ_MXFP4, "nvfp4": GPTQ_NVFP4}
 FP4_BLOCK = {"mxfp4": 32, "nvfp4": 16}
@@ -75,7 +75,7 @@ def _bands(rows, groups, ragged):
     return rows // 128 + groups if ragged else groups * ((rows // groups + 127) // 128)
 
 
-def fp4_check_quantize_args(X, format, tensor_scale=None, row_index=None, offsets=None):
+def fp4_check_quantize_args(X, format, tensor_scale=None, row_index=None, offsets=None, ws=None):
     """The checks gptq_fp4_quantize makes before it touches the device; they
     need no GPU.  Returns (rows, groups) of the result."""
     _check_format(format)
@@ -108,6 +108,7 @@ def fp4_check_quantize_args(X, format, tensor_scale=None, row_index=None, offset
     if tensor_scale is not None:
         _need(format == "nvfp4", "mxfp4 has no tensor scale")
         _vector(tensor_scale, "tensor_scale", torch.float32, groups, device)
+    check_workspace(ws, device)
     return rows, groups
 
 
@@ -118,13 +119,6 @@ def _output(X, out, name, shape, dtype):
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != X.device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {X.device}")
     return t
-
-
-def _aligned(ws):
-    """(pointer, bytes) of the 256-byte aligned part of a workspace tensor."""
-    p = ws.data_ptr()
-    a = (p + 255) & ~255
-    return a, max(0, ws.numel() * ws.element_size() - (a - p))
 
 
 def gptq_fp4_quantize(X, format="nvfp4", tensor_scale=None, row_index=None, offsets=None, want_deq=False, out=None,
@@ -138,7 +132,7 @@ def gptq_fp4_quantize(X, format="nvfp4", tensor_scale=None, row_index=None, offs
     of its own.  tensor_scale: use these (fp32 [groups], positive) instead of
     the rows' own maxima.  out: dict of outputs to write into.
     """
-    rows, groups = fp4_check_quantize_args(X, format, tensor_scale, row_index, offsets)
+    rows, groups = fp4_check_quantize_args(X, format, tensor_scale, row_index, offsets, ws)
     shape, ragged, code = X.shape, offsets is not None, FP4_FORMATS[format]
     n = shape[-1]
     block = 4 * FP4_BLOCK[format]
@@ -155,7 +149,7 @@ def gptq_fp4_quantize(X, format="nvfp4", tensor_scale=None, row_index=None, offs
             wbytes = LIB.gptq_fp4_quantize_workspace_size(rows, n, code, groups, ragged)
             if wbytes > 0:
                 keep = ws if ws is not None else X.new_empty(wbytes + 256, dtype=torch.uint8)
-                wp, wbytes = _aligned(keep)
+                wp, wbytes = aligned_workspace(keep)
         q = {"packed": packed, "scales": scales, "tensor_scale": t, "rows": rows, "n": n, "format": format,
              "groups": groups}
         if want_deq:
@@ -180,6 +174,8 @@ def fp4_check_matrix(q, name, ragged=False):
     except KeyError as e:
         raise ValueError(f"{name} is no quantised matrix: it lacks {e}") from None
     _check_format(format)
+    if groups < 1:
+        raise ValueError(f"{name} must have at least one group, got {groups}")
     if not ragged and rows % groups != 0:
         raise ValueError(f"{name} has {rows} rows, which is no multiple of its {groups} groups")
     if p.dtype != torch.uint8 or s.dtype != torch.uint8:
@@ -215,8 +211,16 @@ def _check_y(y, dtype, tokens, rows, device):
         raise ValueError(f"y must be {(tokens, rows)} with contiguous rows on {device}")
 
 
+def _check_experts(w, offsets):
+    _vector(offsets, "offsets", torch.int32, w["groups"] + 1, w["packed"].device)
+    if w["groups"] > MAX_GROUPS:
+        raise ValueError(f"at most {MAX_GROUPS} groups, w has {w['groups']}")
+
+
 def _product(w, x, offsets, dtype, y, stream):
     fp4_check_matrix(w, "w")
+    if offsets is not None:
+        _check_experts(w, offsets)
     fp4_check_matrix(x, "x", offsets is not None)
     for key in ("format", "n", "groups"):
         if w[key] != x[key]:
@@ -257,17 +261,12 @@ def gptq_fp4_matmul(w, x, dtype=torch.float32, y=None, stream=None):
     return _product(w, x, None, dtype, y, stream)
 
 
-def _check_experts(w, offsets):
-    _vector(offsets, "offsets", torch.int32, w["groups"] + 1, w["packed"].device)
-    if w["groups"] > MAX_GROUPS:
-        raise ValueError(f"at most {MAX_GROUPS} groups, w has {w['groups']}")
-
-
 def gptq_fp4_grouped_matmul(w, x, offsets, dtype=torch.float32, y=None, stream=None):
     """The product of each group of x's rows (offsets as x was quantised with)
     with its own matrix of the stack w ([groups, rows, n] quantised): y
     [x rows, rows].  Rows of y outside the offsets are left as they were."""
-    _check_experts(w, offsets)
+    if offsets is None:
+        raise ValueError("gptq_fp4_grouped_matmul needs the rows' offsets")
     return _product(w, x, offsets, dtype, y, stream)
 
 
@@ -281,7 +280,7 @@ def fp4_linear(w, X, dtype=None, tensor_scale=None, row_index=None, offsets=None
     wp, n, groups, format = w["packed"], w["n"], w["groups"], w["format"]
     if X.dim() != 2 or X.shape[1] != n:
         raise ValueError(f"X must be [tokens, {n}], got {tuple(X.shape)}")
-    tokens, x_groups = fp4_check_quantize_args(X, format, tensor_scale, row_index, offsets)
+    tokens, x_groups = fp4_check_quantize_args(X, format, tensor_scale, row_index, offsets, ws)
     if offsets is not None:
         _check_experts(w, offsets)
     if x_groups != groups:
@@ -299,7 +298,7 @@ def fp4_linear(w, X, dtype=None, tensor_scale=None, row_index=None, offsets=None
         nbytes, base = LIB.gptq_fp4_linear_workspace_size(tokens, rows, n, code, groups, offsets is not None), None
         if nbytes > 0:
             keep = ws if ws is not None else X.new_empty(nbytes + 256, dtype=torch.uint8)
-            base, nbytes = _aligned(keep)
+            base, nbytes = aligned_workspace(keep)
         wt = w["tensor_scale"]
         check("gptq_fp4_linear",
               LIB.gptq_fp4_linear(code, wp.data_ptr(), w["scales"].data_ptr(), None if wt is None else wt.data_ptr(),
