@@ -3,9 +3,12 @@
 A quantised matrix is a dict: ``packed`` uint8 [rows, 16 * ceil(n / 32)] (two
 E2M1 codes a byte), ``scales`` uint8 [bands, quads, 512] (scale tiles of 128
 rows x 4 blocks), ``tensor_scale`` fp32 [groups] ("nvfp4") or None ("mxfp4"),
-and the plain values ``rows``, ``n``, ``format``, ``groups``.  include/gptq.h
-defines the formats and layouts; the functions here check arguments, get
-outputs and workspaces from torch and call the library.
+``offsets`` (the int32 tensor that the rows' groups came from, not a copy of
+it, or None: one group, or groups of one size) and the plain values ``rows``,
+``n``, ``format``, ``groups``.  include/gptq.h defines the formats and layouts;
+the functions here check arguments, get outputs and workspaces from torch and
+call the library.  (A dict that a program lays out itself may leave ``offsets``
+out: how its rows are grouped is then not checked.)
 
 A call runs on ``stream`` or, without one, on the current stream of the
 tensors' device (which need not be the current device); outputs belong to that
@@ -151,7 +154,7 @@ def gptq_fp4_quantize(X, format="nvfp4", tensor_scale=None, row_index=None, offs
                 keep = ws if ws is not None else X.new_empty(wbytes + 256, dtype=torch.uint8)
                 wp, wbytes = aligned_workspace(keep)
         q = {"packed": packed, "scales": scales, "tensor_scale": t, "rows": rows, "n": n, "format": format,
-             "groups": groups}
+             "groups": groups, "offsets": offsets}
         if want_deq:
             q["deq"] = deq = _output(X, out, "deq", (rows, n), torch.float32)
         check("gptq_fp4_quantize",
@@ -199,6 +202,27 @@ def fp4_check_matrix(q, name, ragged=False):
         _vector(t, "a matrix's tensor_scale", torch.float32, groups, device)
 
 
+def _check_even(offsets, rows, groups, why, stream):
+    """That these offsets cut `rows` rows into `groups` groups of one size, in
+    which case the scales lie as without offsets.  Reads them (and so waits for
+    the stream): only where a matrix is used in another way than it was made."""
+    if offsets.is_cuda:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(offsets.device)):
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError(f"{why}, and these cannot be read during a capture")
+            at = offsets.tolist()
+    else:
+        at = offsets.tolist()
+    if at != [rows // groups * g for g in range(groups + 1)]:
+        raise ValueError(f"{why}, and these are not groups of one size from row 0 on")
+
+
+def _check_stack(q, name, stream):
+    """That q is one group of all its rows, or groups of one size."""
+    if q.get("offsets") is not None:
+        _check_even(q["offsets"], q["rows"], q["groups"], f"{name}'s rows were grouped by offsets", stream)
+
+
 def _check_y(y, dtype, tokens, rows, device):
     if y is None:
         if dtype not in _DTYPES:
@@ -230,6 +254,11 @@ def _product(w, x, offsets, dtype, y, stream):
         raise ValueError(f"w is on {wp.device}, x on {xp.device}")
     rows = w["rows"] // groups
     _check_y(y, dtype, tokens, rows, wp.device)
+    _check_stack(w, "w", stream)
+    if offsets is None:
+        _check_stack(x, "x", stream)
+    elif "offsets" in x and x["offsets"] is None:
+        _check_even(offsets, tokens, groups, "x was quantised without the product's offsets", stream)
 
     where, guard = _enter(wp.device, stream)
     try:
@@ -254,17 +283,22 @@ def _product(w, x, offsets, dtype, y, stream):
 
 def gptq_fp4_matmul(w, x, dtype=torch.float32, y=None, stream=None):
     """y[i, r] = sum_c W[r, c] X[i, c] of two quantised matrices (dicts of
-    gptq_fp4_quantize, same format and width): [x rows, w rows] in `dtype`
-    (fp32 or bf16), or written into y in its own."""
+    gptq_fp4_quantize, same format and width, one group of all rows each): [x
+    rows, w rows] in `dtype` (fp32 or bf16), or written into y in its own."""
     if w.get("groups") != 1:
         raise ValueError(f"w has {w.get('groups')} groups: gptq_fp4_grouped_matmul takes them")
     return _product(w, x, None, dtype, y, stream)
 
 
 def gptq_fp4_grouped_matmul(w, x, offsets, dtype=torch.float32, y=None, stream=None):
-    """The product of each group of x's rows (offsets as x was quantised with)
-    with its own matrix of the stack w ([groups, rows, n] quantised): y
-    [x rows, rows].  Rows of y outside the offsets are left as they were."""
+    """The product of each group of x's rows (the offsets that x was quantised
+    with) with its own matrix of the stack w ([groups, rows, n] quantised): y
+    [x rows, rows].  Rows of y outside the offsets are left as they were.
+
+    A matrix whose dict says that it was grouped otherwise (x without offsets,
+    w with some) is taken where the offsets make groups of one size, which are
+    read back for that: such a call waits for the stream, and is refused during
+    a capture."""
     if offsets is None:
         raise ValueError("gptq_fp4_grouped_matmul needs the rows' offsets")
     return _product(w, x, offsets, dtype, y, stream)
@@ -291,6 +325,7 @@ def fp4_linear(w, X, dtype=None, tensor_scale=None, row_index=None, offsets=None
     if dtype is None:
         dtype = X.dtype
     _check_y(y, dtype, tokens, rows, wp.device)
+    _check_stack(w, "w", stream)
     code = FP4_FORMATS[format]
     where, guard = _enter(wp.device, stream)
     try:
