@@ -15,12 +15,9 @@
 #pragma once
 
 #include "common.cuh"
+#include "fp4_shape.h"
 
 namespace gptq {
-
-constexpr int kFp4Band = 128;        // rows of a scale tile
-constexpr int kFp4TileBytes = 512;   // 128 rows x 4 blocks
-constexpr int kFp4MaxGroups = 512;   // groups of an offsets array
 
 inline __host__ __device__ int fp4_block(bool nv) { return nv ? 16 : 32; }
 inline __host__ __device__ int64_t fp4_pitch(int n) { return int64_t(16) * ((n + 31) / 32); }

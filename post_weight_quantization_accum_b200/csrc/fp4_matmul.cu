@@ -24,13 +24,7 @@
 namespace gptq {
 namespace {
 
-constexpr int kRows = 128;    // weight rows of a CTA's tile
 constexpr int kTokens = 256;  // tokens of a pair's tile at most
-constexpr int kStageK = 256;  // columns of K a stage (128 bytes)
-constexpr int kBoxRows = 32;  // token rows a TMA box
-constexpr int kBoxBytes = kBoxRows * kStageK / 2;
-constexpr int kABytes = kRows * kStageK / 2;
-constexpr int kSfBytes = kStageK / 64 * kFp4TileBytes;  // scales of 128 rows of a stage (nvfp4; half of it with mxfp4)
 constexpr uint64_t kDrainNs = 2000000000ull;
 
 struct MatmulArgs {
@@ -244,41 +238,6 @@ __device__ __forceinline__ Tile tile_at(const GroupTable& t, const MatmulArgs& a
 // (one token, 4096 x 4096, nvfp4: 8.3 us in two launches, 7.4 in one).
 
 constexpr int kStreamThreads = 192;  // producer, MMA, 4 epilogue warps
-constexpr int kStreamMaxStages = 8;
-constexpr int kStreamBarBytes = 384;
-constexpr int kPushTokens = 16;      // up to here sums are sent (an MMA's least columns)
-constexpr int kRawTokens = 16;       // of a RAW tile: one MMA's least columns
-constexpr int kRawMaxStages = 8;     // of a RAW CTA's K range
-constexpr int kRawStageBytes = kRawTokens * kStageK / 2 + kSfBytes;
-
-struct StreamShape {
-  int width;   // tokens of a tile: 16, 32, 64 or 128
-  int stages;
-  int splits;  // CTAs of a cluster
-  int accs;    // accumulators: 2 where a CTA walks over tiles
-  int raw_stages;  // RAW: most stages of a CTA's K range
-};
-__host__ __device__ inline int stream_stage_bytes(int width, bool raw) {
-  return kABytes + (raw ? 0 : (width < kBoxRows ? kBoxRows : width) * (kStageK / 2) + kSfBytes) + kSfBytes;
-}
-__host__ __device__ inline int table_bytes(int groups) { return 3 * (groups + 1) * 4; }
-// Shared memory in which a CTA of a split collects sums: for each of the
-// `splits` sources the same number of rows of 128 floats (so up to splits - 1
-// rows more than the tokens).  Up to 32 tokens it stands apart; more use the
-// operand ring again, which is larger than 128 rows.
-__host__ __device__ inline int stream_apart_bytes(int width, int splits) {
-  const int bytes = splits * ((width + splits - 1) / splits) * kRows * 4;
-  return splits > 1 && width <= 32 ? (bytes + 1023) / 1024 * 1024 : 0;  // (an operand may follow)
-}
-// Tensor memory of a CTA: accumulators and 32 scale columns a stage (at most
-// 2 * 128 + 32 * 8).
-__host__ __device__ inline uint32_t stream_tmem_cols(int width, int accs, int stages) {
-  const int need = accs * width + 32 * stages;
-  return need > 256 ? 512 : need > 128 ? 256 : 128;
-}
-constexpr size_t kStreamMaxSmem = 226 * 1024;
-// A walking CTA has the SM to itself: what its ring may take.
-constexpr int kWalkRingBytes = 200 * 1024;
 
 // The epilogue warps' part of a RAW tile: x.count tokens, stages [k0, k1) of K,
 // as B operand rows (128-byte swizzle) and scale tiles, stage by stage at
@@ -1138,37 +1097,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
 }
 
-// How few tokens are laid out.  Tiles are as wide as the tokens; groups, whose
-// sizes the host does not know, take 64 or 128 (a group's second tile of 64
-// starts at the third scale column of its band; a narrower one would start
-// inside a column).  Clusters are chosen for the stages of K that the busiest
-// SM works off: two CTAs that walk over whole tiles and share an odd last one,
-// or k CTAs a tile.  (One token, n = 4096: 32 row tiles take 4 CTAs each; 48
-// tokens, 86 row tiles: 3 each, 12 stages instead of 16.)
-StreamShape stream_shape(int64_t tokens, int groups, bool ragged, int64_t rows, int n, int sms) {
-  StreamShape s;
-  const int64_t each = ragged ? std::max<int64_t>(64, 2 * ceil_div(tokens, groups)) : tokens;
-  s.width = each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : 128;
-  s.raw_stages = 0;
-  const int kstages = static_cast<int>(ceil_div(n, kStageK));
-  const int64_t tiles = (ragged ? std::min<int64_t>(groups, tokens) : ceil_div(tokens, s.width)) * ceil_div(rows, kRows);
-  const int64_t share = ceil_div(tiles, std::max(1, sms / 2));  // tiles of a walking pair
-  int64_t best = kstages >= 2 ? share / 2 * kstages + share % 2 * ((kstages + 1) / 2) : ceil_div(tiles, sms);
-  s.splits = 0;
-  for (int k = 2; k <= 8 && k <= kstages && tiles * k <= 2 * sms; ++k) {  // (more would not run side by side)
-    const int64_t cost = ceil_div(tiles * k, sms) * ceil_div(kstages, k);
-    if (cost < best || (cost == best && s.splits == 0)) {
-      best = cost;
-      s.splits = k;
-    }
-  }
-  s.accs = s.splits == 0 ? 2 : 1;
-  s.stages = s.accs == 2 ? std::min(kStreamMaxStages, kWalkRingBytes / stream_stage_bytes(s.width, false))
-                         : s.width <= 16 ? 4 : 3;  // (two CTAs an SM, with 32 rows of sums apart)
-  if (s.splits == 0) s.splits = kstages >= 2 ? 2 : 1;
-  return s;
-}
-
 template <bool NV, typename OUT, int RAW, bool WALK>
 gptq_status launch_stream(const CUtensorMap& wmap, const CUtensorMap& xmap, const MatmulArgs& a, const StreamShape& s,
                           const QuantArgs& q, const DeviceInfo* info, cudaStream_t st) {
@@ -1179,16 +1107,11 @@ gptq_status launch_stream(const CUtensorMap& wmap, const CUtensorMap& xmap, cons
       return GPTQ_ERR_CUDA;
     attr_set[info->device] = true;
   }
-  // token tiles: each group's last one may be part full
-  const int64_t tiles =
-      a.offsets != nullptr ? a.tokens / s.width + std::min<int64_t>(a.groups, a.tokens) : ceil_div(a.tokens, s.width);
-  const int64_t items = tiles * ceil_div(a.rows, kRows);
+  const int64_t items = stream_tiles(s, a.tokens, a.groups, a.offsets != nullptr, a.rows);
   if (items * s.splits > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
   // clusters walk over the items, or have one each
   const int64_t ctas = s.splits * (s.accs == 2 ? std::min<int64_t>(items, std::max(1, info->sm_count / s.splits)) : items);
-  const size_t smem = 1024 + static_cast<size_t>(s.stages) * stream_stage_bytes(s.width, RAW != 0) +
-                      stream_apart_bytes(s.width, s.splits) + (RAW ? s.raw_stages * kRawStageBytes : 0) + kStreamBarBytes +
-                      table_bytes(a.groups);
+  const size_t smem = stream_smem(s, RAW != 0, a.groups);
   return launch_cluster_pdl(fp4_stream_kernel<NV, OUT, RAW, WALK>, static_cast<unsigned>(ctas), kStreamThreads, smem, s.splits,
                             st, wmap, xmap, a, s, q) == cudaSuccess
              ? launch_status()
@@ -1286,23 +1209,10 @@ static bool weight_map(CUtensorMap* map, const uint8_t* wq, int groups, int64_t 
                             kStageK / 2, kRows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// How the product quantises X itself, or false where X is quantised first: a
-// few tokens whose values every CTA may read, and a K range that its shared
-// memory holds.
-static bool raw_shape(int64_t tokens, int groups, bool ragged, int64_t rows, int n, const DeviceInfo* info, StreamShape* s) {
-  if (tokens > kRawTokens || tokens * n > kFp4RawValues) return false;
-  *s = stream_shape(tokens, groups, ragged, rows, n, info->sm_count);  // (the splits, and so the sums, of the two calls)
-  if (s->accs == 2) return false;  // (it walks)
-  s->width = kRawTokens;
-  s->stages = 4;
-  s->raw_stages = static_cast<int>(ceil_div(ceil_div(n, kStageK), s->splits));
-  return s->raw_stages <= kRawMaxStages;
-}
-
 bool fp4_linear_raw(int64_t tokens, int groups, bool ragged, int64_t rows, int n) {
   const DeviceInfo* info = device_info();
   StreamShape s;
-  return info != nullptr && raw_shape(tokens, groups, ragged, rows, n, info, &s);
+  return info != nullptr && raw_shape(tokens, groups, ragged, rows, n, info->sm_count, &s);
 }
 
 // The product of a few tokens that it quantises itself (fp4_linear_raw).
@@ -1313,7 +1223,7 @@ gptq_status fp4_raw_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, c
   const DeviceInfo* info = device_info();
   StreamShape s;
   CUtensorMap wmap;
-  if (info == nullptr || !raw_shape(tokens, groups, offsets != nullptr, rows, n, info, &s) ||
+  if (info == nullptr || !raw_shape(tokens, groups, offsets != nullptr, rows, n, info->sm_count, &s) ||
       !weight_map(&wmap, wq, groups, rows, n))
     return GPTQ_ERR_CUDA;
   const MatmulArgs a = product_args(wscales, wt, groups, rows, n, tokens, offsets, y, ldy, info);

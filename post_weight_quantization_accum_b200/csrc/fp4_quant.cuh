@@ -19,9 +19,6 @@ constexpr int64_t kFp4SelfValues = 65536;
 inline bool fp4_self_max(int64_t rows, int n, int groups, bool ragged) {
   return ragged ? rows * n <= 4 * kFp4SelfValues && rows * n <= kFp4SelfValues / 2 * groups : rows / groups * n <= kFp4SelfValues;
 }
-// Up to here the CTAs of a product quantise its tokens themselves, each all of
-// its part of K and, for the maximum, each all values.
-constexpr int64_t kFp4RawValues = 16384;
 
 struct QuantArgs {
   const void* X;
