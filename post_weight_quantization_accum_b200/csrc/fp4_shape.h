@@ -81,15 +81,16 @@ inline int64_t stream_tiles(const StreamShape& s, int64_t tokens, int groups, bo
 }
 
 // How few tokens are laid out.  Tiles are as wide as the tokens; groups, whose
-// sizes the host does not know, take 64 or 128 (a group's second tile of 64
-// starts at the third scale column of its band; a narrower one would start
-// inside a column).  Clusters are chosen for the stages of K that the busiest
-// SM works off: two CTAs that walk over whole tiles and share an odd last one,
-// or k CTAs a tile.  (One token, n = 4096: 32 row tiles take 4 CTAs each; 48
-// tokens, 86 row tiles: 3 each, 12 stages instead of 16.)
+// sizes the host does not know, take 64: they come here up to 32 tokens each on
+// average, twice that fills a tile, and a group's second tile then starts at the
+// third scale column of its band (a narrower one would start inside a column).
+// Clusters are chosen for the stages of K that the busiest SM works off: two
+// CTAs that walk over whole tiles and share an odd last one, or k CTAs a tile.
+// (One token, n = 4096: 32 row tiles take 4 CTAs each; 48 tokens, 86 row tiles:
+// 3 each, 12 stages instead of 16.)
 inline StreamShape stream_shape(int64_t tokens, int groups, bool ragged, int64_t rows, int n, int sms) {
   StreamShape s;
-  const int64_t each = ragged ? std::max<int64_t>(64, 2 * div_up(tokens, groups)) : tokens;
+  const int64_t each = ragged ? 64 : tokens;
   s.width = each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : 128;
   s.raw_stages = 0;
   const int kstages = static_cast<int>(div_up(n, kStageK));

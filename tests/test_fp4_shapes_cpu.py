@@ -116,3 +116,11 @@ def test_exchanged_sums_stay_in_their_region(shape, raw):
             else:
                 rows = range(count)
             assert (max(rows) + 1) * 512 <= region, (s, count)
+
+
+def test_groups_take_tiles_of_64(shape):
+    """Up to 32 tokens a group on average, which is as many as come here."""
+    for groups in (1, 2, 8, 60, 512):
+        for tokens in (1, groups, 16 * groups, 32 * groups):
+            for rows, n in ((64, 64), (2048, 4096), (20000, 1000)):
+                assert shape(0, tokens, groups, 1, rows, n)["width"] == 64
