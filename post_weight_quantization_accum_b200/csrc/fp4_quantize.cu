@@ -139,7 +139,7 @@ __device__ __noinline__ uint32_t chunk_max(const QuantArgs& a, const int* src, i
   });
 }
 
-template <bool BF16, bool NV>
+template <bool BF16>
 __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(const __grid_constant__ QuantArgs a) {
   __shared__ int tab[3][kFp4MaxGroups + 1];
   __shared__ uint32_t red[32];
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(const __grid_constan
   if (!find_band(a, t, band, b)) return;
   const int chunks = (a.n + kChunk - 1) / kChunk;
   // this part's columns, a chunk after the other, each down the band's rows
-  using S = Shape<BF16, NV>;
+  using S = Shape<BF16, true>;
   band_rows(a, b.r0, b.rows, src);
   const int c0 = static_cast<int>(int64_t(chunks) * part / a.splits), c1 = static_cast<int>(int64_t(chunks) * (part + 1) / a.splits);
   const char* X = static_cast<const char*>(a.X);
@@ -412,8 +412,9 @@ gptq_status launch_quantize(QuantArgs& a, int64_t bands, const DeviceInfo* info,
   // few bands: a CTA takes 32 rows of one, so that more SMs have work (a layer
   // on 128 tokens, nvfp4, 4096 -> 11008: 21.2 us with whole bands, 17.2 with 32)
   a.strips = bands * chunks <= info->sm_count && a.rows > 32 ? 4 : 1;
-  if (a.partial != nullptr) {
-    if (launch_pdl(fp4_amax_kernel<BF16, NV>, static_cast<unsigned>(bands * a.splits), kThreads, 0, st, a) != cudaSuccess)
+  if constexpr (NV) {
+    if (a.partial != nullptr &&
+        launch_pdl(fp4_amax_kernel<BF16>, static_cast<unsigned>(bands * a.splits), kThreads, 0, st, a) != cudaSuccess)
       return GPTQ_ERR_CUDA;
   }
   if (launch_pdl(fp4_quantize_kernel<BF16, NV>, static_cast<unsigned>(bands * a.strips * chunks), kThreads, 0, st, a) != cudaSuccess)
