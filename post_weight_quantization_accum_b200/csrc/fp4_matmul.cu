@@ -700,9 +700,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 //
 // Bound by shared memory and the tensor cores: a stage of 256 columns brings
 // 38 KB to each CTA, which the products and scale copies read again, 76 KB at
-// 128 bytes a cycle = 608 cycles, while its four products of 256 x 256 x 64
-// take 4 x 131 and its twelve scale copies 10 each.  Measured 610 to 625
-// cycles a stage.  A tile of one CTA (128 x 256) would move 108 KB.  The
+// 128 bytes a cycle = 608 cycles; measured 610 to 625 cycles a stage.  Its four
+// products of 256 x 256 x 64 keep the tensor pipe for 4 x 131 of them (counted:
+// about 520); alone, its twelve scale copies take 10 each, so they overlap products
+// or each other, as 644 in line would be more than measured.  A tile of one CTA (128 x 256) would move 108 KB.  The
 // accumulators of two tiles overlap, as two of 256 columns and the scales do
 // not fit: the next tile's products wait until the epilogue has read the
 // overlap, about 850 cycles.  8192 tokens, 11008 x 4096, nvfp4, bf16 out: 148 us
@@ -966,8 +967,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
       // ---------------- MMA issuer (even CTA) ----------------
-      // Per stage twelve scale copies (nvfp4) and four products, in line: a
-      // copy costs 10 cycles of the tensor pipe, a product 130.  Whole stages
+      // Per stage twelve scale copies (nvfp4) and four products.  Whole stages
       // take a path without conditions, as those are what issuing costs.
       uint32_t stage = 0, phase = 0, tiles = 0;
       uint32_t set = 0;                    // scale columns, in turn
@@ -1161,8 +1161,10 @@ gptq_status launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const 
 // The stream kernel pays for tokens (sums to exchange), the pair kernel, which
 // does not cut K, for its depth.  Above 128 tokens it is the pair kernel, up to
 // 64 the other, and between them the sums below, which are fitted to these
-// times.  Groups: 32 of 2048 x 4096 take 32.7 and 34.2 us at 32 tokens each,
-// 38.9 and 36.4 at 96; 8 of 2048 x 2048 8.5 and 8.6 at 8, 10.2 and 8.4 at 32.
+// times.  Groups: up to 32 tokens each, whatever rows, n and their number are.
+// 32 of 2048 x 4096 take 32.7 and 34.2 us at 32 tokens each, 38.9 and 36.4 at
+// 96; 8 of 2048 x 2048 8.5 and 8.6 at 8, 10.2 and 8.4 at 32, where the rule
+// takes the slower one: it fits many groups, which read much of W, not few.
 bool many_tokens(int64_t tokens, int groups, bool ragged, int64_t rows, int n, int sms) {
   if (ragged) return tokens > 32 * static_cast<int64_t>(groups);
   if (tokens <= 64 || tokens > kFp4Band) return tokens > kFp4Band;
@@ -1288,7 +1290,7 @@ gptq_status fp4_matmul(bool nv, const uint8_t* wq, const uint8_t* wscales, const
   // with groups, whose tiles end early, a lane a feature is faster.  (nvfp4 8192
   // x 4096 -> 11008: 150 us by TMA, 156 without; mxfp4 1555 x 2000 -> 4096 13.5
   // and 14.0, -> 1112 9.0 and 8.3; 32 groups of 125 and 250 tokens x 2000 ->
-  // 2048 25.5 and 24.0, 34.2 and 32.2.)
+  // 2048 25.5 and 24.0, 34.2 and 32.2; groups of thousands were not timed.)
   const bool y_tma = y_bf16 && reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy % 8 == 0 && offsets == nullptr &&
                      ceil_div(tokens, kTokens) * ceil_div(rows, kPairRows) * 2 > info->sm_count;
   if (y_tma && !make_tensor_map_2d(&ymap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, rows, tokens, ldy * 2, 32, 32,

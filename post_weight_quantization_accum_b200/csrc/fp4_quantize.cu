@@ -23,9 +23,12 @@
 // runs backwards, still finds in L2; a small X is read twice by the one
 // kernel.  Measured with the values (B200): mxfp4 of fp32 11008 x 4096 63 us =
 // 6.1 TB/s, 0.93 of the copy rate; nvfp4 of bf16 8192 x 4096 49 us = 4.5 TB/s
-// on the bytes of one pass: 15 us of it the maxima, and the second pass
-// issues 200 instructions for a warp's 512 values (counted without writing
-// values), which bound it.
+// on the bytes of one pass, 15 us of it the maxima (without the values 36 us,
+// and 22 with a given tensor scale).  The second pass issues 305 instructions
+// for a warp's 512 values, 256 without writing them: 55% and 71% of the cycles
+// in which an SM has work.  Besides, with the values it waits for X, without
+// them for the arithmetic pipes, and its 1024 CTAs on 592 places (1.7 waves)
+// leave the SMs without work for 15 to 18% of the time.
 #include <algorithm>
 
 #include "fp4_quant.cuh"
@@ -41,8 +44,8 @@ template <bool BF16, bool NV>
 struct Shape : Fp4Lane<BF16, NV> {
   static constexpr int kAcross = kChunk / Fp4Lane<BF16, NV>::kLane;  // lanes across the tile
   static constexpr int kRowsAtOnce = kThreads / kAcross;
-  // rows loaded ahead of the one in work (nvfp4 is bound by issuing: more
-  // registers would cost it warps; 8192 x 4096 of bf16: 39 us with 1, 46 with 2)
+  // rows loaded ahead of the one in work (8192 x 4096 of bf16 to nvfp4, second
+  // pass: 39 us with 1, 46 with 2, which needs more registers)
   static constexpr int kAhead = NV ? 1 : 2;
 };
 
@@ -400,7 +403,10 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const __grid_
 }
 
 // Parts of a band's columns in the pass that takes the maxima: a chunk each, or
-// more where that would leave over 2048 maxima for every CTA to read.
+// several, down to one part a band, where that would leave over 2048 maxima.
+// Every CTA of the second pass reads all of its group's: 8 KB up to 2048 bands
+// (262,144 rows), 4 bytes a band above (10^6 x 4096: 32 KB in each of 131,072
+// CTAs, half as much as bf16 values of X, though out of L2).
 int amax_splits(int64_t bands, int n) {
   const int64_t chunks = ceil_div(n, kChunk);
   return static_cast<int>(ceil_div(chunks, std::max<int64_t>(1, ceil_div(bands * chunks, 2048))));
