@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const __grid_
 // Parts of a band's columns in the pass that takes the maxima: a chunk each, or
 // several, down to one part a band, where that would leave over 2048 maxima.
 // Every CTA of the second pass reads all of its group's: 8 KB up to 2048 bands
-// (262,144 rows), 4 bytes a band above (10^6 x 4096: 32 KB in each of 131,072
+// (262,144 rows), 4 bytes a band above (2^20 x 4096: 32 KB in each of 131,072
 // CTAs, half as much as bf16 values of X, though out of L2).
 int amax_splits(int64_t bands, int n) {
   const int64_t chunks = ceil_div(n, kChunk);
